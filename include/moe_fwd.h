@@ -418,6 +418,64 @@ int moe_ep_grouped_swiglu(const moe_shape *shape, int rows, const void *a, const
                           const float *w2_scales, int world, uint16_t *const *ret_y,
                           const int *ret_capacity, void *ws, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Block-scaled linear layer: the projections next to the FFN layer, on the
+ * same blockwise FP8 ("DeepSeek-R1" (aguasto.com), "Quantization"; "DeepSeek
+ * v3 and R1 Model Architecture", "First ever FP8 Precision...").
+ *   out[t, n] = sum_kb s_a[t, kb] * s_w[n / 128, kb] *
+ *                      (sum over the 128 columns of K block kb of a * w)
+ *               (+ residual[t, n])
+ * with a the codes of x in 1x128 tiles and w those of 128x128 blocks.  Sums are binary32; the residual is added before
+ * the one rounding of a bf16 output.
+ * Shapes: K a multiple of 128; any N >= 1 (row-major weights: the last block
+ * row may be short, as fp8_block_quant writes it) or a multiple of 128 (tiled
+ * weights); K and N at most 2^20; T >= 0 (T = 0 enqueues nothing); precision
+ * MOE_FP8_BLOCK or MOE_FP8_UE8M0. */
+typedef struct {
+    int T;             /* tokens */
+    int K;             /* input features */
+    int N;             /* output features */
+    int precision;     /* MOE_FP8_BLOCK or MOE_FP8_UE8M0 */
+    int weight_layout; /* enum moe_layout of w */
+    int out_f32;       /* 0: out is bf16; 1: binary32 */
+} moe_linear_shape;
+
+/* Bytes of workspace the three calls below need (0 on an invalid shape): the
+ * status word first (moe_check_status), then tile counters, which every call
+ * leaves zero, the quantised x and partial sums.  Zero-fill it once before
+ * first use; one workspace then serves linear calls of any shapes that it is
+ * large enough for, one after the other on a stream (calls that overlap need
+ * one each). */
+size_t moe_linear_workspace_size(const moe_linear_shape *shape);
+
+/* out = a W^T (+ residual) of codes that are quantised already.
+ *   a        [T, K] e4m3; a_scales fp32 [T, K/128]
+ *   w        [N, K] e4m3 in the shape's weight_layout
+ *   w_scales fp32 [ceil(N/128), K/128]
+ *   residual bf16 [T, N] or NULL
+ *   out      [T, N] bf16 or fp32 (out_f32); may be the residual's memory when
+ *            both are bf16 */
+int fp8_block_gemm(const moe_linear_shape *shape, const uint8_t *a, const float *a_scales,
+                   const void *w, const float *w_scales, const uint16_t *residual, void *out,
+                   void *ws, size_t ws_bytes, void *stream);
+
+/* The same of a bf16 x [T, K], quantised on the way in 1x128 tiles: scale
+ * amax * (1/448), codes e4m3_rn_satfinite(v * (448 * (1/amax))), every
+ * operation rounded to binary32 (power-of-two scales, as by
+ * fp8_block_quant_ue8m0, in MOE_FP8_UE8M0).  The scale and the factor are
+ * within an ulp of fp8_block_quant's quotients, so an element at the border of
+ * two codes may take the other one here. */
+int moe_linear(const moe_linear_shape *shape, const uint16_t *x, const void *w,
+               const float *w_scales, const uint16_t *residual, void *out, void *ws,
+               size_t ws_bytes, void *stream);
+
+/* The same behind the block's pre-norm: x = bf16((h * rstd) * gamma), rstd as
+ * in moe_forward_prenorm.
+ *   h bf16 [T, K]; gamma bf16 [K]; eps >= 0 */
+int moe_linear_prenorm(const moe_linear_shape *shape, const uint16_t *h, const uint16_t *gamma,
+                       float eps, const void *w, const float *w_scales, void *out, void *ws,
+                       size_t ws_bytes, void *stream);
+
 /* Synchronises `stream`, returns the workspace status word (MOE_OK or the
  * first device-recorded MOE_ERR_*), and resets it to MOE_OK.  A workspace must
  * be zero-filled once before first use (or passed here once) so its status

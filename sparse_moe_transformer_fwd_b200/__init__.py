@@ -22,7 +22,9 @@ from ._native import (EXPORTS, MOE_BF16, MOE_FP8_BLOCK, MOE_FP8_UE8M0, MOE_LAYOU
                       make_dense_shape, moe_dense_workspace_size, alloc_dense_workspace,
                       moe_dense_ffn, moe_dense_ffn_prenorm, moe_workspace_layout,
                       moe_quant_scatter, moe_ep_dispatch, moe_ep_workspace_size,
-                      moe_ep_grouped_swiglu, MOE_EP_MAX_RANKS)
+                      moe_ep_grouped_swiglu, MOE_EP_MAX_RANKS, MoeLinearShape, make_linear_shape,
+                      moe_linear_workspace_size, alloc_linear_workspace, fp8_block_gemm, moe_linear,
+                      moe_linear_prenorm)
 
 __all__ = [
     "MoELayer", "MoeError", "MoeShape", "make_shape", "alloc_workspace", "lib", "EXPORTS",
@@ -34,7 +36,9 @@ __all__ = [
     "DenseFFN", "MoeDenseShape", "make_dense_shape", "moe_dense_workspace_size",
     "alloc_dense_workspace", "moe_dense_ffn", "moe_dense_ffn_prenorm", "moe_workspace_layout",
     "moe_quant_scatter", "moe_ep_dispatch", "moe_ep_workspace_size", "moe_ep_grouped_swiglu",
-    "MOE_EP_MAX_RANKS",
+    "MOE_EP_MAX_RANKS", "Fp8Linear", "MoeLinearShape", "make_linear_shape",
+    "moe_linear_workspace_size", "alloc_linear_workspace", "fp8_block_gemm", "moe_linear",
+    "moe_linear_prenorm",
 ]
 
 
@@ -188,6 +192,83 @@ class DenseFFN:
             out = torch.empty(T, self.d, dtype=torch.bfloat16, device=h.device)
         moe_dense_ffn_prenorm(self.shape(T), h, gamma, eps, self.w13, self.w13s, self.w2,
                               self.w2s, out, self.workspace(T), stream=stream)
+        return out
+
+    def check_status(self, T: int) -> int:
+        return moe_check_status(self.workspace(T))
+
+
+class Fp8Linear:
+    """One projection with resident block-scaled e4m3 weights: out = x W^T.
+
+    w bf16 [N, K], K a multiple of 128, quantised once at construction in
+    128x128 blocks; precision "fp8" (fp32 block scales) or "fp8_ue8m0"
+    (power-of-two block scales).  weight_layout "tiled" (default where N is a
+    multiple of 128) or "rowmajor" (any N).  x bf16 [T, K] is quantised 1x128
+    on the way; out is bf16, or fp32 with out_dtype=torch.float32."""
+
+    def __init__(self, w, *, precision: str = "fp8", weight_layout: str | None = None,
+                 out_dtype: torch.dtype = torch.bfloat16):
+        lib()
+        if precision not in ("fp8", "fp8_ue8m0"):
+            raise ValueError(precision)
+        if weight_layout is None:
+            weight_layout = "tiled" if w.shape[0] % 128 == 0 else "rowmajor"
+        if weight_layout not in ("tiled", "rowmajor"):
+            raise ValueError(weight_layout)
+        self.N, self.K = w.shape
+        self.precision, self.weight_layout, self.out_dtype = precision, weight_layout, out_dtype
+        self.shape(1)  # refuses what the library would
+        self.w = torch.empty(self.N, self.K, dtype=torch.uint8, device=w.device)
+        self.w_scales = torch.empty(-(-self.N // 128), self.K // 128, dtype=torch.float32,
+                                    device=w.device)
+        with torch.cuda.device(w.device):
+            fp8_block_quant(w.contiguous(), 128, self.w, self.w_scales,
+                            layout=MOE_LAYOUT_TILED if weight_layout == "tiled" else MOE_LAYOUT_ROWMAJOR,
+                            ue8m0=precision == "fp8_ue8m0")
+        self._ws = {}
+
+    def shape(self, T: int) -> MoeLinearShape:
+        s = make_linear_shape(T, self.K, self.N, self.precision, self.weight_layout, self.out_dtype)
+        moe_linear_workspace_size(s)
+        return s
+
+    def workspace(self, T: int) -> torch.Tensor:
+        ws = self._ws.get(T)
+        if ws is None:
+            ws = alloc_linear_workspace(self.shape(T), self.w.device)
+            self._ws[T] = ws
+        return ws
+
+    def _out(self, T, out):
+        return torch.empty(T, self.N, dtype=self.out_dtype, device=self.w.device) if out is None else out
+
+    def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None,
+                 residual: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """x W^T, plus the residual before the one rounding of a bf16 output."""
+        T = x.shape[0]
+        out = self._out(T, out)
+        moe_linear(self.shape(T), x, self.w, self.w_scales, out, self.workspace(T),
+                   residual=residual, stream=stream)
+        return out
+
+    def quantized(self, a: torch.Tensor, a_scales: torch.Tensor, out: torch.Tensor | None = None,
+                  residual: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """The product of codes that are quantised already (fp8_block_quant,
+        block_rows 1): several projections of one x quantise it once."""
+        T = a.shape[0]
+        out = self._out(T, out)
+        fp8_block_gemm(self.shape(T), a, a_scales, self.w, self.w_scales, out, self.workspace(T),
+                       residual=residual, stream=stream)
+        return out
+
+    def forward_prenorm(self, h: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6,
+                        out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """bf16(RMSNorm(h) * gamma) W^T (pre-norm fused)."""
+        T = h.shape[0]
+        out = self._out(T, out)
+        moe_linear_prenorm(self.shape(T), h, gamma, eps, self.w, self.w_scales, out,
+                           self.workspace(T), stream=stream)
         return out
 
     def check_status(self, T: int) -> int:

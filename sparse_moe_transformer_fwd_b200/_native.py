@@ -32,7 +32,8 @@ EXPORTS = ("moe_workspace_size", "moe_route", "moe_permute", "fp8_block_quant",
            "moe_route_noalloc", "moe_pack_tiles", "moe_forward_prenorm", "moe_last_launch_name",
            "fp8_block_quant_ue8m0", "moe_dense_workspace_size", "moe_dense_ffn",
            "moe_dense_ffn_prenorm", "moe_workspace_layout", "moe_quant_scatter",
-           "moe_ep_dispatch", "moe_ep_workspace_size", "moe_ep_grouped_swiglu")
+           "moe_ep_dispatch", "moe_ep_workspace_size", "moe_ep_grouped_swiglu",
+           "moe_linear_workspace_size", "fp8_block_gemm", "moe_linear", "moe_linear_prenorm")
 
 MOE_EP_MAX_RANKS = 64
 
@@ -50,6 +51,12 @@ class MoeShape(ctypes.Structure):
 class MoeDenseShape(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int), ("d_model", ctypes.c_int), ("d_ff", ctypes.c_int),
                 ("precision", ctypes.c_int), ("weight_layout", ctypes.c_int)]
+
+
+class MoeLinearShape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("K", ctypes.c_int), ("N", ctypes.c_int),
+                ("precision", ctypes.c_int), ("weight_layout", ctypes.c_int),
+                ("out_f32", ctypes.c_int)]
 
 
 class MoeEpBlock(ctypes.Structure):
@@ -109,6 +116,12 @@ def lib() -> ctypes.CDLL:
         L.moe_dense_workspace_size.restype = sz
         L.moe_dense_ffn.argtypes = [dp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.moe_dense_ffn_prenorm.argtypes = [dp, vp, vp, cf, vp, vp, vp, vp, vp, vp, sz, vp]
+        lp = ctypes.POINTER(MoeLinearShape)
+        L.moe_linear_workspace_size.argtypes = [lp]
+        L.moe_linear_workspace_size.restype = sz
+        L.fp8_block_gemm.argtypes = [lp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_linear.argtypes = [lp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_linear_prenorm.argtypes = [lp, vp, vp, cf, vp, vp, vp, vp, sz, vp]
         L.moe_check_status.argtypes = [vp, vp]
         L.moe_last_error.argtypes = []
         L.moe_last_error.restype = ctypes.c_char_p
@@ -121,7 +134,8 @@ def lib() -> ctypes.CDLL:
                      "moe_combine", "moe_forward", "moe_check_status", "moe_last_launch_count",
                      "moe_set_kernel_events", "moe_pack_tiles", "moe_forward_prenorm",
                      "moe_dense_ffn", "moe_dense_ffn_prenorm", "moe_workspace_layout",
-                     "moe_quant_scatter", "moe_ep_dispatch", "moe_ep_grouped_swiglu"):
+                     "moe_quant_scatter", "moe_ep_dispatch", "moe_ep_grouped_swiglu",
+                     "fp8_block_gemm", "moe_linear", "moe_linear_prenorm"):
             getattr(L, name).restype = ci
         _LIB = L
     return _LIB
@@ -381,6 +395,87 @@ def moe_ep_grouped_swiglu(shape, a, a_scales, seg_start, seg_rows, seg_slot, seg
         _ptr(w13_scales, torch.float32, "w13_scales"), _ptr(w2, wt, "w2"),
         _ptr(w2_scales, torch.float32, "w2_scales"), world, _ptr_array(ret_y, _BF16, "ret_y"),
         cap, _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+
+
+def make_linear_shape(T, K, N, precision="fp8", weight_layout=MOE_LAYOUT_TILED,
+                      out_dtype=torch.bfloat16) -> MoeLinearShape:
+    """Shape of a block-scaled linear; out_dtype torch.bfloat16 or torch.float32."""
+    prec = {"fp8": MOE_FP8_BLOCK, "fp8_ue8m0": MOE_FP8_UE8M0}[precision] \
+        if isinstance(precision, str) else int(precision)
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"out_dtype {out_dtype}: bfloat16 or float32 expected")
+    return MoeLinearShape(int(T), int(K), int(N), prec, _layout(weight_layout),
+                          int(out_dtype == torch.float32))
+
+
+def moe_linear_workspace_size(shape: MoeLinearShape) -> int:
+    n = lib().moe_linear_workspace_size(ctypes.byref(shape))
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, lib().moe_last_error().decode())
+    return n
+
+
+def alloc_linear_workspace(shape: MoeLinearShape, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace of moe_linear_workspace_size bytes."""
+    return torch.zeros(moe_linear_workspace_size(shape), dtype=torch.uint8, device=device)
+
+
+def _sized(t, numel, name):
+    """t, checked to hold at least as many elements as the call reads or writes."""
+    if isinstance(t, torch.Tensor) and t.numel() < numel:
+        raise ValueError(f"{name}: {t.numel()} elements, the shape needs {numel}")
+    return t
+
+
+def _device_of(**tensors):
+    """The one device the call's tensors are on."""
+    dev = None
+    for name, t in tensors.items():
+        if isinstance(t, torch.Tensor):
+            dev = t.device if dev is None else dev
+            if t.device != dev:
+                raise ValueError(f"{name}: on {t.device}, other tensors on {dev}")
+    return dev
+
+
+def _linear_call(fn, shape, first, w, w_scales, residual, out, ws, stream, **more):
+    """Checks sizes and devices and calls fn(shape, *first, w, w_scales[, residual], out, ws ...) on the
+    tensors' device; `first` holds the leading arguments, `more` their tensors by name."""
+    T, K, N = shape.T, shape.K, shape.N
+    dev = _device_of(**more, w=w, w_scales=w_scales, residual=residual, out=out, ws=ws)
+    args = [_ptr(_sized(w, N * K, "w"), _FP8, "w"),
+            _ptr(_sized(w_scales, -(-N // 128) * (K // 128), "w_scales"), torch.float32, "w_scales")]
+    if fn is not lib().moe_linear_prenorm:
+        args.append(_ptr(_sized(residual, T * N, "residual"), _BF16, "residual"))
+    args.append(_ptr(_sized(out, T * N, "out"), torch.float32 if shape.out_f32 else _BF16, "out"))
+    if dev is None or dev.type != "cuda":
+        raise ValueError("w: must be a CUDA tensor")
+    with torch.cuda.device(dev):
+        _check(fn(ctypes.byref(shape), *first, *args, _ptr(ws, torch.uint8, "ws"), ws.numel(),
+                  _stream(stream)))
+
+
+def fp8_block_gemm(shape, a, a_scales, w, w_scales, out, ws, residual=None, stream=None):
+    """out = a W^T (+ residual) of e4m3 codes in 1x128 tiles (a) and 128x128 blocks (w)."""
+    T, K = shape.T, shape.K
+    _linear_call(lib().fp8_block_gemm, shape,
+                 [_ptr(_sized(a, T * K, "a"), _FP8, "a"),
+                  _ptr(_sized(a_scales, T * (K // 128), "a_scales"), torch.float32, "a_scales")],
+                 w, w_scales, residual, out, ws, stream, a=a, a_scales=a_scales)
+
+
+def moe_linear(shape, x, w, w_scales, out, ws, residual=None, stream=None):
+    """out = x W^T (+ residual) of a bf16 x, quantised 1x128 on the way."""
+    _linear_call(lib().moe_linear, shape, [_ptr(_sized(x, shape.T * shape.K, "x"), _BF16, "x")],
+                 w, w_scales, residual, out, ws, stream, x=x)
+
+
+def moe_linear_prenorm(shape, h, gamma, eps, w, w_scales, out, ws, stream=None):
+    """out = bf16(RMSNorm(h) * gamma) W^T."""
+    _linear_call(lib().moe_linear_prenorm, shape,
+                 [_ptr(_sized(h, shape.T * shape.K, "h"), _BF16, "h"),
+                  _ptr(_sized(gamma, shape.K, "gamma"), _BF16, "gamma"), float(eps)],
+                 w, w_scales, None, out, ws, stream, h=h, gamma=gamma)
 
 
 def moe_check_status(ws, stream=None) -> int:

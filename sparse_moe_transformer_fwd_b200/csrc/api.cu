@@ -826,6 +826,7 @@ int dense_impl(const moe_dense_shape *s, const uint16_t *x, const uint16_t *gamm
     // one segment of T rows: 64-row tiles only where they save round trips
     g.tile_m = (s->precision == MOE_FP8_BLOCK && T <= 64) ? 64 : 128;
     g.gate_up = true;
+    g.early_b = n > 0;  // a bf16 layer without pre-norm begins with this GEMM
     g.a = a;
     g.a_scales = fp8 ? at<float>(ws, L.a_scales) : nullptr;
     g.b = w13;
@@ -836,6 +837,7 @@ int dense_impl(const moe_dense_shape *s, const uint16_t *x, const uint16_t *gamm
     g.N_out = s->d_ff;
     LAUNCH(launch_grouped_gemm(g, st, &n), "dense gate/up GEMM");
     g.gate_up = false;
+    g.early_b = true;
     g.a = at<uint8_t>(ws, L.h);
     g.a_scales = fp8 ? at<float>(ws, L.h_scales) : nullptr;
     g.b = w2;
@@ -997,6 +999,225 @@ int moe_ep_grouped_swiglu(const moe_shape *s, int rows, const void *a, const flo
     mark_launch(st, n);
     g_launches = n;
     return MOE_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------- block-scaled linear ---
+namespace moe {
+namespace {
+
+// Tile counters of linear_stream sit in a region of fixed size, so that one
+// zero-filled workspace serves linears of any shapes: each launch leaves the
+// counters zero, and no other region of another shape reaches them.
+constexpr int kLinearMaxN = 1 << 20;
+constexpr size_t kLinearCounterBytes = kLinearMaxN / 128 * sizeof(int);
+constexpr int kLinearSplitRows = 256;  // as the dense down GEMM: K split up to here
+
+int check_linear_shape(const moe_linear_shape *s) {
+    if (!s) return fail(MOE_ERR_INVALID_ARG, "shape is NULL");
+    if (s->T < 0) return fail(MOE_ERR_INVALID_ARG, "T < 0");
+    if (s->K <= 0 || s->K % 128 || s->K > kLinearMaxN)
+        return fail(MOE_ERR_INVALID_ARG, "K must be a positive multiple of 128, at most %d", kLinearMaxN);
+    if (s->N <= 0 || s->N > kLinearMaxN) return fail(MOE_ERR_INVALID_ARG, "N must be in 1..%d", kLinearMaxN);
+    if (s->precision != MOE_FP8_BLOCK && s->precision != MOE_FP8_UE8M0)
+        return fail(MOE_ERR_INVALID_ARG, "precision must be MOE_FP8_BLOCK or MOE_FP8_UE8M0");
+    if (s->weight_layout != MOE_LAYOUT_ROWMAJOR && s->weight_layout != MOE_LAYOUT_TILED)
+        return fail(MOE_ERR_INVALID_ARG, "unknown weight_layout %d", s->weight_layout);
+    if (s->weight_layout == MOE_LAYOUT_TILED && s->N % 128)
+        return fail(MOE_ERR_INVALID_ARG, "tiled weights need N %% 128 == 0");
+    if (s->out_f32 != 0 && s->out_f32 != 1) return fail(MOE_ERR_INVALID_ARG, "out_f32 must be 0 or 1");
+    // tensor-map coordinates are 32-bit, and the padded partial sums of a batch stay addressable
+    if (static_cast<long long>(s->N + 255) / 256 * 2 * s->K >= (1LL << 31))
+        return fail(MOE_ERR_INVALID_ARG, "N * K too large");
+    if (static_cast<long long>(s->T) * std::max(s->K, s->N) > (1LL << 36) || s->T > (1 << 30))
+        return fail(MOE_ERR_INVALID_ARG, "T too large");
+    return MOE_OK;
+}
+
+int linear_padded_n(const moe_linear_shape *s) { return (s->N + 255) / 256 * 256; }
+
+// Sums in binary32 and a finishing kernel where the tiled GEMM cannot store
+// the output itself (256 bf16 columns a tile).
+bool linear_direct(const moe_linear_shape *s) { return s->N % 256 == 0 && !s->out_f32; }
+
+// K ranges of the tiled GEMM, by the dense down GEMM's rule: few output tiles
+// leave SMs idle, so up to kMaxSplitK ranges of at least two K blocks.
+int linear_ksplit(const moe_linear_shape *s) {
+    if (s->T > kLinearSplitRows) return 1;
+    const int tiles = gemm_output_tiles(s->T, linear_padded_n(s));
+    int ks = std::min(num_sms() / std::max(tiles, 1), kMaxSplitK);
+    ks = std::min(ks, s->K / 256);
+    return std::max(ks, 1);
+}
+
+struct LinearLayout {
+    size_t status, counters, rstd, a, a_scales, partial, total;
+};
+
+LinearLayout linear_layout(const moe_linear_shape *s) {
+    const size_t T = s->T, K = s->K;
+    LinearLayout L{};
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += (bytes + 255) & ~static_cast<size_t>(255);
+        return at;
+    };
+    L.status = take(256);
+    L.counters = take(kLinearCounterBytes);
+    L.rstd = take(T * 4);
+    L.a = take(T * K);
+    L.a_scales = take(T * (K / 128) * 4);
+    if (s->T <= kLinearStreamRows)
+        L.partial = take(linear_partial_floats(s->T) * 4);
+    else if (s->T <= kLinearSplitRows)
+        L.partial = take(kMaxSplitK * T * linear_padded_n(s) * 4);
+    else
+        L.partial = take(linear_direct(s) ? 0 : T * linear_padded_n(s) * 4);
+    L.total = off;
+    return L;
+}
+
+// out = a W^T (+ residual) of codes and scales: the weight-streaming kernel for
+// few tokens, the tiled GEMM (one segment, one slot) for more.  *n counts the
+// launches before and after; the first one of a call may not read W ahead.
+int linear_product(const moe_linear_shape *s, const void *a, const float *a_scales, const void *w,
+                   const float *w_scales, const uint16_t *residual, void *out, void *ws,
+                   const LinearLayout &L, cudaStream_t st, int *n) {
+    float *partial = at<float>(ws, L.partial);
+    if (s->T <= kLinearStreamRows) {
+        LinearStreamArgs g{};
+        g.a = a;
+        g.a_scales = a_scales;
+        g.w = w;
+        g.w_scales = w_scales;
+        g.residual = residual;
+        g.out = out;
+        g.partial = partial;
+        g.counters = at<int>(ws, L.counters);
+        g.status = at<int>(ws, L.status);
+        g.T = s->T;
+        g.K = s->K;
+        g.N = s->N;
+        g.out_f32 = s->out_f32;
+        g.w_rowmajor = s->weight_layout == MOE_LAYOUT_ROWMAJOR;
+        LAUNCH(launch_linear_stream(g, st, n), "linear");
+        return MOE_OK;
+    }
+    const int ks = linear_ksplit(s);
+    const bool sums = ks > 1 || !linear_direct(s);
+    GemmArgs g{};
+    g.fp8 = true;
+    g.gate_up = false;
+    g.a = a;
+    g.a_scales = a_scales;
+    g.b = w;
+    g.b_rowmajor = s->weight_layout == MOE_LAYOUT_ROWMAJOR;
+    g.b_scales = w_scales;
+    g.out = out;
+    g.rows_total = s->T;
+    g.K = s->K;
+    g.N_out = linear_padded_n(s);
+    g.n_slots = 1;
+    g.n_segments = 1;
+    g.status = at<int>(ws, L.status);
+    // the block-scaled MMA keeps all of K in one accumulator: no binary32
+    // sums per range, so those take the promotion path (a power-of-two scale
+    // is a binary32 scale)
+    g.ue8m0 = s->precision == MOE_FP8_UE8M0 && !sums;
+    g.tile_m = kTileM;
+    g.early_b = *n > 0;
+    g.ksplit = ks;
+    g.partial = sums ? partial : nullptr;
+    g.b_rows_valid = g.N_out != s->N ? s->N : 0;
+    g.residual = sums ? nullptr : residual;
+    LAUNCH(launch_grouped_gemm(g, st, n), "linear GEMM");
+    if (sums)
+        LAUNCH(launch_linear_finish(partial, ks, s->T, s->N, g.N_out, residual, out, s->out_f32, st, n),
+               "linear finish");
+    return MOE_OK;
+}
+
+// codes != NULL: the product of given codes; else x is quantised (after the
+// pre-norm, with gamma set) into the workspace first.
+int linear_impl(const char *name, const moe_linear_shape *s, const uint16_t *x, const uint16_t *gamma,
+                float eps, const uint8_t *codes, const float *code_scales, const void *w,
+                const float *w_scales, const uint16_t *residual, void *out, void *ws, size_t ws_bytes,
+                void *stream) {
+    const CallRange nvtx_range(name);
+    RETURN_IF(check_linear_shape(s));
+    const LinearLayout L = linear_layout(s);
+    if (!ws) return fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
+    if (reinterpret_cast<uintptr_t>(ws) & 255)
+        return fail(MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    if (ws_bytes < L.total)
+        return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, L.total);
+    if (s->T == 0) return g_launches = 0, MOE_OK;
+    if (!codes) CHECK_PTR(x);
+    if (codes && !aligned16(codes)) return fail(MOE_ERR_INVALID_ARG, "a is not 16-byte aligned");
+    if (codes) CHECK_PTR(code_scales);
+    CHECK_PTR(w);
+    CHECK_PTR(w_scales);
+    CHECK_PTR(out);
+    if (residual && !aligned16(residual)) return fail(MOE_ERR_INVALID_ARG, "residual is not 16-byte aligned");
+    if (gamma && !(eps >= 0.0f)) return fail(MOE_ERR_INVALID_ARG, "eps must be >= 0");
+    RETURN_IF(check_device());
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int n = 0;
+    if (!codes) {
+        PreNorm pn{};
+        if (gamma) {
+            float *rstd = at<float>(ws, L.rstd);
+            LAUNCH(launch_rstd(x, s->T, s->K, eps, rstd, st, &n), "pre-norm statistics");
+            pn.rstd = rstd;
+            pn.gamma = gamma;
+        }
+        LAUNCH(launch_linear_quant(x, s->T, s->K, pn, s->precision == MOE_FP8_UE8M0, at<uint8_t>(ws, L.a),
+                                   at<float>(ws, L.a_scales), st, &n),
+               "quantise x");
+        codes = at<uint8_t>(ws, L.a);
+        code_scales = at<float>(ws, L.a_scales);
+    }
+    RETURN_IF(linear_product(s, codes, code_scales, w, w_scales, residual, out, ws, L, st, &n));
+    mark_launch(st, n);
+    g_launches = n;
+    return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" {
+
+size_t moe_linear_workspace_size(const moe_linear_shape *s) {
+    if (check_linear_shape(s) != MOE_OK) return 0;
+    return linear_layout(s).total;
+}
+
+int fp8_block_gemm(const moe_linear_shape *s, const uint8_t *a, const float *a_scales, const void *w,
+                   const float *w_scales, const uint16_t *residual, void *out, void *ws,
+                   size_t ws_bytes, void *stream) {
+    if (!a && s && s->T > 0) return fail(MOE_ERR_INVALID_ARG, "a is NULL");
+    // T = 0 takes any pointer; a non-NULL stand-in keeps it on this path
+    static const uint8_t none = 0;
+    return linear_impl("fp8_block_gemm", s, nullptr, nullptr, 0.0f, a ? a : &none, a_scales, w, w_scales, residual,
+                       out, ws, ws_bytes, stream);
+}
+
+int moe_linear(const moe_linear_shape *s, const uint16_t *x, const void *w, const float *w_scales,
+               const uint16_t *residual, void *out, void *ws, size_t ws_bytes, void *stream) {
+    return linear_impl("moe_linear", s, x, nullptr, 0.0f, nullptr, nullptr, w, w_scales, residual, out, ws,
+                       ws_bytes, stream);
+}
+
+int moe_linear_prenorm(const moe_linear_shape *s, const uint16_t *h, const uint16_t *gamma, float eps,
+                       const void *w, const float *w_scales, void *out, void *ws, size_t ws_bytes,
+                       void *stream) {
+    if (!gamma) return fail(MOE_ERR_INVALID_ARG, "gamma is NULL");
+    if (!aligned16(gamma)) return fail(MOE_ERR_INVALID_ARG, "gamma is not 16-byte aligned");
+    return linear_impl("moe_linear_prenorm", s, h, gamma, eps, nullptr, nullptr, w, w_scales, nullptr, out, ws,
+                       ws_bytes, stream);
 }
 
 int moe_check_status(void *ws, void *stream) {

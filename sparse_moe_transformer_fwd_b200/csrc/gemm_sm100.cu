@@ -163,6 +163,8 @@ struct KParams {
     const int32_t *seg_slot, *seg_src, *seg_ret;
     uint16_t *const *ret_y;  // device array [world]
     int sc_tma;            // fp32 promotion: the scale groups are loaded by TMA (tmap_sa, tmap_sw)
+    int early_b;           // single segment: B may be read ahead of the kernel before this one
+    int nb_valid;          // 128-row blocks of B that have scales (a single slot's ragged last tile)
 };
 
 template <int TM>
@@ -327,7 +329,8 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
         fence_mbar_init();
     }
     // One segment (a dense layer): the block's first work item and the weights
-    // it streams depend on no earlier kernel, so thread 0 (which initialised
+    // it streams depend on no earlier kernel of the call (early_b: nor on one
+    // before the call, which an earlier launch of the call has waited for), so thread 0 (which initialised
     // the barriers) starts the B loads of its first `pre` stages before the
     // wait below; the producer adds their A loads after it.
     int pre = 0;
@@ -348,7 +351,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
         prefetch_tmap(&tmap_a);
         prefetch_tmap(&tmap_b);
         const int single_items = ((p.rows_total + TM - 1) / TM) * p.n_tiles_n * KS;
-        if (!p.seg_start && !MX && static_cast<int>(blockIdx.x) < single_items) {
+        if (p.early_b && !p.seg_start && !MX && static_cast<int>(blockIdx.x) < single_items) {
             int tile, ks, kb0, nk;
             k_range(blockIdx.x, tile, ks, kb0, nk);
             long long t_lo, t_hi;
@@ -590,7 +593,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                             const int which = lane / SF_GROUP, j = lane % SF_GROUP;
                             const int nb = which == 0 ? (GATE_UP ? nt : 2 * nt)
                                                       : (GATE_UP ? p.N_out / 128 + nt : 2 * nt + 1);
-                            const bool in = kb0 + j < KB;
+                            const bool in = kb0 + j < KB && nb < p.nb_valid;
                             const int slot_w = p.seg_slot ? __ldg(p.seg_slot + seg) : seg;
                             cp_async4(&s.sf_b[slot][which][j],
                                       p.b_scales + (in ? (static_cast<size_t>(slot_w) * NB + nb) * KB + kb0 + j : 0),
@@ -702,7 +705,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                         a0[j] = (in && r0 < rows_valid) ? __ldg(p.a_scales + (static_cast<size_t>(row0) + r0) * KB + kb) : 0.0f;
                         a1[j] = (in && r1 < rows_valid) ? __ldg(p.a_scales + (static_cast<size_t>(row0) + r1) * KB + kb) : 0.0f;
                     }
-                    if (lane < 8 && kbg + wj < kb0 + nk)
+                    if (lane < 8 && kbg + wj < kb0 + nk && (wh ? nb_hi : nb_lo) < p.nb_valid)
                         wv = __ldg(p.b_scales + (static_cast<size_t>(slot_w) * NB + (wh ? nb_hi : nb_lo)) * KB + kbg + wj);
                     int go = 1;
                     if (lane == 0) go = mbar_wait(&s.sc_empty[slot], par, abort, p.status) ? 1 : 0;
@@ -936,8 +939,8 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     }
                 }
             } else {
-                if (DENSE && KS > 1) {
-                    // split K: store this K range's binary32 partial sums; the
+                if (DENSE && p.partial) {
+                    // split K (or sums wanted in binary32): store this K range's binary32 partial sums; the
                     // reduce kernel that follows adds the KS ranges in K order
                     ks = item - (item / KS) * KS;  // recomputed: not kept live through the chunk loop
                     if (store_row) {
@@ -1036,7 +1039,9 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-bool make_map_2d(CUtensorMap *m, const void *base, bool fp8, int K, int rows, int box_rows = 128) {
+}  // namespace
+
+bool make_map_2d(CUtensorMap *m, const void *base, bool fp8, int K, int rows, int box_rows) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
     const int es = fp8 ? 1 : 2;
@@ -1050,6 +1055,7 @@ bool make_map_2d(CUtensorMap *m, const void *base, bool fp8, int K, int rows, in
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+namespace {
 
 // binary32 [rows, cols] row-major, boxes of box_rows x 4 (16 bytes a row, no
 // swizzle; reads past the array give 0)
@@ -1102,12 +1108,15 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launche
     if (!m64 && g.tile_m != 128) return cudaErrorInvalidValue;
     if (!make_map_2d(&ma, g.a, g.fp8, g.K, g.rows_total, m64 ? 64 : 128))
         return cudaErrorInvalidValue;
+    if (g.b_rows_valid && (g.n_slots != 1 || g.gate_up || g.seg_start || !g.partial || g.b_rows_valid > b_rows))
+        return cudaErrorInvalidValue;
+    // rows of B: past them the maps fill with zeros
+    const long long rows = g.b_rows_valid ? g.b_rows_valid : static_cast<long long>(g.n_slots) * b_rows;
     if (g.b_rowmajor) {
-        const long long rows = static_cast<long long>(g.n_slots) * b_rows;
         if (rows >= (1LL << 31)) return cudaErrorInvalidValue;
         if (!make_map_2d(&mb, g.b, g.fp8, g.K, static_cast<int>(rows))) return cudaErrorInvalidValue;
     } else {
-        const long long b_tile_rows = static_cast<long long>(g.n_slots) * b_rows * (g.K * (g.fp8 ? 1 : 2) / 128);
+        const long long b_tile_rows = rows * (g.K * (g.fp8 ? 1 : 2) / 128);
         if (b_tile_rows >= (1LL << 31)) return cudaErrorInvalidValue;
         if (!make_map_2d(&mb, g.b, g.fp8, g.fp8 ? 128 : 64, static_cast<int>(b_tile_rows)))
             return cudaErrorInvalidValue;
@@ -1130,6 +1139,8 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launche
     kp.ue8m0 = g.ue8m0 ? 1 : 0;
     kp.rows_total = g.rows_total;
     kp.b_rowmajor = g.b_rowmajor ? 1 : 0;
+    kp.early_b = g.early_b ? 1 : 0;
+    kp.nb_valid = g.b_rows_valid ? (g.b_rows_valid + 127) / 128 : b_rows / 128;
     kp.seg_slot = g.seg_slot;
     kp.seg_src = g.seg_src;
     kp.seg_ret = g.seg_ret;
@@ -1147,7 +1158,7 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launche
         for (int ks = 0; ks < ksp; ++ks) aligned = aligned && (ks * kbn / ksp) % 4 == 0;
         kp.sc_tma = aligned &&
                     make_map_scales(&msa, g.a_scales, kbn, g.rows_total, m64 ? 64 : 128) &&
-                    make_map_scales(&msw, g.b_scales, kbn, static_cast<long long>(g.n_slots) * (b_rows / 128), 1)
+                    make_map_scales(&msw, g.b_scales, kbn, (rows + 127) / 128, 1)
                         ? 1 : 0;
     }
     // block-scaled MMA (UE8M0 scales): all of K accumulates in TMEM
@@ -1158,7 +1169,7 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launche
         return cudaErrorInvalidValue;
     kp.partial = g.partial;
     // with split K the residual is added by the reduce kernel
-    kp.residual = (g.gate_up || kp.ksplit > 1) ? nullptr : g.residual;
+    kp.residual = (g.gate_up || g.partial) ? nullptr : g.residual;
     // upper bound of work items: every segment's tiles, each at most one partial
     const long long max_mtiles = g.rows_total / g.tile_m + g.n_segments;
     const long long max_tiles = max_mtiles * kp.n_tiles_n * kp.ksplit;
@@ -1167,7 +1178,8 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launche
     cudaError_t e;
     mark_launch(st, *launches, g.gate_up ? "grouped_gemm_gate_up" : "grouped_gemm_down");
     // the dense layer's down GEMM (split K or a residual) has its own instances
-    const bool dense = !g.gate_up && (kp.ksplit > 1 || kp.residual);
+    const bool dense = !g.gate_up && (kp.partial || kp.residual);
+    if (mx && kp.partial) return cudaErrorInvalidValue;
     if (dense && mx)
         e = launch_t<true, false, true, false, true>(ma, mb, msa, msw, kp, grid, st);
     else if (g.fp8 && g.ue8m0)

@@ -141,9 +141,20 @@ struct GemmArgs {
     // sums to partial [ksplit][rows_total][N_out] instead of Y; the caller
     // then runs launch_splitk_reduce.
     int ksplit;
-    float *partial;
+    float *partial;            // also taken with ksplit 1: binary32 sums instead of Y
+    // Single segment: an earlier launch of the same call has waited for the
+    // stream, so B may be loaded ahead of this launch's own wait.
+    bool early_b;
+    // Rows of B that exist, of the N_out read (one slot, no gate/up; 0: all
+    // of them).  Columns past them come out as 0, in partial only.
+    int b_rows_valid;
     const uint16_t *residual;  // down GEMM without split: bf16 [rows_total, N_out] added before rounding
 };
+// Tensor map of a row-major [rows, K] operand of the tensor cores (e4m3 or
+// bf16): boxes of 128 bytes of K x box_rows rows, 128-byte swizzle; reads past
+// the last row give 0.
+bool make_map_2d(CUtensorMap *m, const void *base, bool fp8, int K, int rows, int box_rows = 128);
+
 constexpr int kMaxSplitK = 8;
 constexpr int kMaxEpRanks = MOE_EP_MAX_RANKS;  // ranks of an expert-parallel group
 // Output tiles of a GEMM with one segment of `rows` rows.
@@ -153,6 +164,34 @@ cudaError_t launch_splitk_reduce(const float *partial, int ksplit, int rows, int
                                  const uint16_t *residual, uint16_t *out, cudaStream_t st,
                                  int *launches);
 cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launches);
+
+// Block-scaled product of at most kLinearStreamRows rows of codes (linear.cu).
+constexpr int kLinearStreamRows = 64;
+constexpr int kLinearMaxCtas = 160;  // CTAs of linear_stream (sizes its partial sums)
+struct LinearStreamArgs {
+    const void *a;             // e4m3 [T, K]
+    const float *a_scales;     // [T, K/128]
+    const void *w;             // e4m3 [N, K], row-major or tiled
+    const float *w_scales;     // [ceil(N/128), K/128]
+    const uint16_t *residual;  // bf16 [T, N] or NULL
+    void *out;                 // [T, N] bf16, or binary32 with out_f32
+    float *partial;            // linear_partial_floats(T)
+    int *counters;             // [ceil(N/128)], zero; left zero
+    int *status;
+    int T, K, N;
+    int out_f32, w_rowmajor;
+};
+inline size_t linear_partial_floats(int T) {
+    return static_cast<size_t>(kLinearMaxCtas) * 2 * 128 * (T <= 16 ? 16 : (T <= 32 ? 32 : 64));
+}
+cudaError_t launch_linear_stream(const LinearStreamArgs &g, cudaStream_t st, int *launches);
+// x (behind the pre-norm) -> codes and scales, as moe_linear quantises it.
+cudaError_t launch_linear_quant(const uint16_t *x, int rows, int K, PreNorm pn, bool ue8m0, uint8_t *a,
+                                float *a_scales, cudaStream_t st, int *launches);
+// out [T, N] = sum of ksplit planes [T, ldp] in order (+ residual).
+cudaError_t launch_linear_finish(const float *partial, int ksplit, int T, int N, int ldp,
+                                 const uint16_t *residual, void *out, int out_f32, cudaStream_t st,
+                                 int *launches);
 
 int num_sms();
 
