@@ -419,6 +419,41 @@ int moe_ep_grouped_swiglu(const moe_shape *shape, int rows, const void *a, const
                           const int *ret_capacity, void *ws, size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
+ * The whole layer for a few tokens (a decode step of a few users, or drafted
+ * tokens to verify), in one cooperative launch: router, quantisation, the
+ * experts' two products and the combine run side by side on one persistent
+ * block per SM, so that expert weights stream from HBM all the while.
+ * Arguments, weights and layouts as for moe_forward; T at most
+ * MOE_FEW_MAX_TOKENS (larger: MOE_ERR_INVALID_ARG).
+ * Routing (topk_idx_out and the gates) is moe_forward's bit for bit.  The
+ * numerics differ from moe_forward's in roundings only: x and H are quantised
+ * as by moe_linear, and the experts' rows are kept in binary32 up to the one
+ * rounding of out.
+ * The launch needs every SM of the device for its blocks to wait for one
+ * another: it starts when the kernels of other streams leave room for them,
+ * and two such calls need a workspace each if they can overlap. */
+#define MOE_FEW_MAX_TOKENS 16
+
+/* Bytes of workspace the calls below need (0 on an invalid shape): the status
+ * word first, then counters that every call leaves zero.  Zero-fill it once
+ * before first use; one workspace then serves these calls for any shapes that
+ * it is large enough for, one after the other on a stream. */
+size_t moe_few_workspace_size(const moe_shape *shape);
+
+int moe_forward_few(const moe_shape *shape, const uint16_t *x, const uint16_t *w_router,
+                    const float *bias, const void *w13, const float *w13_scales, const void *w2,
+                    const float *w2_scales, uint16_t *out, int32_t *topk_idx_out, void *ws,
+                    size_t ws_bytes, void *stream);
+
+/* The FFN block, as moe_forward_prenorm: out = h + MoE(x), x = bf16((h * rstd)
+ * * gamma); the statistics are a launch of their own. */
+int moe_forward_few_prenorm(const moe_shape *shape, const uint16_t *h, const uint16_t *gamma,
+                            float eps, const uint16_t *w_router, const float *bias, const void *w13,
+                            const float *w13_scales, const void *w2, const float *w2_scales,
+                            uint16_t *out, int32_t *topk_idx_out, void *ws, size_t ws_bytes,
+                            void *stream);
+
+/* ------------------------------------------------------------------------
  * Block-scaled linear layer: the projections next to the FFN layer, on the
  * same blockwise FP8 ("DeepSeek-R1" (aguasto.com), "Quantization"; "DeepSeek
  * v3 and R1 Model Architecture", "First ever FP8 Precision...").

@@ -24,7 +24,8 @@ from ._native import (EXPORTS, MOE_BF16, MOE_FP8_BLOCK, MOE_FP8_UE8M0, MOE_LAYOU
                       moe_quant_scatter, moe_ep_dispatch, moe_ep_workspace_size,
                       moe_ep_grouped_swiglu, MOE_EP_MAX_RANKS, MoeLinearShape, make_linear_shape,
                       moe_linear_workspace_size, alloc_linear_workspace, fp8_block_gemm, moe_linear,
-                      moe_linear_prenorm)
+                      moe_linear_prenorm, MOE_FEW_MAX_TOKENS, moe_few_workspace_size,
+                      alloc_few_workspace, moe_forward_few, moe_forward_few_prenorm)
 
 __all__ = [
     "MoELayer", "MoeError", "MoeShape", "make_shape", "alloc_workspace", "lib", "EXPORTS",
@@ -38,7 +39,8 @@ __all__ = [
     "moe_quant_scatter", "moe_ep_dispatch", "moe_ep_workspace_size", "moe_ep_grouped_swiglu",
     "MOE_EP_MAX_RANKS", "Fp8Linear", "MoeLinearShape", "make_linear_shape",
     "moe_linear_workspace_size", "alloc_linear_workspace", "fp8_block_gemm", "moe_linear",
-    "moe_linear_prenorm",
+    "moe_linear_prenorm", "MOE_FEW_MAX_TOKENS", "moe_few_workspace_size", "alloc_few_workspace",
+    "moe_forward_few", "moe_forward_few_prenorm",
 ]
 
 
@@ -102,7 +104,7 @@ class MoELayer:
             self.w13s = self.w2s = None
         else:
             raise ValueError(precision)
-        self._ws = {}
+        self._ws, self._few_ws = {}, {}
 
     def shape(self, T: int) -> MoeShape:
         return make_shape(T, self.d, self.E, self.top_k, self.de, self.n_shared,
@@ -136,8 +138,41 @@ class MoELayer:
                             topk_idx_out=topk_idx_out, stream=stream)
         return out
 
+    def few_workspace(self, T: int) -> torch.Tensor:
+        ws = self._few_ws.get(T)
+        if ws is None:
+            ws = alloc_few_workspace(self.shape(T), self.w13.device)
+            self._few_ws[T] = ws
+        return ws
+
+    def forward_few(self, x: torch.Tensor, out: torch.Tensor | None = None,
+                    topk_idx_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """The layer for at most MOE_FEW_MAX_TOKENS tokens, in one launch;
+        routing as in __call__, out equal up to roundings."""
+        T = x.shape[0]
+        if out is None:
+            out = torch.empty(T, self.d, dtype=torch.bfloat16, device=x.device)
+        moe_forward_few(self.shape(T), x, self.w_router, self.bias, self.w13, self.w13s, self.w2,
+                        self.w2s, out, self.few_workspace(T), topk_idx_out=topk_idx_out, stream=stream)
+        return out
+
+    def forward_few_prenorm(self, h: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6,
+                            out: torch.Tensor | None = None,
+                            topk_idx_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """forward_prenorm for at most MOE_FEW_MAX_TOKENS tokens."""
+        T = h.shape[0]
+        if out is None:
+            out = torch.empty(T, self.d, dtype=torch.bfloat16, device=h.device)
+        moe_forward_few_prenorm(self.shape(T), h, gamma, eps, self.w_router, self.bias, self.w13,
+                                self.w13s, self.w2, self.w2s, out, self.few_workspace(T),
+                                topk_idx_out=topk_idx_out, stream=stream)
+        return out
+
     def check_status(self, T: int) -> int:
-        return moe_check_status(self.workspace(T))
+        """Status of the calls with T tokens so far: the first error that
+        either workspace recorded."""
+        few = moe_check_status(self._few_ws[T]) if T in self._few_ws else 0
+        return moe_check_status(self.workspace(T)) or few
 
 
 class DenseFFN:

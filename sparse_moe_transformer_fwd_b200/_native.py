@@ -33,9 +33,11 @@ EXPORTS = ("moe_workspace_size", "moe_route", "moe_permute", "fp8_block_quant",
            "fp8_block_quant_ue8m0", "moe_dense_workspace_size", "moe_dense_ffn",
            "moe_dense_ffn_prenorm", "moe_workspace_layout", "moe_quant_scatter",
            "moe_ep_dispatch", "moe_ep_workspace_size", "moe_ep_grouped_swiglu",
-           "moe_linear_workspace_size", "fp8_block_gemm", "moe_linear", "moe_linear_prenorm")
+           "moe_linear_workspace_size", "fp8_block_gemm", "moe_linear", "moe_linear_prenorm",
+           "moe_few_workspace_size", "moe_forward_few", "moe_forward_few_prenorm")
 
 MOE_EP_MAX_RANKS = 64
+MOE_FEW_MAX_TOKENS = 16  # tokens of moe_forward_few
 
 # fixed score scratch of moe_route_noalloc, in floats (include/moe_fwd.h)
 MOE_ROUTE_NOALLOC_MAX_SCORES = 1 << 20
@@ -116,6 +118,10 @@ def lib() -> ctypes.CDLL:
         L.moe_dense_workspace_size.restype = sz
         L.moe_dense_ffn.argtypes = [dp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.moe_dense_ffn_prenorm.argtypes = [dp, vp, vp, cf, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_few_workspace_size.argtypes = [sp]
+        L.moe_few_workspace_size.restype = sz
+        L.moe_forward_few.argtypes = L.moe_forward.argtypes
+        L.moe_forward_few_prenorm.argtypes = L.moe_forward_prenorm.argtypes
         lp = ctypes.POINTER(MoeLinearShape)
         L.moe_linear_workspace_size.argtypes = [lp]
         L.moe_linear_workspace_size.restype = sz
@@ -135,7 +141,8 @@ def lib() -> ctypes.CDLL:
                      "moe_set_kernel_events", "moe_pack_tiles", "moe_forward_prenorm",
                      "moe_dense_ffn", "moe_dense_ffn_prenorm", "moe_workspace_layout",
                      "moe_quant_scatter", "moe_ep_dispatch", "moe_ep_grouped_swiglu",
-                     "fp8_block_gemm", "moe_linear", "moe_linear_prenorm"):
+                     "fp8_block_gemm", "moe_linear", "moe_linear_prenorm", "moe_forward_few",
+                     "moe_forward_few_prenorm"):
             getattr(L, name).restype = ci
         _LIB = L
     return _LIB
@@ -395,6 +402,56 @@ def moe_ep_grouped_swiglu(shape, a, a_scales, seg_start, seg_rows, seg_slot, seg
         _ptr(w13_scales, torch.float32, "w13_scales"), _ptr(w2, wt, "w2"),
         _ptr(w2_scales, torch.float32, "w2_scales"), world, _ptr_array(ret_y, _BF16, "ret_y"),
         cap, _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+
+
+def moe_few_workspace_size(shape: MoeShape) -> int:
+    n = lib().moe_few_workspace_size(ctypes.byref(shape))
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, lib().moe_last_error().decode())
+    return n
+
+
+def alloc_few_workspace(shape: MoeShape, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace of moe_few_workspace_size bytes."""
+    return torch.zeros(moe_few_workspace_size(shape), dtype=torch.uint8, device=device)
+
+
+def _few_call(fn, shape, x, gamma, eps, w_router, bias, w13, w13_scales, w2, w2_scales, out, ws,
+              topk_idx_out, stream):
+    """Checks sizes and devices and calls fn on the tensors' device."""
+    T, d, E, de, S = shape.T, shape.d_model, shape.n_experts, shape.d_expert, shape.n_experts + shape.n_shared
+    fp8 = shape.precision in (MOE_FP8_BLOCK, MOE_FP8_UE8M0)
+    wt, f32 = _FP8 if fp8 else _BF16, torch.float32
+    dev = _device_of(x=x, gamma=gamma, w_router=w_router, bias=bias, w13=w13, w13_scales=w13_scales, w2=w2,
+                     w2_scales=w2_scales, out=out, ws=ws, topk_idx_out=topk_idx_out)
+    n13, n2 = S * 2 * de * d, S * d * de
+    args = [_ptr(_sized(x, T * d, "x"), _BF16, "x")]
+    if fn is lib().moe_forward_few_prenorm:
+        args += [_ptr(_sized(gamma, d, "gamma"), _BF16, "gamma"), float(eps)]
+    args += [_ptr(_sized(w_router, E * d, "w_router"), _BF16, "w_router"), _ptr(_sized(bias, E, "bias"), f32, "bias"),
+             _ptr(_sized(w13, n13, "w13"), wt, "w13"),
+             _ptr(_sized(w13_scales, n13 // 16384 if fp8 else 0, "w13_scales"), f32, "w13_scales"),
+             _ptr(_sized(w2, n2, "w2"), wt, "w2"),
+             _ptr(_sized(w2_scales, n2 // 16384 if fp8 else 0, "w2_scales"), f32, "w2_scales"),
+             _ptr(_sized(out, T * d, "out"), _BF16, "out"),
+             _ptr(_sized(topk_idx_out, T * shape.top_k, "topk_idx_out"), torch.int32, "topk_idx_out"),
+             _ptr(ws, torch.uint8, "ws")]
+    with torch.cuda.device(dev):
+        _check(fn(ctypes.byref(shape), *args, ws.numel(), _stream(stream)))
+
+
+def moe_forward_few(shape, x, w_router, bias, w13, w13_scales, w2, w2_scales, out, ws,
+                    topk_idx_out=None, stream=None):
+    """The whole layer for at most MOE_FEW_MAX_TOKENS tokens, in one launch."""
+    _few_call(lib().moe_forward_few, shape, x, None, 0.0, w_router, bias, w13, w13_scales, w2, w2_scales, out,
+              ws, topk_idx_out, stream)
+
+
+def moe_forward_few_prenorm(shape, h, gamma, eps, w_router, bias, w13, w13_scales, w2, w2_scales, out,
+                            ws, topk_idx_out=None, stream=None):
+    """out = h + MoE(bf16(RMSNorm(h) * gamma)) for at most MOE_FEW_MAX_TOKENS tokens."""
+    _few_call(lib().moe_forward_few_prenorm, shape, h, gamma, eps, w_router, bias, w13, w13_scales, w2,
+              w2_scales, out, ws, topk_idx_out, stream)
 
 
 def make_linear_shape(T, K, N, precision="fp8", weight_layout=MOE_LAYOUT_TILED,

@@ -1003,6 +1003,146 @@ int moe_ep_grouped_swiglu(const moe_shape *s, int rows, const void *a, const flo
 
 }  // extern "C"
 
+// ------------------------------------------- MoE layer for a few tokens ---
+namespace moe {
+namespace {
+
+struct FewLayout {
+    size_t status, counters, rstd, rough, scores, idx, gates, xq, xs, xn, h, hs, y, total;
+    int list_rows;
+};
+
+int check_few_shape(const moe_shape *s) {
+    RETURN_IF(check_shape(s));
+    if (s->T > kFewTokens)
+        return fail(MOE_ERR_INVALID_ARG, "T must be at most %d here; moe_forward takes larger batches", kFewTokens);
+    if (s->d_model > kFewMaxCols * 128)
+        return fail(MOE_ERR_INVALID_ARG, "d_model must be at most %d here", kFewMaxCols * 128);
+    const long long slots = s->n_experts + s->n_shared, es = is_fp8(s) ? 1 : 2;
+    if (slots * 2 * s->d_expert * s->d_model * es / 128 >= (1LL << 31))
+        return fail(MOE_ERR_INVALID_ARG, "expert weights too large for one tensor map");
+    return MOE_OK;
+}
+
+// Status word and counters lie at the same place in every shape's layout and
+// nothing else reaches them, so one zero-filled workspace serves any shapes.
+FewLayout few_layout(const moe_shape *s) {
+    const size_t T = s->T, E = s->n_experts, k = s->top_k, d = s->d_model, de = s->d_expert;
+    const bool fp8 = is_fp8(s);
+    FewLayout L{};
+    // experts worked on: those that the rough or the exact logits select
+    L.list_rows = static_cast<int>(std::min(E, 2 * T * k)) + s->n_shared;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += (bytes + 255) & ~static_cast<size_t>(255);
+        return at;
+    };
+    L.status = take(256);
+    L.counters = take(sizeof(FewCounters));
+    L.rstd = take(T * 4);
+    L.rough = take(T * E * 4);
+    L.scores = take(T * E * 4);
+    L.idx = take(T * k * 4);
+    L.gates = take(T * k * 4);
+    L.xq = take(fp8 ? T * d : 0);
+    L.xs = take(fp8 ? d / 128 * kFewTokens * 4 : 0);
+    L.xn = take(T * d * 2);
+    L.h = take(static_cast<size_t>(L.list_rows) * kFewTokens * de * (fp8 ? 1 : 2));
+    L.hs = take(fp8 ? L.list_rows * (de / 128) * kFewTokens * 4 : 0);
+    L.y = take(T * (k + s->n_shared) * d * 4);
+    L.total = off;
+    return L;
+}
+
+int few_impl(const moe_shape *s, const uint16_t *x, const uint16_t *gamma, float eps,
+             const uint16_t *w_router, const float *bias, const void *w13, const float *w13_scales,
+             const void *w2, const float *w2_scales, uint16_t *out, int32_t *topk_idx_out, void *ws,
+             size_t ws_bytes, void *stream) {
+    const CallRange nvtx_range(gamma ? "moe_forward_few_prenorm" : "moe_forward_few");
+    RETURN_IF(check_few_shape(s));
+    const FewLayout L = few_layout(s);
+    if (!ws) return fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
+    if (reinterpret_cast<uintptr_t>(ws) & 255)
+        return fail(MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    if (ws_bytes < L.total)
+        return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, L.total);
+    if (s->T == 0) return g_launches = 0, MOE_OK;
+    CHECK_PTR(x);
+    CHECK_PTR(w_router);
+    CHECK_PTR(bias);
+    CHECK_PTR(out);
+    if (topk_idx_out && !aligned16(topk_idx_out))
+        return fail(MOE_ERR_INVALID_ARG, "topk_idx_out is not 16-byte aligned");
+    if (gamma && !(eps >= 0.0f)) return fail(MOE_ERR_INVALID_ARG, "eps must be >= 0");
+    RETURN_IF(check_weights(s, w13, w13_scales, w2, w2_scales));
+    RETURN_IF(check_device());
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int n = 0;
+    FewArgs g{};
+    if (gamma) {
+        float *rstd = at<float>(ws, L.rstd);
+        LAUNCH(launch_rstd(x, s->T, s->d_model, eps, rstd, st, &n), "pre-norm statistics");
+        g.pn.rstd = rstd;
+        g.pn.gamma = gamma;
+    }
+    g.shape = s;
+    g.x = x;
+    g.w_router = w_router;
+    g.bias = bias;
+    g.w13 = w13;
+    g.w2 = w2;
+    g.w13_scales = w13_scales;
+    g.w2_scales = w2_scales;
+    g.out = out;
+    g.idx = topk_idx_out ? topk_idx_out : at<int32_t>(ws, L.idx);
+    g.gates = at<float>(ws, L.gates);
+    g.rough = at<float>(ws, L.rough);
+    g.scores = at<float>(ws, L.scores);
+    g.xq = at<uint8_t>(ws, L.xq);
+    g.xs = at<float>(ws, L.xs);
+    g.xn = at<uint16_t>(ws, L.xn);
+    g.h = at<uint8_t>(ws, L.h);
+    g.hs = at<float>(ws, L.hs);
+    g.y = at<float>(ws, L.y);
+    g.list_rows = L.list_rows;
+    g.counters = at<FewCounters>(ws, L.counters);
+    g.status = at<int>(ws, L.status);
+    LAUNCH(launch_few(g, st, &n), "moe few");
+    mark_launch(st, n);
+    g_launches = n;
+    return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" {
+
+size_t moe_few_workspace_size(const moe_shape *s) {
+    if (check_few_shape(s) != MOE_OK) return 0;
+    return few_layout(s).total;
+}
+
+int moe_forward_few(const moe_shape *s, const uint16_t *x, const uint16_t *w_router, const float *bias,
+                    const void *w13, const float *w13_scales, const void *w2, const float *w2_scales,
+                    uint16_t *out, int32_t *topk_idx_out, void *ws, size_t ws_bytes, void *stream) {
+    return few_impl(s, x, nullptr, 0.0f, w_router, bias, w13, w13_scales, w2, w2_scales, out, topk_idx_out, ws,
+                    ws_bytes, stream);
+}
+
+int moe_forward_few_prenorm(const moe_shape *s, const uint16_t *h, const uint16_t *gamma, float eps,
+                            const uint16_t *w_router, const float *bias, const void *w13,
+                            const float *w13_scales, const void *w2, const float *w2_scales,
+                            uint16_t *out, int32_t *topk_idx_out, void *ws, size_t ws_bytes, void *stream) {
+    if (!gamma) return fail(MOE_ERR_INVALID_ARG, "gamma is NULL");
+    if (!aligned16(gamma)) return fail(MOE_ERR_INVALID_ARG, "gamma is not 16-byte aligned");
+    return few_impl(s, h, gamma, eps, w_router, bias, w13, w13_scales, w2, w2_scales, out, topk_idx_out, ws,
+                    ws_bytes, stream);
+}
+
+}  // extern "C"
+
 // ------------------------------------------------- block-scaled linear ---
 namespace moe {
 namespace {

@@ -56,25 +56,6 @@ __device__ __forceinline__ float ue8m0_scale(float amax, float *inv) {
                      : __uint_as_float(1u << 22);
 }
 
-// Scale and factor of a 1x128 activation tile in the calls that quantise on
-// the way to a product (moe_linear, moe_forward_few): scale = amax * (1/448)
-// and *inv = 448 * (1/amax), each operation a correctly rounded binary32 one.
-// One reciprocal serves both where fp8_block_quant divides twice (a tile is
-// quantised again by every CTA that reads it); either value is within an ulp
-// of the quotient, so only an element at a border of two codes can differ.
-// The factor of a tile below 448 / FLT_MAX is held at FLT_MAX (no code is NaN
-// for 0 * inf); an all-zero tile gets scale 1 and factor 0; ue: power-of-two
-// scale (ue8m0_scale).
-__device__ __forceinline__ float tile_scale(float amax, bool ue, float *inv) {
-    if (amax == 0.0f) {
-        *inv = 0.0f;
-        return 1.0f;
-    }
-    if (ue) return ue8m0_scale(amax, inv);
-    *inv = fminf(__fmul_rn(__frcp_rn(amax), 448.0f), 3.402823466e38f);
-    return __fmul_rn(amax, static_cast<float>(1.0 / 448.0));
-}
-
 // Pre-norm of one element: bf16((h * rstd) * gamma) widened back to binary32.
 __device__ __forceinline__ float prenorm_elem(float h, float rstd, float gamma) {
     const float v = __fmul_rn(__fmul_rn(h, rstd), gamma);

@@ -1,0 +1,839 @@
+// The whole MoE layer for a few tokens in one launch ("DeepSeek-R1"
+// architecture card: 256 routed experts, 8 active per token, 1 shared expert).
+//
+// For at most 16 tokens the layer reads the weights of the experts that the
+// tokens meet (44 MB an expert at d 7168, d_expert 2048) and little else, so
+// its floor is that many bytes of HBM: 61 us at one token.  What stands above
+// the floor in separate kernels is the chain between them (router, top-k,
+// permutation, quantisation, two GEMMs, combine) and the router itself, whose
+// logits are sequential chains of d fused multiply-adds (20 us at d = 7168).
+// This kernel runs all of it on one persistent CTA per SM, so that weights
+// stream while everything else is worked out:
+//   1. every CTA quantises its share of x and computes its experts' logits
+//      roughly (order of summation left free).  Once all have (one grid
+//      barrier), each CTA finds the experts that the rough logits select and
+//      starts on their gate/up products, for all tokens at once (the tokens
+//      are the MMA's 16 columns whether they chose the expert or not, so an
+//      expert's H does not depend on who chose it).
+//   2. meanwhile four warps run the exact logit chains, in the order that
+//      moe_route defines, and select from them.  An expert that the rough
+//      logits missed is appended to the work; one that they took in vain has
+//      cost its time.  So routing is moe_route's, bit for bit.
+//   3. down products of the experts selected, each begun as soon as that
+//      expert's H is complete; its weights are loaded ahead of that.
+//   4. the CTA that completes a 128-column block of the output (all experts)
+//      adds the experts' rows with their gates, in rank order.
+// Work items are 128 features of one expert (gate and up rows, all of K) and
+// 128 output columns of one expert; weights are the M operand of the MMA.
+//   warp 0      TMA producer: two weight tiles a stage (gate and up rows of one
+//               K block, or two K blocks of the down product) and the tokens'
+//               columns
+//   warp 1      TMEM allocator and MMA issuer (two accumulators of 16 columns
+//               a stage, NBUF stages in flight)
+//   warp 2      the stage's scales (e4m3), copied ahead with cp.async
+//   warp 3      idle after the setup
+//   warps 4-7   epilogue: thread = weight row
+//   warps 8-11  exact routing
+// The kernel is launched cooperatively (all CTAs resident), since CTAs wait for
+// one another.  Every wait is bounded: on expiry the CTA records
+// MOE_ERR_TIMEOUT, sets an abort word that ends the others' waits, drains what
+// it has in flight, frees its TMEM and exits; the last CTA to exit zeroes every
+// counter, so the workspace serves the next call.
+#include "common.cuh"
+#include "kernels.h"
+#include "quant_math.cuh"
+#include "route_math.cuh"
+
+#include <algorithm>
+
+namespace moe {
+namespace {
+
+constexpr int FT = kFewTokens;  // MMA columns
+constexpr int FEW_THREADS = 384;
+constexpr int FEW_STAGES = 6;
+constexpr int W_BYTES = 128 * 128;
+constexpr int X_BYTES = FT * 128;
+constexpr int NBUF = 4;
+constexpr int SC_RING = 8;
+constexpr int TMEM_COLS = NBUF * 2 * FT;
+constexpr int ROUTE_THREADS = 128;
+constexpr int MAX_K = 32;
+static_assert(FT == 16, "a stage's two accumulators are one 32-column TMEM load");
+
+struct FewSmem {
+    alignas(1024) uint8_t w[FEW_STAGES][2][W_BYTES];
+    alignas(1024) uint8_t x[FEW_STAGES][2][X_BYTES];
+    struct alignas(16) Scales {
+        float x[2][FT];
+        float w[2];
+        float pad[2];
+    } sc[SC_RING];
+    float amax[4][FT];
+    float gate[FT][MAX_K];
+    int16_t sel[FT][MAX_K];        // exact selection
+    uint16_t list[kFewMaxList];    // experts worked on: shared, predicted, missed
+    uint16_t used[kFewMaxList];    // positions in list of the experts selected
+    uint32_t rough_set[32], exact_set[32];
+    int8_t rank[FT];
+    int n_rough, n_list, n_used;
+    uint64_t full[FEW_STAGES], empty[FEW_STAGES];
+    uint64_t sfull[SC_RING], sempty[SC_RING];
+    uint64_t tfull[NBUF], tempty[NBUF];
+    uint64_t routed;
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    int abort;
+    int last;
+};
+static_assert(sizeof(FewSmem) + 1024 <= 227 * 1024, "shared memory budget of one CTA");
+
+struct FewParams {
+    const uint16_t *x;       // [T, d] (the residual stream h behind the pre-norm)
+    PreNorm pn;
+    const uint16_t *w_router;
+    const float *bias;
+    const float *w13_scales, *w2_scales;
+    uint16_t *out;
+    int32_t *idx_out;        // [T, k]
+    float *gates_out;        // [T, k]
+    uint8_t *xq;             // [T, d] codes (fp8)
+    float *xs;               // [d/128][16]
+    uint16_t *xn;            // [T, d] pre-normed x
+    float *rough, *scores;   // [T, E]
+    void *h;                 // [list][16][de]
+    float *hs;               // [list][de/128][16]
+    float *y;                // [T][k + n_shared][d] binary32
+    FewCounters *ctr;
+    int *status;
+    int T, d, E, k, de, n_shared;
+    float routed_scale;
+    int ue, w_rowmajor;
+};
+
+__device__ __forceinline__ int ld_acquire(const int *p) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void red_release(int *p, int v) {
+    asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ int add_acq_rel(int *p, int v) {
+    int old;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
+}
+// generic-proxy writes to global memory before, async-proxy (TMA) reads after
+__device__ __forceinline__ void fence_proxy_async_global() {
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+
+// Waits until *p reaches `want`; false on abort or when the budget runs out
+// (which aborts every CTA of the launch).
+__device__ __forceinline__ bool wait_count(const int *p, int want, const FewParams &q, volatile int *abort) {
+    if (ld_acquire(p) >= want) return true;
+    const long long t0 = clock64();
+    while (true) {
+        if (ld_acquire(p) >= want) return true;
+        if (*abort) return false;
+        if (ld_acquire(&q.ctr->abort)) {
+            *abort = 1;
+            return false;
+        }
+        if (clock64() - t0 > kWaitBudgetCycles) {
+            *abort = 1;
+            atomicExch(&q.ctr->abort, 1);
+            set_status(q.status, MOE_ERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+// The same for an mbarrier of this CTA; a CTA that gives up ends the others'
+// waits too.
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const FewParams &q, volatile int *abort) {
+    if (mbar_wait(bar, parity, abort, q.status)) return true;
+    atomicExch(&q.ctr->abort, 1);
+    return false;
+}
+
+struct Item {
+    bool down;
+    int pos;     // position in the list
+    int expert;  // weight slot
+    int blk;     // 128-feature block of H, or 128-column block of the output
+    int stages;
+};
+
+__device__ __forceinline__ void topk_any(const float *row, const float *bias, int E, int k, int lane, int &e, float &s) {
+    if (E <= 256) warp_topk<8>(row, bias, E, k, lane, e, s);
+    else warp_topk<kMaxPerLane>(row, bias, E, k, lane, e, s);
+}
+
+// One warp appends the set bits of `set` that `without` lacks, in ascending
+// order, to `list` from position n on; returns the new length.
+__device__ __forceinline__ int append_set(const uint32_t *set, const uint32_t *without, uint16_t *list, int n, int lane) {
+    const uint32_t m = set[lane] & (without ? ~without[lane] : 0xffffffffu);
+    int before = __popc(m);
+    const int mine = before;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, before, off);
+        if (lane >= off) before += o;
+    }
+    int at = n + before - mine;
+    for (uint32_t b = m; b; b &= b - 1) list[at++] = static_cast<uint16_t>(32 * lane + __ffs(b) - 1);
+    return n + __shfl_sync(0xffffffffu, before, 31);
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(FEW_THREADS, 1)
+moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w13,
+               const __grid_constant__ CUtensorMap tmap_h, const __grid_constant__ CUtensorMap tmap_w2,
+               const FewParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    FewSmem &s = *reinterpret_cast<FewSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+    const int G = gridDim.x, cta = blockIdx.x;
+    const int T = p.T, d = p.d, E = p.E, k = p.k, de = p.de;
+    constexpr int KE = FP8 ? 128 : 64;  // elements of a 128-byte K block
+    const int KB1 = d / KE, KB2 = de / KE;
+    const int nf = de / 128, nd = d / 128;
+    volatile int *abort = &s.abort;
+
+    if (tid == 0) {
+        for (int i = 0; i < FEW_STAGES; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], 1);
+        }
+        for (int i = 0; i < SC_RING; ++i) {
+            mbar_init(&s.sfull[i], 32);
+            mbar_init(&s.sempty[i], 4);
+        }
+        for (int i = 0; i < NBUF; ++i) {
+            mbar_init(&s.tfull[i], 1);
+            mbar_init(&s.tempty[i], 4);
+        }
+        mbar_init(&s.routed, 1);
+        mbar_init(&s.mma_done, 1);
+        s.abort = 0;
+        fence_mbar_init();
+        prefetch_tmap(&tmap_x);
+        prefetch_tmap(&tmap_w13);
+        prefetch_tmap(&tmap_h);
+        prefetch_tmap(&tmap_w2);
+    }
+    if (tid < 32) s.rough_set[tid] = s.exact_set[tid] = 0;
+    if (warp == 1) {
+        tmem_alloc(&s.tmem_base, TMEM_COLS);
+        tmem_relinquish();
+    }
+
+    // -------------------------------------- 1. x, rough logits, rough selection
+    // x: half-warps over the (token, 128-column) tiles of all CTAs
+    {
+        const int half = cta * (FEW_THREADS / 16) + tid / 16, l16 = tid % 16, nx = d / 128;
+        for (int i0 = half & ~1; i0 < T * nx; i0 += G * (FEW_THREADS / 16)) {
+            const int i = i0 + (half & 1);
+            const bool in = i < T * nx;
+            const int t = in ? i / nx : 0, kb = in ? i % nx : 0, c = kb * 128 + l16 * 8;
+            if constexpr (FP8) {
+                float v[8];
+                load_x8(p.x, t, c, d, p.pn, v);
+                uint2 code;
+                const float sc = quant_tile8(v, p.ue, &code);
+                if (in) {
+                    *reinterpret_cast<uint2 *>(p.xq + static_cast<size_t>(t) * d + c) = code;
+                    if (l16 == 0) p.xs[kb * FT + t] = sc;
+                }
+            }
+            if (p.pn.gamma && in) {
+                const uint4 raw = *reinterpret_cast<const uint4 *>(p.x + static_cast<size_t>(t) * d + c);
+                *reinterpret_cast<uint4 *>(p.xn + static_cast<size_t>(t) * d + c) = x_vec(raw, p.pn, t, c);
+            }
+        }
+    }
+    // rough logits of experts cta, cta + G, ...: one warp a (token, expert) pair
+    {
+        const int ne = E > cta ? (E - 1 - cta) / G + 1 : 0;
+        for (int i = warp; i < ne * T; i += FEW_THREADS / 32) {
+            const int e = cta + i / T * G, t = i % T;
+            const uint4 *wr = reinterpret_cast<const uint4 *>(p.w_router + static_cast<size_t>(e) * d);
+            const uint4 *xr = reinterpret_cast<const uint4 *>(p.x + static_cast<size_t>(t) * d);
+            float a0 = 0.0f, a1 = 0.0f;
+#pragma unroll 4
+            for (int v = lane; v < d / 8; v += 32) {
+                const uint4 a = wr[v], b = x_vec(xr[v], p.pn, t, v * 8);
+                a0 = fmaf(bf16_lo(a.x), bf16_lo(b.x), a0);
+                a1 = fmaf(bf16_hi(a.x), bf16_hi(b.x), a1);
+                a0 = fmaf(bf16_lo(a.y), bf16_lo(b.y), a0);
+                a1 = fmaf(bf16_hi(a.y), bf16_hi(b.y), a1);
+                a0 = fmaf(bf16_lo(a.z), bf16_lo(b.z), a0);
+                a1 = fmaf(bf16_hi(a.z), bf16_hi(b.z), a1);
+                a0 = fmaf(bf16_lo(a.w), bf16_lo(b.w), a0);
+                a1 = fmaf(bf16_hi(a.w), bf16_hi(b.w), a1);
+            }
+            a0 += a1;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) a0 += __shfl_xor_sync(0xffffffffu, a0, off);
+            if (lane == 0) p.rough[static_cast<size_t>(t) * E + e] = sigmoid_cw(a0, exp_consts());
+        }
+    }
+    fence_proxy_async_global();  // x is read by TMA
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+        red_release(&p.ctr->prepared, 1);
+        wait_count(&p.ctr->prepared, G, p, abort);
+        fence_proxy_async_global();
+    }
+    __syncthreads();
+    const bool ready = !s.abort;  // uniform: without x and the rough selection no work is done
+    if (ready)
+        for (int t = warp; t < T; t += FEW_THREADS / 32) {
+            int e;
+            float sc;
+            topk_any(p.rough + static_cast<size_t>(t) * E, p.bias, E, k, lane, e, sc);
+            if (lane < k) atomicOr(&s.rough_set[e >> 5], 1u << (e & 31));
+        }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) {
+        if (lane == 0 && p.n_shared) s.list[0] = static_cast<uint16_t>(E);
+        const int n = append_set(s.rough_set, nullptr, s.list, p.n_shared, lane);
+        if (lane == 0) s.n_rough = s.n_list = n;
+    }
+    __syncthreads();
+    const uint32_t tmem_base = s.tmem_base;
+    const int gu_rough = s.n_rough * nf;  // gate/up items of the rough selection
+
+    // Work items in one order for every role: gate/up of the list, then down of
+    // the experts selected; item i belongs to CTA i mod G.  Past the rough
+    // selection's items the exact routing has to be known.
+    auto next_item = [&](int &i, bool &routed, Item &it) {
+        if (!ready) return false;
+        if (i >= gu_rough && !routed) {
+            if (!wait_bar(&s.routed, 0, p, abort)) return false;
+            routed = true;
+        }
+        const int gu = i < gu_rough ? gu_rough : s.n_list * nf;
+        it.down = i >= gu;
+        if (!it.down) {
+            it.pos = i / nf;
+            it.blk = i - it.pos * nf;
+            it.stages = KB1;
+        } else {
+            const int j = i - gu;
+            const int u = j / nd;
+            if (u >= s.n_used) return false;
+            it.pos = s.used[u];
+            it.blk = j - u * nd;
+            it.stages = (KB2 + 1) / 2;
+        }
+        it.expert = s.list[it.pos];
+        i += G;
+        return true;
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------- producer
+        if (lane == 0) {
+            int stage = 0, i = cta;
+            uint32_t phase = 0, armed = 0, armed_phase = 0;
+            bool ok = true, routed = false;
+            Item it;
+            while (ok && next_item(i, routed, it)) {
+                // the down product's tokens (H) are loaded once the expert's H is
+                // complete; the weights of the ring's stages go ahead of that
+                bool have_x = !it.down;
+                int deferred = 0, issued = 0;
+                auto load_x = [&](int st, int q) {  // stage q of the item, in ring slot st
+                    const int n = it.down ? min(2, KB2 - 2 * q) : 1;
+                    for (int j = 0; j < n; ++j) {
+                        if (it.down) tma_load_2d(s.x[st][j], &tmap_h, (2 * q + j) * KE, it.pos * FT, &s.full[st]);
+                        else tma_load_2d(s.x[st][0], &tmap_x, q * KE, 0, &s.full[st]);
+                    }
+                };
+                auto flush = [&] {  // the last `deferred` stages issued wait for their tokens
+                    have_x = wait_count(&p.ctr->h_done[it.pos], nf, p, abort);
+                    fence_proxy_async_global();
+                    // (given up: whatever H holds, so that the drain below ends)
+                    for (; deferred > 0; --deferred)
+                        load_x((stage - deferred + FEW_STAGES) % FEW_STAGES, issued - deferred);
+                    return have_x;
+                };
+                for (int q = 0; q < it.stages; ++q) {
+                    if (deferred == FEW_STAGES && !flush()) {
+                        ok = false;
+                        break;
+                    }
+                    if (!wait_bar(&s.empty[stage], phase ^ 1, p, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    const int n = it.down ? min(2, KB2 - 2 * q) : 2;  // weight tiles
+                    const int nx = it.down ? n : 1;
+                    mbar_arrive_expect_tx(&s.full[stage], n * W_BYTES + nx * X_BYTES);
+                    for (int j = 0; j < n; ++j) {
+                        const int kb = it.down ? 2 * q + j : q;
+                        const long long band = it.down ? static_cast<long long>(it.expert) * nd + it.blk
+                                                       : static_cast<long long>(it.expert) * 2 * nf + j * nf + it.blk;
+                        const CUtensorMap *m = it.down ? &tmap_w2 : &tmap_w13;
+                        if (p.w_rowmajor) tma_load_2d(s.w[stage][j], m, kb * KE, static_cast<int>(band * 128), &s.full[stage]);
+                        else tma_load_2d(s.w[stage][j], m, 0, static_cast<int>((band * (it.down ? KB2 : KB1) + kb) * 128), &s.full[stage]);
+                    }
+                    armed |= 1u << stage;
+                    armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
+                    if (have_x) load_x(stage, q);
+                    else ++deferred;
+                    ++issued;
+                    if (++stage == FEW_STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (deferred > 0 && !flush()) ok = false;
+            }
+            const long long t0 = clock64();
+            for (int st = 0; st < FEW_STAGES; ++st) {
+                if (!(armed >> st & 1)) continue;
+                while (!mbar_try_wait(&s.full[st], armed_phase >> st & 1)) {
+                    if (clock64() - t0 > kWaitBudgetCycles) {
+                        set_status(p.status, MOE_ERR_TIMEOUT);
+                        break;
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA
+        if (lane == 0) {
+            constexpr uint32_t idesc = instr_desc<FP8>(128, FT);
+            int stage = 0, tb = 0, i = cta;
+            uint32_t phase = 0, tphase = 0;
+            bool ok = true, routed = false;
+            Item it;
+            while (ok && next_item(i, routed, it)) {
+                for (int q = 0; q < it.stages; ++q) {
+                    if (!wait_bar(&s.tempty[tb], tphase ^ 1, p, abort) || !wait_bar(&s.full[stage], phase, p, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const int n = it.down ? min(2, KB2 - 2 * q) : 2;
+                    for (int j = 0; j < n; ++j) {
+                        const uint32_t dt = tmem_base + (2 * tb + j) * FT;
+                        const uint64_t wd = smem_desc_sw128(smem_u32(s.w[stage][j]));
+                        const uint64_t xd = smem_desc_sw128(smem_u32(s.x[stage][it.down ? j : 0]));
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) tc_mma<FP8>(dt, wd + 2 * kk, xd + 2 * kk, idesc, kk != 0);
+                    }
+                    tc_commit(&s.empty[stage]);
+                    tc_commit(&s.tfull[tb]);
+                    if (++tb == NBUF) {
+                        tb = 0;
+                        tphase ^= 1;
+                    }
+                    if (++stage == FEW_STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            tc_commit(&s.mma_done);
+            const long long t0 = clock64();
+            while (!mbar_try_wait(&s.mma_done, 0)) {
+                if (clock64() - t0 > kWaitBudgetCycles) {
+                    set_status(p.status, MOE_ERR_TIMEOUT);
+                    break;
+                }
+            }
+        }
+    } else if (warp == 2) {
+        // --------------------------------------------------------- scales
+        // lanes 0-3: the first tile's token scales (16 bytes each), 4-7 the
+        // second's, 8 and 9 the tiles' weight scales.  The token scales bypass
+        // L1 (other CTAs wrote them during this launch).
+        if constexpr (FP8) {
+            int slot = 0, i = cta;
+            uint32_t phase = 0;
+            bool ok = true, routed = false;
+            Item it;
+            while (ok) {
+                const bool more = next_item(i, routed, it);
+                if (!__all_sync(0xffffffffu, more)) break;
+                if (it.down && !__all_sync(0xffffffffu, wait_count(&p.ctr->h_done[it.pos], nf, p, abort))) break;
+                for (int q = 0; q < it.stages; ++q) {
+                    if (!__all_sync(0xffffffffu, wait_bar(&s.sempty[slot], phase ^ 1, p, abort))) {
+                        ok = false;
+                        break;
+                    }
+                    const int n = it.down ? min(2, KB2 - 2 * q) : 2;
+                    if (lane < 8) {
+                        const int j = lane >> 2;
+                        const float *src = it.down ? p.hs + (static_cast<size_t>(it.pos) * KB2 + min(2 * q + j, KB2 - 1)) * FT
+                                                   : p.xs + q * FT;
+                        cp_async16(&s.sc[slot].x[j][4 * (lane & 3)], src + 4 * (lane & 3), true);
+                    } else if (lane < 8 + n) {
+                        const int j = lane - 8;
+                        const float *src = it.down
+                            ? p.w2_scales + (static_cast<size_t>(it.expert) * nd + it.blk) * KB2 + 2 * q + j
+                            : p.w13_scales + (static_cast<size_t>(it.expert) * 2 * nf + j * nf + it.blk) * KB1 + q;
+                        cp_async4(&s.sc[slot].w[j], src, true);
+                    }
+                    cp_async_mbar_arrive(&s.sfull[slot]);
+                    if (++slot == SC_RING) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            cp_async_wait_all();
+        }
+    } else if (warp >= 4 && warp < 8) {
+        // ------------------------------------------------------- epilogue
+        const int q4 = warp & 3, r = q4 * 32 + lane, etid = tid - 128;
+        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q4 * 32) << 16);
+        int tb = 0, slot = 0, i = cta;
+        uint32_t tphase = 0, sphase = 0;
+        bool ok = true, routed = false;
+        Item it;
+        // the four warps agree on every step that has a barrier of theirs
+        auto all_ok = [&](bool mine) {
+            int all;
+            __syncwarp();
+            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
+                         "bar.red.and.pred q, 1, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+                         : "=r"(all) : "r"(mine ? 1 : 0) : "memory");
+            return all != 0;
+        };
+        while (true) {
+            if (!all_ok(next_item(i, routed, it))) break;
+            float acc0[FT], acc1[FT];
+#pragma unroll
+            for (int t = 0; t < FT; ++t) acc0[t] = acc1[t] = 0.0f;
+            for (int q = 0; q < it.stages; ++q) {
+                bool go = true;
+                if constexpr (FP8) go = wait_bar(&s.sfull[slot], sphase, p, abort);
+                go = go && wait_bar(&s.tfull[tb], tphase, p, abort);
+                if (!__all_sync(0xffffffffu, go)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const bool both = !it.down || 2 * q + 1 < KB2;
+                float v[32];
+                tmem_ld32(lane_base + 2 * tb * FT, v);
+                tmem_wait_ld(v);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.tempty[tb]);
+                if constexpr (FP8) {
+                    const auto &sc = s.sc[slot];
+                    const float w0 = sc.w[0], w1 = sc.w[1];
+#pragma unroll
+                    for (int t = 0; t < FT; t += 4) {
+                        const float4 x0 = *reinterpret_cast<const float4 *>(&sc.x[0][t]);
+                        acc0[t] = __fmaf_rn(v[t], __fmul_rn(x0.x, w0), acc0[t]);
+                        acc0[t + 1] = __fmaf_rn(v[t + 1], __fmul_rn(x0.y, w0), acc0[t + 1]);
+                        acc0[t + 2] = __fmaf_rn(v[t + 2], __fmul_rn(x0.z, w0), acc0[t + 2]);
+                        acc0[t + 3] = __fmaf_rn(v[t + 3], __fmul_rn(x0.w, w0), acc0[t + 3]);
+                        if (both) {
+                            const float4 x1 = *reinterpret_cast<const float4 *>(&sc.x[1][t]);
+                            acc1[t] = __fmaf_rn(v[FT + t], __fmul_rn(x1.x, w1), acc1[t]);
+                            acc1[t + 1] = __fmaf_rn(v[FT + t + 1], __fmul_rn(x1.y, w1), acc1[t + 1]);
+                            acc1[t + 2] = __fmaf_rn(v[FT + t + 2], __fmul_rn(x1.z, w1), acc1[t + 2]);
+                            acc1[t + 3] = __fmaf_rn(v[FT + t + 3], __fmul_rn(x1.w, w1), acc1[t + 3]);
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.sempty[slot]);
+                    if (++slot == SC_RING) {
+                        slot = 0;
+                        sphase ^= 1;
+                    }
+                } else {
+#pragma unroll
+                    for (int t = 0; t < FT; ++t) {
+                        acc0[t] = __fadd_rn(acc0[t], v[t]);
+                        if (both) acc1[t] = __fadd_rn(acc1[t], v[FT + t]);
+                    }
+                }
+                if (++tb == NBUF) {
+                    tb = 0;
+                    tphase ^= 1;
+                }
+            }
+            if (!all_ok(ok)) break;
+            if (!it.down) {
+                // H = silu(G) U of feature blk*128 + r, every token; then its
+                // 1x128 tile's codes (the tile is this CTA's 128 rows)
+                float h[FT];
+#pragma unroll
+                for (int t = 0; t < FT; ++t) h[t] = __fdividef(acc0[t], 1.0f + __expf(-acc0[t])) * acc1[t];
+                const size_t row = static_cast<size_t>(it.pos) * FT;
+                if constexpr (FP8) {
+#pragma unroll
+                    for (int t = 0; t < FT; ++t) {
+                        float m = fabsf(h[t]);
+#pragma unroll
+                        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+                        if (lane == 0) s.amax[q4][t] = m;
+                    }
+                    named_bar_sync(1, 128);
+#pragma unroll
+                    for (int t = 0; t < FT; ++t) {
+                        if (t >= T) break;
+                        const float m = fmaxf(fmaxf(s.amax[0][t], s.amax[1][t]), fmaxf(s.amax[2][t], s.amax[3][t]));
+                        float inv;
+                        const float sc = tile_scale(m, p.ue, &inv);
+                        static_cast<uint8_t *>(p.h)[(row + t) * de + it.blk * 128 + r] =
+                            static_cast<uint8_t>(e4m3x2(__fmul_rn(h[t], inv), 0.0f));
+                        if (r == 0) p.hs[(static_cast<size_t>(it.pos) * KB2 + it.blk) * FT + t] = sc;
+                    }
+                } else {
+#pragma unroll
+                    for (int t = 0; t < FT; ++t)
+                        if (t < T)
+                            static_cast<__nv_bfloat16 *>(p.h)[(row + t) * de + it.blk * 128 + r] = __float2bfloat16_rn(h[t]);
+                }
+                fence_proxy_async_global();  // H is read by TMA
+                __threadfence();
+                named_bar_sync(1, 128);
+                if (etid == 0) red_release(&p.ctr->h_done[it.pos], 1);
+                continue;
+            }
+            // Y rows of the tokens that chose this expert (binary32: few rows)
+            const int kk = k + p.n_shared;
+            if (etid < FT) {
+                int rank = -1;
+                if (it.expert == E) rank = k;
+                else if (etid < T)
+                    for (int j = k - 1; j >= 0; --j)
+                        if (s.sel[etid][j] == it.expert) rank = j;
+                s.rank[etid] = static_cast<int8_t>(rank);
+            }
+            named_bar_sync(1, 128);
+#pragma unroll
+            for (int t = 0; t < FT; ++t) {
+                if (t >= T) break;
+                const int j = s.rank[t];
+                if (j >= 0) p.y[(static_cast<size_t>(t) * kk + j) * d + it.blk * 128 + r] = __fadd_rn(acc0[t], acc1[t]);
+            }
+            __threadfence();
+            named_bar_sync(1, 128);
+            if (etid == 0) s.last = add_acq_rel(&p.ctr->col_done[it.blk], 1) == s.n_used - 1;
+            named_bar_sync(1, 128);
+            if (!s.last) continue;
+            // combine of 128 columns: out = sum_j g_j Y_j (rank order) + shared
+            // (+ h); warp q4 takes tokens q4, q4 + 4, ..., lane l columns 4l ..
+            __threadfence();
+            for (int t = q4; t < T; t += 4) {
+                const int c = it.blk * 128 + lane * 4;
+                const float4 *yr = reinterpret_cast<const float4 *>(p.y + static_cast<size_t>(t) * kk * d + c);
+                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int j0 = 0; j0 < kk; j0 += 9) {
+                    float4 v[9];
+#pragma unroll
+                    for (int j = 0; j < 9; ++j)
+                        if (j0 + j < kk) v[j] = __ldcg(yr + static_cast<size_t>(j0 + j) * (d / 4));
+#pragma unroll
+                    for (int j = 0; j < 9; ++j) {
+                        if (j0 + j >= kk) break;
+                        const float g = j0 + j < k ? s.gate[t][j0 + j] : 1.0f;
+                        acc.x = __fmaf_rn(g, v[j].x, acc.x);
+                        acc.y = __fmaf_rn(g, v[j].y, acc.y);
+                        acc.z = __fmaf_rn(g, v[j].z, acc.z);
+                        acc.w = __fmaf_rn(g, v[j].w, acc.w);
+                    }
+                }
+                const size_t at = static_cast<size_t>(t) * d + c;
+                if (p.pn.gamma) {
+                    const uint2 res = *reinterpret_cast<const uint2 *>(p.x + at);
+                    acc.x = __fadd_rn(acc.x, bf16_lo(res.x));
+                    acc.y = __fadd_rn(acc.y, bf16_hi(res.x));
+                    acc.z = __fadd_rn(acc.z, bf16_lo(res.y));
+                    acc.w = __fadd_rn(acc.w, bf16_hi(res.y));
+                }
+                *reinterpret_cast<uint2 *>(p.out + at) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+            }
+        }
+    } else if (warp >= 8 && ready) {
+        // -------------------------------------------------- exact routing
+        // One lane a (token, expert) logit: sequential fused multiply-adds over
+        // d, operands eight 16-byte vectors ahead.
+        const int rt = tid - 256, rw = warp - 8;
+        const uint16_t *x = p.pn.gamma ? p.xn : p.x;
+        const int ne = E > cta ? (E - 1 - cta) / G + 1 : 0;
+        for (int i = rt; i < ne * T; i += ROUTE_THREADS) {
+            const int e = cta + i / T * G, t = i % T;
+            const uint4 *wr = reinterpret_cast<const uint4 *>(p.w_router + static_cast<size_t>(e) * d);
+            const uint4 *xr = reinterpret_cast<const uint4 *>(x + static_cast<size_t>(t) * d);
+            constexpr int AHEAD = 8;  // d is a multiple of 256: d / 8 of 32
+            uint4 a[AHEAD], b[AHEAD];
+#pragma unroll
+            for (int v = 0; v < AHEAD; ++v) {
+                a[v] = __ldg(wr + v);
+                b[v] = __ldcg(xr + v);
+            }
+            float l = 0.0f;
+            for (int v0 = 0; v0 < d / 8; v0 += AHEAD) {
+#pragma unroll
+                for (int v = 0; v < AHEAD; ++v) {
+                    const uint4 av = a[v], bv = b[v];
+                    if (v0 + AHEAD < d / 8) {
+                        a[v] = __ldg(wr + v0 + AHEAD + v);
+                        b[v] = __ldcg(xr + v0 + AHEAD + v);
+                    }
+                    l = __fmaf_rn(bf16_lo(bv.x), bf16_lo(av.x), l);
+                    l = __fmaf_rn(bf16_hi(bv.x), bf16_hi(av.x), l);
+                    l = __fmaf_rn(bf16_lo(bv.y), bf16_lo(av.y), l);
+                    l = __fmaf_rn(bf16_hi(bv.y), bf16_hi(av.y), l);
+                    l = __fmaf_rn(bf16_lo(bv.z), bf16_lo(av.z), l);
+                    l = __fmaf_rn(bf16_hi(bv.z), bf16_hi(av.z), l);
+                    l = __fmaf_rn(bf16_lo(bv.w), bf16_lo(av.w), l);
+                    l = __fmaf_rn(bf16_hi(bv.w), bf16_hi(av.w), l);
+                }
+            }
+            p.scores[static_cast<size_t>(t) * E + e] = sigmoid_cw(l, exp_consts());
+        }
+        __threadfence();
+        named_bar_sync(2, ROUTE_THREADS);
+        if (rt == 0) {
+            red_release(&p.ctr->scored, 1);
+            wait_count(&p.ctr->scored, G, p, abort);
+        }
+        named_bar_sync(2, ROUTE_THREADS);
+        if (!*abort) {
+            for (int t = rw; t < T; t += 4) {
+                int e;
+                float sc;
+                topk_any(p.scores + static_cast<size_t>(t) * E, p.bias, E, k, lane, e, sc);
+                const float g = warp_gate(sc, k, p.routed_scale);
+                if (lane < k) {
+                    s.sel[t][lane] = static_cast<int16_t>(e);
+                    s.gate[t][lane] = g;
+                    atomicOr(&s.exact_set[e >> 5], 1u << (e & 31));
+                    if (cta == 0) {
+                        p.idx_out[static_cast<size_t>(t) * k + lane] = e;
+                        p.gates_out[static_cast<size_t>(t) * k + lane] = g;
+                    }
+                }
+            }
+        }
+        named_bar_sync(2, ROUTE_THREADS);
+        if (rw == 0 && !*abort) {
+            const int n = append_set(s.exact_set, s.rough_set, s.list, s.n_rough, lane);
+            __syncwarp();
+            // positions of the selected experts, in list order
+            int n_used = 0;
+            for (int j0 = 0; j0 < n; j0 += 32) {
+                const int j = j0 + lane;
+                const int e = j < n ? s.list[j] : 0;
+                const bool use = j < n && (e == E || (s.exact_set[e >> 5] >> (e & 31) & 1));
+                const uint32_t m = __ballot_sync(0xffffffffu, use);
+                if (use) s.used[n_used + __popc(m & ((1u << lane) - 1))] = static_cast<uint16_t>(j);
+                n_used += __popc(m);
+            }
+            __syncwarp();
+            if (lane == 0) {
+                s.n_list = n;
+                s.n_used = n_used;
+                mbar_arrive(&s.routed);
+            }
+        }
+    }
+
+    // ------------------------------------------------------------- teardown
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, TMEM_COLS);
+    }
+    if (tid == 0) s.last = add_acq_rel(&p.ctr->exited, 1) == G - 1;
+    __syncthreads();
+    if (s.last) {  // nobody waits any more: every counter back to zero
+        int *c = reinterpret_cast<int *>(p.ctr);
+        for (int j = tid; j < static_cast<int>(sizeof(FewCounters) / sizeof(int)); j += FEW_THREADS) c[j] = 0;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_few(const FewArgs &g, cudaStream_t st, int *launches) {
+    const moe_shape &s = *g.shape;
+    const bool fp8 = s.precision != MOE_BF16;
+    const int slots = s.n_experts + s.n_shared;
+    const int es = fp8 ? 1 : 2;
+    const bool rm = s.weight_layout == MOE_LAYOUT_ROWMAJOR;
+    CUtensorMap mx, m13, mh, m2;
+    const long long rows13 = static_cast<long long>(slots) * 2 * s.d_expert, rows2 = static_cast<long long>(slots) * s.d_model;
+    const long long t13 = rm ? rows13 : rows13 * s.d_model * es / 128, t2 = rm ? rows2 : rows2 * s.d_expert * es / 128;
+    if (t13 >= (1LL << 31) || t2 >= (1LL << 31)) return cudaErrorInvalidValue;
+    const int per = 128 / es;
+    const void *xop = fp8 ? static_cast<const void *>(g.xq) : (g.pn.gamma ? g.xn : g.x);
+    if (!make_map_2d(&mx, xop, fp8, s.d_model, s.T, FT) ||
+        !make_map_2d(&mh, g.h, fp8, s.d_expert, g.list_rows * FT, FT) ||
+        !make_map_2d(&m13, g.w13, fp8, rm ? s.d_model : per, static_cast<int>(t13)) ||
+        !make_map_2d(&m2, g.w2, fp8, rm ? s.d_expert : per, static_cast<int>(t2)))
+        return cudaErrorInvalidValue;
+    FewParams p{};
+    p.x = g.x;
+    p.pn = g.pn;
+    p.w_router = g.w_router;
+    p.bias = g.bias;
+    p.w13_scales = g.w13_scales;
+    p.w2_scales = g.w2_scales;
+    p.out = g.out;
+    p.idx_out = g.idx;
+    p.gates_out = g.gates;
+    p.xq = g.xq;
+    p.xs = g.xs;
+    p.xn = g.xn;
+    p.rough = g.rough;
+    p.scores = g.scores;
+    p.h = g.h;
+    p.hs = g.hs;
+    p.y = g.y;
+    p.ctr = g.counters;
+    p.status = g.status;
+    p.T = s.T;
+    p.d = s.d_model;
+    p.E = s.n_experts;
+    p.k = s.top_k;
+    p.de = s.d_expert;
+    p.n_shared = s.n_shared;
+    p.routed_scale = s.routed_scale;
+    p.ue = s.precision == MOE_FP8_UE8M0;
+    p.w_rowmajor = rm;
+    const size_t smem = sizeof(FewSmem) + 1024;
+    static DeviceConfigured configured{};
+    if (first_use_on_device(configured)) {
+        cudaError_t e = cudaFuncSetAttribute(moe_few_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(moe_few_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+        mark_used_on_device(configured);
+    }
+    mark_launch(st, *launches, "moe_few");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_sms());
+    cfg.blockDim = dim3(FEW_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;  // CTAs wait for one another: all resident, or no launch
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    LAUNCH_OR_RETURN(fp8 ? cudaLaunchKernelEx(&cfg, moe_few_kernel<true>, mx, m13, mh, m2, p)
+                         : cudaLaunchKernelEx(&cfg, moe_few_kernel<false>, mx, m13, mh, m2, p));
+    ++*launches;
+    return cudaGetLastError();
+}
+
+}  // namespace moe

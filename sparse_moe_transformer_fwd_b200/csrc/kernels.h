@@ -165,6 +165,41 @@ cudaError_t launch_splitk_reduce(const float *partial, int ksplit, int rows, int
                                  int *launches);
 cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launches);
 
+// The whole MoE layer for at most kFewTokens tokens (few.cu).
+constexpr int kFewTokens = MOE_FEW_MAX_TOKENS;
+constexpr int kFewMaxList = 1025;  // experts worked on: n_experts + n_shared at most
+constexpr int kFewMaxCols = 1024;  // 128-column blocks of d_model
+// Counters of one launch: zero before it, and left zero.
+struct FewCounters {
+    int prepared, scored, exited, abort;
+    int pad[60];
+    int h_done[kFewMaxList + 63];  // [list position] gate/up items done
+    int col_done[kFewMaxCols];     // [128-column block] experts' down items done
+};
+struct FewArgs {
+    const moe_shape *shape;
+    const uint16_t *x;
+    PreNorm pn;
+    const uint16_t *w_router;
+    const float *bias;
+    const void *w13, *w2;
+    const float *w13_scales, *w2_scales;
+    uint16_t *out;
+    int32_t *idx;           // [T, k]
+    float *gates;           // [T, k]
+    float *rough, *scores;  // [T, E]
+    uint8_t *xq;            // [T, d] (fp8)
+    float *xs;              // [d/128][kFewTokens] (fp8)
+    uint16_t *xn;           // [T, d] (pre-norm)
+    void *h;                // [list_rows][kFewTokens][de] e4m3 or bf16
+    float *hs;              // [list_rows][de/128][kFewTokens] (fp8)
+    float *y;               // [T][k + n_shared][d]
+    int list_rows;
+    FewCounters *counters;
+    int *status;
+};
+cudaError_t launch_few(const FewArgs &g, cudaStream_t st, int *launches);
+
 // Block-scaled product of at most kLinearStreamRows rows of codes (linear.cu).
 constexpr int kLinearStreamRows = 64;
 constexpr int kLinearMaxCtas = 160;  // CTAs of linear_stream (sizes its partial sums)

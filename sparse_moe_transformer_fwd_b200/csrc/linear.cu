@@ -27,49 +27,12 @@
 // drains its loads and MMAs, frees its TMEM and exits.
 #include "common.cuh"
 #include "kernels.h"
+#include "quant_math.cuh"
 
 #include <algorithm>
 
 namespace moe {
 namespace {
-
-// Eight consecutive columns c .. c + 7 of token t: bf16 inputs, or the pre-norm
-// of the residual stream.
-__device__ __forceinline__ void load_x8(const uint16_t *x, int t, int c, int K, const PreNorm &pn, float (&v)[8]) {
-    const uint4 raw = *reinterpret_cast<const uint4 *>(x + static_cast<size_t>(t) * K + c);
-    const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16_lo(r[i]);
-        v[2 * i + 1] = bf16_hi(r[i]);
-    }
-    if (!pn.gamma) return;
-    const float rs = pn.rstd[t];
-    const uint4 graw = *reinterpret_cast<const uint4 *>(pn.gamma + c);
-    const uint32_t g[4] = {graw.x, graw.y, graw.z, graw.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = prenorm_elem(v[2 * i], rs, bf16_lo(g[i]));
-        v[2 * i + 1] = prenorm_elem(v[2 * i + 1], rs, bf16_hi(g[i]));
-    }
-}
-
-// A 1x128 tile held by 16 lanes, 8 values each: this lane's codes, and the
-// tile's scale.
-__device__ __forceinline__ float quant_tile8(const float (&v)[8], bool ue, uint2 *code) {
-    float m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
-#pragma unroll
-    for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    float inv;
-    const float sc = tile_scale(m, ue, &inv);
-    uint32_t c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = e4m3x2(__fmul_rn(v[2 * i], inv), __fmul_rn(v[2 * i + 1], inv));
-    *code = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-    return sc;
-}
 
 constexpr int LS_THREADS = 256;
 constexpr int W_BYTES = 128 * 128;  // one tile of weights

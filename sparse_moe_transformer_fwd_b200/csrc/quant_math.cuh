@@ -1,0 +1,68 @@
+// Quantisation of activations by the kernels that read them (linear.cu,
+// few.cu): the input vector, pre-normed or not, and its 1x128 tile's codes and
+// scale ("DeepSeek-R1" (aguasto.com), "Quantization": blockwise FP8).
+#pragma once
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+// Scale and factor of a 1x128 activation tile in the calls that quantise on
+// the way to a product (moe_linear, moe_forward_few): scale = amax * (1/448)
+// and *inv = 448 * (1/amax), each operation a correctly rounded binary32 one.
+// One reciprocal serves both where fp8_block_quant divides twice (a tile is
+// quantised again by every CTA that reads it); either value is within an ulp
+// of the quotient, so only an element at a border of two codes can differ.
+// The factor of a tile below 448 / FLT_MAX is held at FLT_MAX (no code is NaN
+// for 0 * inf); an all-zero tile gets scale 1 and factor 0; ue: power-of-two
+// scale (ue8m0_scale).
+__device__ __forceinline__ float tile_scale(float amax, bool ue, float *inv) {
+    if (amax == 0.0f) {
+        *inv = 0.0f;
+        return 1.0f;
+    }
+    if (ue) return ue8m0_scale(amax, inv);
+    *inv = fminf(__fmul_rn(__frcp_rn(amax), 448.0f), 3.402823466e38f);
+    return __fmul_rn(amax, static_cast<float>(1.0 / 448.0));
+}
+
+// Eight consecutive columns c .. c + 7 of token t: bf16 inputs, or the pre-norm
+// of the residual stream.
+__device__ __forceinline__ void load_x8(const uint16_t *x, int t, int c, int K, const PreNorm &pn, float (&v)[8]) {
+    const uint4 raw = *reinterpret_cast<const uint4 *>(x + static_cast<size_t>(t) * K + c);
+    const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(r[i]);
+        v[2 * i + 1] = bf16_hi(r[i]);
+    }
+    if (!pn.gamma) return;
+    const float rs = pn.rstd[t];
+    const uint4 graw = *reinterpret_cast<const uint4 *>(pn.gamma + c);
+    const uint32_t g[4] = {graw.x, graw.y, graw.z, graw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = prenorm_elem(v[2 * i], rs, bf16_lo(g[i]));
+        v[2 * i + 1] = prenorm_elem(v[2 * i + 1], rs, bf16_hi(g[i]));
+    }
+}
+
+// A 1x128 tile held by 16 lanes, 8 values each: this lane's codes, and the
+// tile's scale.
+__device__ __forceinline__ float quant_tile8(const float (&v)[8], bool ue, uint2 *code) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    float inv;
+    const float sc = tile_scale(m, ue, &inv);
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = e4m3x2(__fmul_rn(v[2 * i], inv), __fmul_rn(v[2 * i + 1], inv));
+    *code = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+    return sc;
+}
+
+}  // namespace moe
