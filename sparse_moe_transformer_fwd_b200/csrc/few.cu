@@ -51,7 +51,7 @@ namespace {
 
 constexpr int FT = kFewTokens;  // MMA columns
 constexpr int FEW_THREADS = 384;
-constexpr int FEW_STAGES = 6;
+constexpr int FEW_STAGES = 5;
 constexpr int W_BYTES = 128 * 128;
 constexpr int X_BYTES = FT * 128;
 constexpr int NBUF = 4;
@@ -59,6 +59,10 @@ constexpr int SC_RING = 8;
 constexpr int TMEM_COLS = NBUF * 2 * FT;
 constexpr int ROUTE_THREADS = 128;
 constexpr int MAX_K = 32;
+// Exact logits: chunks of RC columns of the router rows and tokens of one pass
+// (RC_ROWS in all) in a ring of RC_BUFS in shared memory; rows are padded by 16
+// bytes, so that lanes on different rows read different banks.
+constexpr int RC = 128, RC_ROWS = 18, RC_BUFS = 7, RC_LD = RC + 8;
 static_assert(FT == 16, "a stage's two accumulators are one 32-column TMEM load");
 
 struct FewSmem {
@@ -69,7 +73,11 @@ struct FewSmem {
         float w[2];
         float pad[2];
     } sc[SC_RING];
-    float amax[4][FT];
+    alignas(16) uint16_t chunk[RC_BUFS][RC_ROWS][RC_LD];
+    union {
+        float amax[4][FT];
+        float part[FEW_THREADS / 32][8];  // rough logits of one pass
+    };
     float gate[FT][MAX_K];
     int16_t sel[FT][MAX_K];        // exact selection
     uint16_t list[kFewMaxList];    // experts worked on: shared, predicted, missed
@@ -93,6 +101,7 @@ struct FewParams {
     PreNorm pn;
     const uint16_t *w_router;
     const float *bias;
+    const uint8_t *w13, *w2;
     const float *w13_scales, *w2_scales;
     uint16_t *out;
     int32_t *idx_out;        // [T, k]
@@ -165,9 +174,51 @@ struct Item {
     int stages;
 };
 
+// Top-k of one token's affinities by one warp, as warp_topk selects (s + bias
+// descending, lowest expert first; the affinities are positive, so the sums
+// order as integers once negative ones are turned over): k rounds of two warp
+// reductions.  0.5 us at 256 experts, k = 8, against 2 us for the shuffles.
+template <int PER_LANE>
+__device__ __forceinline__ void topk_keys(const float *row, const float *bias, int E, int k, int lane, int &my_e,
+                                          float &my_s) {
+    float s[PER_LANE];
+    uint32_t key[PER_LANE];
+#pragma unroll
+    for (int m = 0; m < PER_LANE; ++m) {
+        const int e = lane + 32 * m;
+        s[m] = e < E ? __ldcg(row + e) : 0.0f;
+        key[m] = e < E ? __float_as_uint(__ldg(bias + e)) : 0u;
+    }
+#pragma unroll
+    for (int m = 0; m < PER_LANE; ++m) {
+        const uint32_t b = __float_as_uint(__fadd_rn(s[m], __uint_as_float(key[m])));
+        // 0: taken or none; a real key is at least 1
+        key[m] = lane + 32 * m < E ? max(b >> 31 ? ~b : b | 0x80000000u, 1u) : 0u;
+    }
+    my_e = 0;
+    my_s = 0.0f;
+    for (int j = 0; j < k; ++j) {
+        uint32_t best = 0;
+        int at = 0;
+        float bs = 0.0f;
+#pragma unroll
+        for (int m = 0; m < PER_LANE; ++m)
+            if (key[m] > best) best = key[m], at = m, bs = s[m];
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        const uint32_t e = __reduce_min_sync(0xffffffffu, best == top ? static_cast<uint32_t>(lane + 32 * at) : 0xffffffffu);
+        const float es = __shfl_sync(0xffffffffu, bs, e & 31);
+#pragma unroll
+        for (int m = 0; m < PER_LANE; ++m)
+            if (static_cast<uint32_t>(lane + 32 * m) == e) key[m] = 0;
+        if (lane == j) {
+            my_e = static_cast<int>(e);
+            my_s = es;
+        }
+    }
+}
 __device__ __forceinline__ void topk_any(const float *row, const float *bias, int E, int k, int lane, int &e, float &s) {
-    if (E <= 256) warp_topk<8>(row, bias, E, k, lane, e, s);
-    else warp_topk<kMaxPerLane>(row, bias, E, k, lane, e, s);
+    if (E <= 256) topk_keys<8>(row, bias, E, k, lane, e, s);
+    else topk_keys<kMaxPerLane>(row, bias, E, k, lane, e, s);
 }
 
 // One warp appends the set bits of `set` that `without` lacks, in ascending
@@ -253,31 +304,80 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
             }
         }
     }
-    // rough logits of experts cta, cta + G, ...: one warp a (token, expert) pair
+    // rough logits of experts cta, cta + G, ...: every thread a few columns of
+    // two experts and four tokens a pass, so that all of a pass's loads are in
+    // flight together (one warp a logit took 5 us at d = 7168, one token)
     {
         const int ne = E > cta ? (E - 1 - cta) / G + 1 : 0;
-        for (int i = warp; i < ne * T; i += FEW_THREADS / 32) {
-            const int e = cta + i / T * G, t = i % T;
-            const uint4 *wr = reinterpret_cast<const uint4 *>(p.w_router + static_cast<size_t>(e) * d);
-            const uint4 *xr = reinterpret_cast<const uint4 *>(p.x + static_cast<size_t>(t) * d);
-            float a0 = 0.0f, a1 = 0.0f;
-#pragma unroll 4
-            for (int v = lane; v < d / 8; v += 32) {
-                const uint4 a = wr[v], b = x_vec(xr[v], p.pn, t, v * 8);
-                a0 = fmaf(bf16_lo(a.x), bf16_lo(b.x), a0);
-                a1 = fmaf(bf16_hi(a.x), bf16_hi(b.x), a1);
-                a0 = fmaf(bf16_lo(a.y), bf16_lo(b.y), a0);
-                a1 = fmaf(bf16_hi(a.y), bf16_hi(b.y), a1);
-                a0 = fmaf(bf16_lo(a.z), bf16_lo(b.z), a0);
-                a1 = fmaf(bf16_hi(a.z), bf16_hi(b.z), a1);
-                a0 = fmaf(bf16_lo(a.w), bf16_lo(b.w), a0);
-                a1 = fmaf(bf16_hi(a.w), bf16_hi(b.w), a1);
-            }
-            a0 += a1;
+        for (int e0 = 0; e0 < ne; e0 += 2)
+            for (int t0 = 0; t0 < T; t0 += 4) {
+                const uint4 *wr[2], *xr[4];
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) a0 += __shfl_xor_sync(0xffffffffu, a0, off);
-            if (lane == 0) p.rough[static_cast<size_t>(t) * E + e] = sigmoid_cw(a0, exp_consts());
-        }
+                for (int i = 0; i < 2; ++i)
+                    wr[i] = reinterpret_cast<const uint4 *>(p.w_router + static_cast<size_t>(cta + min(e0 + i, ne - 1) * G) * d);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    xr[i] = reinterpret_cast<const uint4 *>(p.x + static_cast<size_t>(min(t0 + i, T - 1)) * d);
+                float acc[2][4] = {};
+                for (int v0 = tid; v0 < d / 8; v0 += 3 * FEW_THREADS) {
+                    uint4 a[3][2], b[3][4];
+#pragma unroll
+                    for (int c = 0; c < 3; ++c) {
+                        const int v = v0 + c * FEW_THREADS;
+                        const bool in = v < d / 8;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) a[c][i] = in ? __ldg(wr[i] + v) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) b[c][i] = in && t0 + i < T ? __ldg(xr[i] + v) : make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 3; ++c) {
+                        const int v = min(v0 + c * FEW_THREADS, d / 8 - 1);  // past the end: zeros
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (t0 + i >= T) break;
+                            const uint4 xv = x_vec(b[c][i], p.pn, t0 + i, v * 8);
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                acc[j][i] = fmaf(bf16_lo(a[c][j].x), bf16_lo(xv.x), acc[j][i]);
+                                acc[j][i] = fmaf(bf16_hi(a[c][j].x), bf16_hi(xv.x), acc[j][i]);
+                                acc[j][i] = fmaf(bf16_lo(a[c][j].y), bf16_lo(xv.y), acc[j][i]);
+                                acc[j][i] = fmaf(bf16_hi(a[c][j].y), bf16_hi(xv.y), acc[j][i]);
+                                acc[j][i] = fmaf(bf16_lo(a[c][j].z), bf16_lo(xv.z), acc[j][i]);
+                                acc[j][i] = fmaf(bf16_hi(a[c][j].z), bf16_hi(xv.z), acc[j][i]);
+                                acc[j][i] = fmaf(bf16_lo(a[c][j].w), bf16_lo(xv.w), acc[j][i]);
+                                acc[j][i] = fmaf(bf16_hi(a[c][j].w), bf16_hi(xv.w), acc[j][i]);
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float v = acc[i >> 2][i & 3];
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+                    if (lane == 0) s.part[warp][i] = v;
+                }
+                __syncthreads();
+                if (tid < 8 && e0 + (tid >> 2) < ne && t0 + (tid & 3) < T) {
+                    float l = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < FEW_THREADS / 32; ++w) l += s.part[w][tid];
+                    p.rough[static_cast<size_t>(t0 + (tid & 3)) * E + cta + (e0 + (tid >> 2)) * G] =
+                        __fdividef(1.0f, 1.0f + __expf(-l));
+                }
+                __syncthreads();
+            }
+    }
+    // The shared expert's weights are needed whatever the routing: into L2 while
+    // it is found (behind the router's own loads, which they would hold up: the
+    // rough logits took 6.4 us, not 1.2).
+    if (tid == 32 && p.n_shared) {
+        const size_t es = FP8 ? 1 : 2, b13 = static_cast<size_t>(2) * de * d * es, b2 = static_cast<size_t>(d) * de * es;
+        for (size_t o = static_cast<size_t>(cta) * W_BYTES; o < b13; o += static_cast<size_t>(G) * W_BYTES)
+            l2_prefetch(p.w13 + E * b13 + o, static_cast<uint32_t>(min(b13 - o, static_cast<size_t>(W_BYTES))));
+        for (size_t o = static_cast<size_t>(cta) * W_BYTES; o < b2; o += static_cast<size_t>(G) * W_BYTES)
+            l2_prefetch(p.w2 + E * b2 + o, static_cast<uint32_t>(min(b2 - o, static_cast<size_t>(W_BYTES))));
     }
     fence_proxy_async_global();  // x is read by TMA
     __threadfence();
@@ -662,41 +762,69 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
     } else if (warp >= 8 && ready) {
         // -------------------------------------------------- exact routing
         // One lane a (token, expert) logit: sequential fused multiply-adds over
-        // d, operands eight 16-byte vectors ahead.
+        // d.  The operands come through a ring in shared memory: read straight
+        // from L2, under the load of the weight stream, they took 100 us at d =
+        // 7168 (a chain needs 15); and 45 us with the copies issued by the
+        // warp that runs the chains.
         const int rt = tid - 256, rw = warp - 8;
         const uint16_t *x = p.pn.gamma ? p.xn : p.x;
         const int ne = E > cta ? (E - 1 - cta) / G + 1 : 0;
-        for (int i = rt; i < ne * T; i += ROUTE_THREADS) {
-            const int e = cta + i / T * G, t = i % T;
-            const uint4 *wr = reinterpret_cast<const uint4 *>(p.w_router + static_cast<size_t>(e) * d);
-            const uint4 *xr = reinterpret_cast<const uint4 *>(x + static_cast<size_t>(t) * d);
-            constexpr int AHEAD = 8;  // d is a multiple of 256: d / 8 of 32
-            uint4 a[AHEAD], b[AHEAD];
+        const int per_pass = min(RC_ROWS - T, 32 / T);  // experts a pass: a warp's lanes
+        for (int e0 = 0; e0 < ne; e0 += per_pass) {
+            const int n = min(per_pass, ne - e0), rows = n + T;
+            auto load_chunk = [&](int c) {  // rows 0 .. n - 1: router, then the tokens
+                for (int v = rt - 32; v < rows * (RC / 8); v += ROUTE_THREADS - 32) {
+                    const int row = v / (RC / 8), col = v % (RC / 8) * 8;
+                    const uint16_t *src = row < n ? p.w_router + static_cast<size_t>(cta + (e0 + row) * G) * d
+                                                  : x + static_cast<size_t>(row - n) * d;
+                    cp_async16(&s.chunk[c % RC_BUFS][row][col], src + c * RC + col, true);
+                }
+            };
+            const int nc = d / RC;
+            if (rw > 0) {  // three warps copy, chunk after chunk
 #pragma unroll
-            for (int v = 0; v < AHEAD; ++v) {
-                a[v] = __ldg(wr + v);
-                b[v] = __ldcg(xr + v);
+                for (int c = 0; c < RC_BUFS - 1; ++c) {
+                    if (c < nc) load_chunk(c);
+                    cp_async_commit();
+                }
+                for (int c = 0; c < nc; ++c) {
+                    cp_async_wait<RC_BUFS - 2>();
+                    named_bar_sync(2, ROUTE_THREADS);  // chunk c landed; chunk c - 1 is done with
+                    if (c + RC_BUFS - 1 < nc) load_chunk(c + RC_BUFS - 1);
+                    cp_async_commit();
+                }
+                cp_async_wait<0>();
+                named_bar_sync(2, ROUTE_THREADS);  // the ring is free for the next pass
+                continue;
             }
+            const bool mine = lane < n * T;
+            const int t = mine ? lane % T : 0, ei = mine ? lane / T : 0;
             float l = 0.0f;
-            for (int v0 = 0; v0 < d / 8; v0 += AHEAD) {
+            for (int c = 0; c < nc; ++c) {
+                named_bar_sync(2, ROUTE_THREADS);
+                const uint4 *wr = reinterpret_cast<const uint4 *>(s.chunk[c % RC_BUFS][ei]);
+                const uint4 *xr = reinterpret_cast<const uint4 *>(s.chunk[c % RC_BUFS][n + t]);
+                // operands two vectors ahead of the chain (a 3-slot register ring)
+                constexpr int NV = RC / 8, PD = 2;
+                uint4 av[PD + 1], bv[PD + 1];
 #pragma unroll
-                for (int v = 0; v < AHEAD; ++v) {
-                    const uint4 av = a[v], bv = b[v];
-                    if (v0 + AHEAD < d / 8) {
-                        a[v] = __ldg(wr + v0 + AHEAD + v);
-                        b[v] = __ldcg(xr + v0 + AHEAD + v);
-                    }
-                    l = __fmaf_rn(bf16_lo(bv.x), bf16_lo(av.x), l);
-                    l = __fmaf_rn(bf16_hi(bv.x), bf16_hi(av.x), l);
-                    l = __fmaf_rn(bf16_lo(bv.y), bf16_lo(av.y), l);
-                    l = __fmaf_rn(bf16_hi(bv.y), bf16_hi(av.y), l);
-                    l = __fmaf_rn(bf16_lo(bv.z), bf16_lo(av.z), l);
-                    l = __fmaf_rn(bf16_hi(bv.z), bf16_hi(av.z), l);
-                    l = __fmaf_rn(bf16_lo(bv.w), bf16_lo(av.w), l);
-                    l = __fmaf_rn(bf16_hi(bv.w), bf16_hi(av.w), l);
+                for (int v = 0; v < PD; ++v) av[v] = wr[v], bv[v] = xr[v];
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    if (v + PD < NV) av[(v + PD) % (PD + 1)] = wr[v + PD], bv[(v + PD) % (PD + 1)] = xr[v + PD];
+                    const uint4 a = av[v % (PD + 1)], b = bv[v % (PD + 1)];
+                    l = __fmaf_rn(bf16_lo(b.x), bf16_lo(a.x), l);
+                    l = __fmaf_rn(bf16_hi(b.x), bf16_hi(a.x), l);
+                    l = __fmaf_rn(bf16_lo(b.y), bf16_lo(a.y), l);
+                    l = __fmaf_rn(bf16_hi(b.y), bf16_hi(a.y), l);
+                    l = __fmaf_rn(bf16_lo(b.z), bf16_lo(a.z), l);
+                    l = __fmaf_rn(bf16_hi(b.z), bf16_hi(a.z), l);
+                    l = __fmaf_rn(bf16_lo(b.w), bf16_lo(a.w), l);
+                    l = __fmaf_rn(bf16_hi(b.w), bf16_hi(a.w), l);
                 }
             }
-            p.scores[static_cast<size_t>(t) * E + e] = sigmoid_cw(l, exp_consts());
+            named_bar_sync(2, ROUTE_THREADS);
+            if (mine) p.scores[static_cast<size_t>(t) * E + cta + (e0 + ei) * G] = sigmoid_cw(l, exp_consts());
         }
         __threadfence();
         named_bar_sync(2, ROUTE_THREADS);
@@ -784,6 +912,8 @@ cudaError_t launch_few(const FewArgs &g, cudaStream_t st, int *launches) {
     p.pn = g.pn;
     p.w_router = g.w_router;
     p.bias = g.bias;
+    p.w13 = static_cast<const uint8_t *>(g.w13);
+    p.w2 = static_cast<const uint8_t *>(g.w2);
     p.w13_scales = g.w13_scales;
     p.w2_scales = g.w2_scales;
     p.out = g.out;
