@@ -446,7 +446,7 @@ int moe_forward_few(const moe_shape *shape, const uint16_t *x, const uint16_t *w
                     size_t ws_bytes, void *stream);
 
 /* The FFN block, as moe_forward_prenorm: out = h + MoE(x), x = bf16((h * rstd)
- * * gamma); the statistics are a launch of their own. */
+ * * gamma), which is a launch of its own. */
 int moe_forward_few_prenorm(const moe_shape *shape, const uint16_t *h, const uint16_t *gamma,
                             float eps, const uint16_t *w_router, const float *bias, const void *w13,
                             const float *w13_scales, const void *w2, const float *w2_scales,

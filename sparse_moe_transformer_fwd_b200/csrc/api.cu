@@ -1008,7 +1008,7 @@ namespace moe {
 namespace {
 
 struct FewLayout {
-    size_t status, counters, rstd, rough, scores, idx, gates, xq, xs, xn, h, hs, y, total;
+    size_t status, counters, rough, scores, idx, gates, xq, xs, xn, h, hs, y, total;
     int list_rows;
 };
 
@@ -1040,7 +1040,6 @@ FewLayout few_layout(const moe_shape *s) {
     };
     L.status = take(256);
     L.counters = take(sizeof(FewCounters));
-    L.rstd = take(T * 4);
     L.rough = take(T * E * 4);
     L.scores = take(T * E * 4);
     L.idx = take(T * k * 4);
@@ -1050,7 +1049,7 @@ FewLayout few_layout(const moe_shape *s) {
     L.xn = take(T * d * 2);
     L.h = take(static_cast<size_t>(L.list_rows) * kFewTokens * de * (fp8 ? 1 : 2));
     L.hs = take(fp8 ? L.list_rows * (de / 128) * kFewTokens * 4 : 0);
-    L.y = take(T * (k + s->n_shared) * d * 4);
+    L.y = take(3 * T * (k + s->n_shared) * d * 4);
     L.total = off;
     return L;
 }
@@ -1080,14 +1079,14 @@ int few_impl(const moe_shape *s, const uint16_t *x, const uint16_t *gamma, float
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     int n = 0;
     FewArgs g{};
-    if (gamma) {
-        float *rstd = at<float>(ws, L.rstd);
-        LAUNCH(launch_rstd(x, s->T, s->d_model, eps, rstd, st, &n), "pre-norm statistics");
-        g.pn.rstd = rstd;
-        g.pn.gamma = gamma;
-    }
     g.shape = s;
     g.x = x;
+    if (gamma) {
+        uint16_t *xn = at<uint16_t>(ws, L.xn);
+        LAUNCH(launch_few_prenorm(x, gamma, s->T, s->d_model, eps, xn, st, &n), "pre-norm");
+        g.x = xn;
+        g.residual = x;
+    }
     g.w_router = w_router;
     g.bias = bias;
     g.w13 = w13;
@@ -1101,7 +1100,6 @@ int few_impl(const moe_shape *s, const uint16_t *x, const uint16_t *gamma, float
     g.scores = at<float>(ws, L.scores);
     g.xq = at<uint8_t>(ws, L.xq);
     g.xs = at<float>(ws, L.xs);
-    g.xn = at<uint16_t>(ws, L.xn);
     g.h = at<uint8_t>(ws, L.h);
     g.hs = at<float>(ws, L.hs);
     g.y = at<float>(ws, L.y);

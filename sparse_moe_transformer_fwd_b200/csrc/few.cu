@@ -54,10 +54,11 @@ constexpr int FEW_THREADS = 384;
 constexpr int FEW_STAGES = 5;
 constexpr int W_BYTES = 128 * 128;
 constexpr int X_BYTES = FT * 128;
-constexpr int NBUF = 4;
 constexpr int SC_RING = 8;
-constexpr int TMEM_COLS = NBUF * 2 * FT;
-constexpr int ROUTE_THREADS = 128;
+constexpr int TMEM_COLS = 256;  // two accumulators of 16 columns a stage
+static_assert(FEW_STAGES * 2 * FT <= TMEM_COLS, "accumulators of the ring's stages");
+constexpr int MAIN_THREADS = 256;   // warps 0-7
+constexpr int ROUTE_THREADS = 128;  // warps 8-11
 constexpr int MAX_K = 32;
 // Exact logits: chunks of RC columns of the router rows and tokens of one pass
 // (RC_ROWS in all) in a ring of RC_BUFS in shared memory; rows are padded by 16
@@ -76,19 +77,19 @@ struct FewSmem {
     alignas(16) uint16_t chunk[RC_BUFS][RC_ROWS][RC_LD];
     union {
         float amax[4][FT];
-        float part[FEW_THREADS / 32][8];  // rough logits of one pass
+        float part[MAIN_THREADS / 32][8];  // rough logits of one pass
     };
     float gate[FT][MAX_K];
-    int16_t sel[FT][MAX_K];        // exact selection
+    uint16_t sel[FT][MAX_K];       // exact selection: its index in used
     uint16_t list[kFewMaxList];    // experts worked on: shared, predicted, missed
     uint16_t used[kFewMaxList];    // positions in list of the experts selected
     uint32_t rough_set[32], exact_set[32];
     int8_t rank[FT];
     int n_rough, n_list, n_used;
-    uint64_t full[FEW_STAGES], empty[FEW_STAGES];
+    uint64_t full[FEW_STAGES];  // operands landed, and the accumulators drained (4 warps)
+    uint64_t done[FEW_STAGES];  // MMAs done: accumulators to read, operands to overwrite
     uint64_t sfull[SC_RING], sempty[SC_RING];
-    uint64_t tfull[NBUF], tempty[NBUF];
-    uint64_t routed;
+    uint64_t selected, routed;  // the rough selection; the exact one
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort;
@@ -97,8 +98,8 @@ struct FewSmem {
 static_assert(sizeof(FewSmem) + 1024 <= 227 * 1024, "shared memory budget of one CTA");
 
 struct FewParams {
-    const uint16_t *x;       // [T, d] (the residual stream h behind the pre-norm)
-    PreNorm pn;
+    const uint16_t *x;         // [T, d]
+    const uint16_t *residual;  // [T, d] added to out, or NULL
     const uint16_t *w_router;
     const float *bias;
     const uint8_t *w13, *w2;
@@ -108,11 +109,10 @@ struct FewParams {
     float *gates_out;        // [T, k]
     uint8_t *xq;             // [T, d] codes (fp8)
     float *xs;               // [d/128][16]
-    uint16_t *xn;            // [T, d] pre-normed x
     float *rough, *scores;   // [T, E]
     void *h;                 // [list][16][de]
     float *hs;               // [list][de/128][16]
-    float *y;                // [T][k + n_shared][d] binary32
+    float *y;                // [3][T][k + n_shared][d] binary32: a part of the product each
     FewCounters *ctr;
     int *status;
     int T, d, E, k, de, n_shared;
@@ -171,8 +171,34 @@ struct Item {
     int pos;     // position in the list
     int expert;  // weight slot
     int blk;     // 128-feature block of H, or 128-column block of the output
-    int stages;
+    int q0, stages;  // its stages: q0 .. q0 + stages - 1 (gate/up: all)
+    int used, seg;   // down: index of the expert among those selected, part of the product
 };
+
+// The down products' stages, all items in order, cut into one contiguous range
+// a CTA, so that all CTAs have the same work in all.  With g = gate/up items /
+// CTAs, the first gate/up items mod CTAs CTAs have one item more than the
+// others; where g >= 1 the others have been working on complete experts since,
+// and take that many stages more (and the first ranges: the experts that are
+// complete by then).  A range is at least half an item, so an item is cut into
+// three parts at most; each part's sums go to rows of their own.
+struct DownPlan {
+    int light, a, b;  // ranges 0 .. light - 1 have a stages, the rest b
+    int total;
+    __device__ int begin(int r) const { return min(r <= light ? r * a : light * a + (r - light) * b, total); }
+    __device__ int range_of(int u) const { return u < light * a ? u / a : light + (u - light * a) / b; }
+};
+__device__ __forceinline__ DownPlan down_plan(int gu_items, int gu_stages, int items, int S, int G) {
+    DownPlan d;
+    d.total = items * S;
+    const int g = gu_items / G, heavy = gu_items - g * G, least = (S + 1) / 2;
+    d.light = g >= 1 && heavy > 0 ? G - heavy : 0;
+    // light * a + (G - light) * b >= total, a = b + gu_stages where that leaves b any
+    const int extra = min(gu_stages, d.light ? d.total / d.light : 0);
+    d.b = max((d.total - d.light * extra + G - 1) / G, least);
+    d.a = max(d.b + extra, least);
+    return d;
+}
 
 // Top-k of one token's affinities by one warp, as warp_topk selects (s + bias
 // descending, lowest expert first; the affinities are positive, so the sums
@@ -254,17 +280,14 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
 
     if (tid == 0) {
         for (int i = 0; i < FEW_STAGES; ++i) {
-            mbar_init(&s.full[i], 1);
-            mbar_init(&s.empty[i], 1);
+            mbar_init(&s.full[i], 1 + 4);
+            mbar_init(&s.done[i], 1);
         }
         for (int i = 0; i < SC_RING; ++i) {
             mbar_init(&s.sfull[i], 32);
             mbar_init(&s.sempty[i], 4);
         }
-        for (int i = 0; i < NBUF; ++i) {
-            mbar_init(&s.tfull[i], 1);
-            mbar_init(&s.tempty[i], 4);
-        }
+        mbar_init(&s.selected, 1);
         mbar_init(&s.routed, 1);
         mbar_init(&s.mma_done, 1);
         s.abort = 0;
@@ -275,22 +298,26 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
         prefetch_tmap(&tmap_w2);
     }
     if (tid < 32) s.rough_set[tid] = s.exact_set[tid] = 0;
-    if (warp == 1) {
-        tmem_alloc(&s.tmem_base, TMEM_COLS);
-        tmem_relinquish();
-    }
+    __syncthreads();
 
-    // -------------------------------------- 1. x, rough logits, rough selection
-    // x: half-warps over the (token, 128-column) tiles of all CTAs
-    {
-        const int half = cta * (FEW_THREADS / 16) + tid / 16, l16 = tid % 16, nx = d / 128;
-        for (int i0 = half & ~1; i0 < T * nx; i0 += G * (FEW_THREADS / 16)) {
-            const int i = i0 + (half & 1);
-            const bool in = i < T * nx;
-            const int t = in ? i / nx : 0, kb = in ? i % nx : 0, c = kb * 128 + l16 * 8;
-            if constexpr (FP8) {
+    // --------------- 1. x, rough logits, rough selection (warps 0-7; the exact
+    // logits run in warps 8-11 meanwhile)
+    bool ready = true;
+    uint32_t tmem_base = 0;
+    if (warp < 8) {
+        if (warp == 1) {
+            tmem_alloc(&s.tmem_base, TMEM_COLS);
+            tmem_relinquish();
+        }
+        if constexpr (FP8) {
+            // half-warps over the (token, 128-column) tiles of all CTAs
+            const int half = cta * (MAIN_THREADS / 16) + tid / 16, l16 = tid % 16;
+            for (int i0 = half & ~1; i0 < T * nd; i0 += G * (MAIN_THREADS / 16)) {
+                const int i = i0 + (half & 1);
+                const bool in = i < T * nd;
+                const int t = in ? i / nd : 0, kb = in ? i % nd : 0, c = kb * 128 + l16 * 8;
                 float v[8];
-                load_x8(p.x, t, c, d, p.pn, v);
+                load_x8(p.x, t, c, d, PreNorm{}, v);
                 uint2 code;
                 const float sc = quant_tile8(v, p.ue, &code);
                 if (in) {
@@ -298,16 +325,10 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                     if (l16 == 0) p.xs[kb * FT + t] = sc;
                 }
             }
-            if (p.pn.gamma && in) {
-                const uint4 raw = *reinterpret_cast<const uint4 *>(p.x + static_cast<size_t>(t) * d + c);
-                *reinterpret_cast<uint4 *>(p.xn + static_cast<size_t>(t) * d + c) = x_vec(raw, p.pn, t, c);
-            }
         }
-    }
-    // rough logits of experts cta, cta + G, ...: every thread a few columns of
-    // two experts and four tokens a pass, so that all of a pass's loads are in
-    // flight together (one warp a logit took 5 us at d = 7168, one token)
-    {
+        // rough logits of experts cta, cta + G, ...: every thread a few columns
+        // of two experts and four tokens a pass, all of a pass's loads in flight
+        // together
         const int ne = E > cta ? (E - 1 - cta) / G + 1 : 0;
         for (int e0 = 0; e0 < ne; e0 += 2)
             for (int t0 = 0; t0 < T; t0 += 4) {
@@ -319,11 +340,12 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                 for (int i = 0; i < 4; ++i)
                     xr[i] = reinterpret_cast<const uint4 *>(p.x + static_cast<size_t>(min(t0 + i, T - 1)) * d);
                 float acc[2][4] = {};
-                for (int v0 = tid; v0 < d / 8; v0 += 3 * FEW_THREADS) {
-                    uint4 a[3][2], b[3][4];
+                constexpr int NV = 4;
+                for (int v0 = tid; v0 < d / 8; v0 += NV * MAIN_THREADS) {
+                    uint4 a[NV][2], b[NV][4];
 #pragma unroll
-                    for (int c = 0; c < 3; ++c) {
-                        const int v = v0 + c * FEW_THREADS;
+                    for (int c = 0; c < NV; ++c) {
+                        const int v = v0 + c * MAIN_THREADS;
                         const bool in = v < d / 8;
 #pragma unroll
                         for (int i = 0; i < 2; ++i) a[c][i] = in ? __ldg(wr[i] + v) : make_uint4(0, 0, 0, 0);
@@ -331,12 +353,11 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                         for (int i = 0; i < 4; ++i) b[c][i] = in && t0 + i < T ? __ldg(xr[i] + v) : make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
-                    for (int c = 0; c < 3; ++c) {
-                        const int v = min(v0 + c * FEW_THREADS, d / 8 - 1);  // past the end: zeros
+                    for (int c = 0; c < NV; ++c)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             if (t0 + i >= T) break;
-                            const uint4 xv = x_vec(b[c][i], p.pn, t0 + i, v * 8);
+                            const uint4 xv = b[c][i];
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
                                 acc[j][i] = fmaf(bf16_lo(a[c][j].x), bf16_lo(xv.x), acc[j][i]);
@@ -349,7 +370,6 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                                 acc[j][i] = fmaf(bf16_hi(a[c][j].w), bf16_hi(xv.w), acc[j][i]);
                             }
                         }
-                    }
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -358,142 +378,184 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
                     if (lane == 0) s.part[warp][i] = v;
                 }
-                __syncthreads();
+                named_bar_sync(3, MAIN_THREADS);
                 if (tid < 8 && e0 + (tid >> 2) < ne && t0 + (tid & 3) < T) {
                     float l = 0.0f;
 #pragma unroll
-                    for (int w = 0; w < FEW_THREADS / 32; ++w) l += s.part[w][tid];
+                    for (int w = 0; w < MAIN_THREADS / 32; ++w) l += s.part[w][tid];
                     p.rough[static_cast<size_t>(t0 + (tid & 3)) * E + cta + (e0 + (tid >> 2)) * G] =
                         __fdividef(1.0f, 1.0f + __expf(-l));
                 }
-                __syncthreads();
+                named_bar_sync(3, MAIN_THREADS);
             }
-    }
-    // The shared expert's weights are needed whatever the routing: into L2 while
-    // it is found (behind the router's own loads, which they would hold up: the
-    // rough logits took 6.4 us, not 1.2).
-    if (tid == 32 && p.n_shared) {
-        const size_t es = FP8 ? 1 : 2, b13 = static_cast<size_t>(2) * de * d * es, b2 = static_cast<size_t>(d) * de * es;
-        for (size_t o = static_cast<size_t>(cta) * W_BYTES; o < b13; o += static_cast<size_t>(G) * W_BYTES)
-            l2_prefetch(p.w13 + E * b13 + o, static_cast<uint32_t>(min(b13 - o, static_cast<size_t>(W_BYTES))));
-        for (size_t o = static_cast<size_t>(cta) * W_BYTES; o < b2; o += static_cast<size_t>(G) * W_BYTES)
-            l2_prefetch(p.w2 + E * b2 + o, static_cast<uint32_t>(min(b2 - o, static_cast<size_t>(W_BYTES))));
-    }
-    fence_proxy_async_global();  // x is read by TMA
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-        red_release(&p.ctr->prepared, 1);
-        wait_count(&p.ctr->prepared, G, p, abort);
-        fence_proxy_async_global();
-    }
-    __syncthreads();
-    const bool ready = !s.abort;  // uniform: without x and the rough selection no work is done
-    if (ready)
-        for (int t = warp; t < T; t += FEW_THREADS / 32) {
-            int e;
-            float sc;
-            topk_any(p.rough + static_cast<size_t>(t) * E, p.bias, E, k, lane, e, sc);
-            if (lane < k) atomicOr(&s.rough_set[e >> 5], 1u << (e & 31));
+        // The shared expert's weights are needed whatever the routing: into L2
+        // while it is found (behind the router's own loads, which they would
+        // hold up).
+        if (tid == 32 && p.n_shared) {
+            const size_t es = FP8 ? 1 : 2, b13 = static_cast<size_t>(2) * de * d * es, b2 = static_cast<size_t>(d) * de * es;
+            for (size_t o = static_cast<size_t>(cta) * W_BYTES; o < b13; o += static_cast<size_t>(G) * W_BYTES)
+                l2_prefetch(p.w13 + E * b13 + o, static_cast<uint32_t>(min(b13 - o, static_cast<size_t>(W_BYTES))));
+            for (size_t o = static_cast<size_t>(cta) * W_BYTES; o < b2; o += static_cast<size_t>(G) * W_BYTES)
+                l2_prefetch(p.w2 + E * b2 + o, static_cast<uint32_t>(min(b2 - o, static_cast<size_t>(W_BYTES))));
         }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 0) {
-        if (lane == 0 && p.n_shared) s.list[0] = static_cast<uint16_t>(E);
-        const int n = append_set(s.rough_set, nullptr, s.list, p.n_shared, lane);
-        if (lane == 0) s.n_rough = s.n_list = n;
+        fence_proxy_async_global();  // the codes of x are read by TMA
+        __threadfence();
+        named_bar_sync(3, MAIN_THREADS);
+        if (tid == 0) {
+            red_release(&p.ctr->prepared, 1);
+            wait_count(&p.ctr->prepared, G, p, abort);
+            fence_proxy_async_global();
+        }
+        named_bar_sync(3, MAIN_THREADS);
+        ready = !s.abort;  // without x and the rough selection no work is done
+        ready = __all_sync(0xffffffffu, ready);
+        if (ready)
+            for (int t = warp; t < T; t += MAIN_THREADS / 32) {
+                int e;
+                float sc;
+                topk_any(p.rough + static_cast<size_t>(t) * E, p.bias, E, k, lane, e, sc);
+                if (lane < k) atomicOr(&s.rough_set[e >> 5], 1u << (e & 31));
+            }
+        tc_fence_before();
+        named_bar_sync(3, MAIN_THREADS);
+        tc_fence_after();
+        if (warp == 0) {
+            if (lane == 0 && p.n_shared) s.list[0] = static_cast<uint16_t>(E);
+            const int n = append_set(s.rough_set, nullptr, s.list, p.n_shared, lane);
+            __syncwarp();
+            if (lane == 0) {
+                s.n_rough = s.n_list = n;
+                mbar_arrive(&s.selected);
+            }
+        }
+        named_bar_sync(3, MAIN_THREADS);
+        tmem_base = __shfl_sync(0xffffffffu, s.tmem_base, 0);
     }
-    __syncthreads();
-    const uint32_t tmem_base = s.tmem_base;
-    const int gu_rough = s.n_rough * nf;  // gate/up items of the rough selection
+    const int gu_rough = warp < 8 ? s.n_rough * nf : 0;  // gate/up items of the rough selection
 
-    // Work items in one order for every role: gate/up of the list, then down of
-    // the experts selected; item i belongs to CTA i mod G.  Past the rough
+    // Work items in one order for every role: gate/up of the list, item i by CTA
+    // i mod G, then the CTA's range of the down stages.  Past the rough
     // selection's items the exact routing has to be known.
-    auto next_item = [&](int &i, bool &routed, Item &it) {
+    const int S2 = (KB2 + 1) / 2;  // stages of a down item
+    struct Walk {
+        int i, u, u1, r;  // next gate/up item; next down stage, end and number of the range
+        bool routed;
+    };
+    auto next_item = [&](Walk &w, Item &it) {
         if (!ready) return false;
-        if (i >= gu_rough && !routed) {
+        if (w.i >= gu_rough && !w.routed) {
             if (!wait_bar(&s.routed, 0, p, abort)) return false;
-            routed = true;
+            w.routed = true;
+            const int gu = s.n_list * nf, heavy = gu % G;
+            const DownPlan dp = down_plan(gu, KB1, s.n_used * nd, S2, G);
+            // CTAs heavy .. G - 1 have one gate/up item less
+            w.r = cta >= heavy ? cta - heavy : G - heavy + cta;
+            w.u = dp.begin(w.r);
+            w.u1 = dp.begin(w.r + 1);
         }
-        const int gu = i < gu_rough ? gu_rough : s.n_list * nf;
-        it.down = i >= gu;
-        if (!it.down) {
-            it.pos = i / nf;
-            it.blk = i - it.pos * nf;
+        if (w.i < (w.routed ? s.n_list * nf : gu_rough)) {
+            it.down = false;
+            it.pos = w.i / nf;
+            it.blk = w.i - it.pos * nf;
+            it.q0 = 0;
             it.stages = KB1;
+            w.i += G;
         } else {
-            const int j = i - gu;
-            const int u = j / nd;
-            if (u >= s.n_used) return false;
-            it.pos = s.used[u];
-            it.blk = j - u * nd;
-            it.stages = (KB2 + 1) / 2;
+            if (w.u >= w.u1) return false;
+            const int j = w.u / S2;
+            it.down = true;
+            it.used = j / nd;
+            it.pos = s.used[it.used];
+            it.blk = j - it.used * nd;
+            it.q0 = w.u - j * S2;
+            it.stages = min(S2 - it.q0, w.u1 - w.u);
+            it.seg = 0;
+            if (it.q0 > 0) {  // begun by the range before this one, or the one before that
+                const DownPlan dp = down_plan(s.n_list * nf, KB1, s.n_used * nd, S2, G);
+                it.seg = dp.begin(w.r - 1) <= j * S2 ? 1 : 2;
+            }
+            w.u += it.stages;
         }
         it.expert = s.list[it.pos];
-        i += G;
         return true;
     };
 
     if (warp == 0) {
         // ------------------------------------------------------- producer
+        // One lane; coordinates advance by constants, since every instruction
+        // of this loop costs a lone thread about five clocks (address arithmetic
+        // in it held a stage to 1130 clk; a stage of HBM takes 1190, one of L2
+        // 470).
         if (lane == 0) {
-            int stage = 0, i = cta;
+            const uint32_t w_base = smem_u32(s.w[0][0]), x_base = smem_u32(s.x[0][0]), f_base = smem_u32(&s.full[0]);
+            const uint64_t once = l2_evict_first(), keep = l2_evict_normal();  // a weight is read once
+            int stage = 0;
             uint32_t phase = 0, armed = 0, armed_phase = 0;
-            bool ok = true, routed = false;
+            bool ok = true;
+            Walk walk{cta, 0, 0, 0, false};
             Item it;
-            while (ok && next_item(i, routed, it)) {
-                // the down product's tokens (H) are loaded once the expert's H is
-                // complete; the weights of the ring's stages go ahead of that
+            while (ok && next_item(walk, it)) {
+                // tiles a and b of a stage: gate and up rows of one K block, or
+                // two K blocks of the same rows
+                const CUtensorMap *wm = it.down ? &tmap_w2 : &tmap_w13, *xm = it.down ? &tmap_h : &tmap_x;
+                const int per = it.down ? 2 : 1;  // K blocks a stage
+                const long long band = it.down ? static_cast<long long>(it.expert) * nd + it.blk
+                                               : static_cast<long long>(it.expert) * 2 * nf + it.blk;
+                const int kb = per * it.q0, KB = it.down ? KB2 : KB1;
+                int ax, ay, bx, by, dx, dy;
+                if (p.w_rowmajor) {
+                    ax = kb * KE, ay = static_cast<int>(band * 128);
+                    bx = it.down ? ax + KE : ax, by = it.down ? ay : ay + nf * 128;
+                    dx = per * KE, dy = 0;
+                } else {
+                    ax = bx = 0, ay = static_cast<int>((band * KB + kb) * 128);
+                    by = it.down ? ay + 128 : ay + nf * KB1 * 128;
+                    dx = 0, dy = per * 128;
+                }
+                const int xy = it.down ? it.pos * FT : 0, last = it.q0 + it.stages - 1;
+                const bool odd = it.down && 2 * last + 1 == KB2;  // the last stage holds one K block
+                int xx = kb * KE;
+                // H is loaded once the expert's H is complete; the weights of the
+                // ring's stages go ahead of that
                 bool have_x = !it.down;
-                int deferred = 0, issued = 0;
-                auto load_x = [&](int st, int q) {  // stage q of the item, in ring slot st
-                    const int n = it.down ? min(2, KB2 - 2 * q) : 1;
-                    for (int j = 0; j < n; ++j) {
-                        if (it.down) tma_load_2d(s.x[st][j], &tmap_h, (2 * q + j) * KE, it.pos * FT, &s.full[st]);
-                        else tma_load_2d(s.x[st][0], &tmap_x, q * KE, 0, &s.full[st]);
-                    }
+                int deferred = 0;
+                auto load_x = [&](int st, int x0, bool two) {
+                    tma_load_2d_policy(x_base + st * 2 * X_BYTES, xm, x0, xy, f_base + st * 8, keep);
+                    if (two) tma_load_2d_policy(x_base + st * 2 * X_BYTES + X_BYTES, xm, x0 + KE, xy, f_base + st * 8, keep);
                 };
-                auto flush = [&] {  // the last `deferred` stages issued wait for their tokens
+                auto flush = [&](bool short_last) {  // the last `deferred` stages issued wait for their tokens
                     have_x = wait_count(&p.ctr->h_done[it.pos], nf, p, abort);
                     fence_proxy_async_global();
                     // (given up: whatever H holds, so that the drain below ends)
                     for (; deferred > 0; --deferred)
-                        load_x((stage - deferred + FEW_STAGES) % FEW_STAGES, issued - deferred);
+                        load_x((stage - deferred + FEW_STAGES) % FEW_STAGES, xx - deferred * 2 * KE, deferred > 1 || !short_last);
                     return have_x;
                 };
-                for (int q = 0; q < it.stages; ++q) {
-                    if (deferred == FEW_STAGES && !flush()) {
+                for (int q = it.q0; q <= last; ++q) {
+                    if (deferred == FEW_STAGES && !flush(false)) {
                         ok = false;
                         break;
                     }
-                    if (!wait_bar(&s.empty[stage], phase ^ 1, p, abort)) {
+                    if (!wait_bar(&s.done[stage], phase ^ 1, p, abort)) {
                         ok = false;
                         break;
                     }
-                    const int n = it.down ? min(2, KB2 - 2 * q) : 2;  // weight tiles
-                    const int nx = it.down ? n : 1;
-                    mbar_arrive_expect_tx(&s.full[stage], n * W_BYTES + nx * X_BYTES);
-                    for (int j = 0; j < n; ++j) {
-                        const int kb = it.down ? 2 * q + j : q;
-                        const long long band = it.down ? static_cast<long long>(it.expert) * nd + it.blk
-                                                       : static_cast<long long>(it.expert) * 2 * nf + j * nf + it.blk;
-                        const CUtensorMap *m = it.down ? &tmap_w2 : &tmap_w13;
-                        if (p.w_rowmajor) tma_load_2d(s.w[stage][j], m, kb * KE, static_cast<int>(band * 128), &s.full[stage]);
-                        else tma_load_2d(s.w[stage][j], m, 0, static_cast<int>((band * (it.down ? KB2 : KB1) + kb) * 128), &s.full[stage]);
-                    }
+                    const bool one = odd && q == last;
+                    const uint32_t bar = f_base + stage * 8, w = w_base + stage * 2 * W_BYTES;
+                    mbar_arrive_expect_tx(&s.full[stage], one ? W_BYTES + X_BYTES : 2 * W_BYTES + per * X_BYTES);
+                    tma_load_2d_policy(w, wm, ax, ay, bar, once);
+                    if (!one) tma_load_2d_policy(w + W_BYTES, wm, bx, by, bar, once);
+                    if (have_x) load_x(stage, xx, it.down && !one);
+                    else ++deferred;
+                    ax += dx, ay += dy, bx += dx, by += dy, xx += per * KE;
                     armed |= 1u << stage;
                     armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
-                    if (have_x) load_x(stage, q);
-                    else ++deferred;
-                    ++issued;
                     if (++stage == FEW_STAGES) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
-                if (deferred > 0 && !flush()) ok = false;
+                if (deferred > 0 && !flush(ok && odd)) ok = false;
             }
             const long long t0 = clock64();
             for (int st = 0; st < FEW_STAGES; ++st) {
@@ -508,46 +570,53 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA
-        if (lane == 0) {
-            constexpr uint32_t idesc = instr_desc<FP8>(128, FT);
-            int stage = 0, tb = 0, i = cta;
-            uint32_t phase = 0, tphase = 0;
-            bool ok = true, routed = false;
-            Item it;
-            while (ok && next_item(i, routed, it)) {
-                for (int q = 0; q < it.stages; ++q) {
-                    if (!wait_bar(&s.tempty[tb], tphase ^ 1, p, abort) || !wait_bar(&s.full[stage], phase, p, abort)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const int n = it.down ? min(2, KB2 - 2 * q) : 2;
-                    for (int j = 0; j < n; ++j) {
-                        const uint32_t dt = tmem_base + (2 * tb + j) * FT;
-                        const uint64_t wd = smem_desc_sw128(smem_u32(s.w[stage][j]));
-                        const uint64_t xd = smem_desc_sw128(smem_u32(s.x[stage][it.down ? j : 0]));
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) tc_mma<FP8>(dt, wd + 2 * kk, xd + 2 * kk, idesc, kk != 0);
-                    }
-                    tc_commit(&s.empty[stage]);
-                    tc_commit(&s.tfull[tb]);
-                    if (++tb == NBUF) {
-                        tb = 0;
-                        tphase ^= 1;
-                    }
-                    if (++stage == FEW_STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
-                }
-            }
-            tc_commit(&s.mma_done);
-            const long long t0 = clock64();
-            while (!mbar_try_wait(&s.mma_done, 0)) {
-                if (clock64() - t0 > kWaitBudgetCycles) {
-                    set_status(p.status, MOE_ERR_TIMEOUT);
+        // One wait and one commit a stage, the warp together: with separate
+        // barriers for operands and accumulators on both sides, and one lane
+        // issuing, a stage took 1340 clk here, which held the whole stream to
+        // 6.4 TB/s; the eight MMAs themselves take 330.
+        constexpr uint32_t idesc = instr_desc<FP8>(128, FT);
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        Walk walk{cta, 0, 0, 0, false};
+        Item it;
+        const uint64_t wd0 = smem_desc_sw128(smem_u32(s.w[0][0])), xd0 = smem_desc_sw128(smem_u32(s.x[0][0]));
+        while (ok && __all_sync(0xffffffffu, next_item(walk, it))) {
+            // both tiles of a gate/up stage take the same tokens
+            const uint64_t x_step = it.down ? X_BYTES >> 4 : 0;
+            for (int q = it.q0; q < it.q0 + it.stages; ++q) {
+                if (!__all_sync(0xffffffffu, wait_bar(&s.full[stage], phase, p, abort))) {
+                    ok = false;
                     break;
                 }
+                tc_fence_after();
+                const uint32_t dt = tmem_base + 2 * stage * FT;
+                const uint64_t wd = wd0 + stage * (2 * W_BYTES >> 4), xd = xd0 + stage * (2 * X_BYTES >> 4);
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) tc_mma<FP8>(dt, wd + 2 * kk, xd + 2 * kk, idesc, kk != 0);
+                    if (!it.down || 2 * q + 1 < KB2)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc_mma<FP8>(dt + FT, wd + (W_BYTES >> 4) + 2 * kk, xd + x_step + 2 * kk, idesc, kk != 0);
+                    tc_commit(&s.done[stage]);
+                }
+                __syncwarp();
+                if (++stage == FEW_STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        // all MMAs issued are complete before TMEM is freed (the same lane is
+        // elected every time, and a commit covers that lane's MMAs)
+        if (elect_one()) tc_commit(&s.mma_done);
+        __syncwarp();
+        const long long t0 = clock64();
+        while (!mbar_try_wait(&s.mma_done, 0)) {
+            if (clock64() - t0 > kWaitBudgetCycles) {
+                set_status(p.status, MOE_ERR_TIMEOUT);
+                break;
             }
         }
     } else if (warp == 2) {
@@ -556,15 +625,16 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
         // second's, 8 and 9 the tiles' weight scales.  The token scales bypass
         // L1 (other CTAs wrote them during this launch).
         if constexpr (FP8) {
-            int slot = 0, i = cta;
+            int slot = 0;
             uint32_t phase = 0;
-            bool ok = true, routed = false;
+            bool ok = true;
+            Walk walk{cta, 0, 0, 0, false};
             Item it;
             while (ok) {
-                const bool more = next_item(i, routed, it);
+                const bool more = next_item(walk, it);
                 if (!__all_sync(0xffffffffu, more)) break;
                 if (it.down && !__all_sync(0xffffffffu, wait_count(&p.ctr->h_done[it.pos], nf, p, abort))) break;
-                for (int q = 0; q < it.stages; ++q) {
+                for (int q = it.q0; q < it.q0 + it.stages; ++q) {
                     if (!__all_sync(0xffffffffu, wait_bar(&s.sempty[slot], phase ^ 1, p, abort))) {
                         ok = false;
                         break;
@@ -595,10 +665,13 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
         // ------------------------------------------------------- epilogue
         const int q4 = warp & 3, r = q4 * 32 + lane, etid = tid - 128;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q4 * 32) << 16);
-        int tb = 0, slot = 0, i = cta;
-        uint32_t tphase = 0, sphase = 0;
-        bool ok = true, routed = false;
+        int stage = 0, slot = 0;
+        uint32_t phase = 0, sphase = 0;
+        bool ok = true;
+        Walk walk{cta, 0, 0, 0, false};
         Item it;
+        if (lane < FEW_STAGES) mbar_arrive(&s.full[lane]);  // the accumulators are free
+        __syncwarp();
         // the four warps agree on every step that has a barrier of theirs
         auto all_ok = [&](bool mine) {
             int all;
@@ -609,14 +682,14 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
             return all != 0;
         };
         while (true) {
-            if (!all_ok(next_item(i, routed, it))) break;
+            if (!all_ok(next_item(walk, it))) break;
             float acc0[FT], acc1[FT];
 #pragma unroll
             for (int t = 0; t < FT; ++t) acc0[t] = acc1[t] = 0.0f;
-            for (int q = 0; q < it.stages; ++q) {
+            for (int q = it.q0; q < it.q0 + it.stages; ++q) {
                 bool go = true;
                 if constexpr (FP8) go = wait_bar(&s.sfull[slot], sphase, p, abort);
-                go = go && wait_bar(&s.tfull[tb], tphase, p, abort);
+                go = go && wait_bar(&s.done[stage], phase, p, abort);
                 if (!__all_sync(0xffffffffu, go)) {
                     ok = false;
                     break;
@@ -624,11 +697,11 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                 tc_fence_after();
                 const bool both = !it.down || 2 * q + 1 < KB2;
                 float v[32];
-                tmem_ld32(lane_base + 2 * tb * FT, v);
+                tmem_ld32(lane_base + 2 * stage * FT, v);
                 tmem_wait_ld(v);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s.tempty[tb]);
+                if (lane == 0) mbar_arrive(&s.full[stage]);
                 if constexpr (FP8) {
                     const auto &sc = s.sc[slot];
                     const float w0 = sc.w[0], w1 = sc.w[1];
@@ -660,9 +733,9 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                         if (both) acc1[t] = __fadd_rn(acc1[t], v[FT + t]);
                     }
                 }
-                if (++tb == NBUF) {
-                    tb = 0;
-                    tphase ^= 1;
+                if (++stage == FEW_STAGES) {
+                    stage = 0;
+                    phase ^= 1;
                 }
             }
             if (!all_ok(ok)) break;
@@ -704,14 +777,16 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                 if (etid == 0) red_release(&p.ctr->h_done[it.pos], 1);
                 continue;
             }
-            // Y rows of the tokens that chose this expert (binary32: few rows)
+            // Y rows of the tokens that chose this expert (binary32: few rows),
+            // apart for each part of the product
             const int kk = k + p.n_shared;
+            const size_t part_rows = static_cast<size_t>(T) * kk * d;
             if (etid < FT) {
                 int rank = -1;
                 if (it.expert == E) rank = k;
                 else if (etid < T)
                     for (int j = k - 1; j >= 0; --j)
-                        if (s.sel[etid][j] == it.expert) rank = j;
+                        if (s.sel[etid][j] == it.used) rank = j;
                 s.rank[etid] = static_cast<int8_t>(rank);
             }
             named_bar_sync(1, 128);
@@ -719,38 +794,68 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
             for (int t = 0; t < FT; ++t) {
                 if (t >= T) break;
                 const int j = s.rank[t];
-                if (j >= 0) p.y[(static_cast<size_t>(t) * kk + j) * d + it.blk * 128 + r] = __fadd_rn(acc0[t], acc1[t]);
+                if (j >= 0)
+                    p.y[it.seg * part_rows + (static_cast<size_t>(t) * kk + j) * d + it.blk * 128 + r] = __fadd_rn(acc0[t], acc1[t]);
             }
             __threadfence();
             named_bar_sync(1, 128);
-            if (etid == 0) s.last = add_acq_rel(&p.ctr->col_done[it.blk], 1) == s.n_used - 1;
-            named_bar_sync(1, 128);
-            if (!s.last) continue;
-            // combine of 128 columns: out = sum_j g_j Y_j (rank order) + shared
-            // (+ h); warp q4 takes tokens q4, q4 + 4, ..., lane l columns 4l ..
-            __threadfence();
-            for (int t = q4; t < T; t += 4) {
-                const int c = it.blk * 128 + lane * 4;
+            if (etid == 0) red_release(&p.ctr->col_done[it.blk], it.stages);
+        }
+        // ------------------------------------------------------- combine
+        // out = sum_j g_j Y_j (rank order) + shared (+ residual): the (token,
+        // 128-column) pieces over the warps of all CTAs, each when every
+        // expert's stages of its columns are counted (the last CTA to count
+        // doing a whole column block left 16 CTAs with three or four each, 10
+        // us at one token).  Lane l takes columns 4l .. 4l + 3.
+        if (ready && ok && walk.routed) {
+            const DownPlan dp = down_plan(s.n_list * nf, KB1, s.n_used * nd, S2, G);
+            const int kk = k + p.n_shared;
+            const size_t part_rows = static_cast<size_t>(T) * kk * d;
+            for (int piece = q4 * G + cta; piece < T * nd; piece += 4 * G) {
+                const int t = piece / nd, blk = piece - t * nd;
+                if (!__all_sync(0xffffffffu, wait_count(&p.ctr->col_done[blk], s.n_used * S2, p, abort))) break;
+                const int c = blk * 128 + lane * 4;
                 const float4 *yr = reinterpret_cast<const float4 *>(p.y + static_cast<size_t>(t) * kk * d + c);
+                // lane j: the parts of its rank's product (rank k, the shared
+                // expert's, is the first of used)
+                auto parts_of = [&](int used) {
+                    const int u = (used * nd + blk) * S2;
+                    return dp.range_of(u + S2 - 1) - dp.range_of(u) + 1;
+                };
+                const int parts = lane < k ? parts_of(s.sel[t][lane]) : 1, parts_shared = parts_of(0);
                 float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                for (int j0 = 0; j0 < kk; j0 += 9) {
-                    float4 v[9];
+                constexpr int BATCH = 5;  // ranks whose loads are in flight together
+                for (int j0 = 0; j0 < kk; j0 += BATCH) {
+                    float4 v[BATCH], v1[BATCH];
+                    int np[BATCH];
 #pragma unroll
-                    for (int j = 0; j < 9; ++j)
-                        if (j0 + j < kk) v[j] = __ldcg(yr + static_cast<size_t>(j0 + j) * (d / 4));
+                    for (int j = 0; j < BATCH; ++j) {
+                        np[j] = __shfl_sync(0xffffffffu, parts, (j0 + j) & 31);
+                        if (j0 + j == k) np[j] = parts_shared;
+                        if (j0 + j >= kk) break;
+                        const float4 *src = yr + static_cast<size_t>(j0 + j) * (d / 4);
+                        v[j] = __ldcg(src);
+                        v1[j] = np[j] > 1 ? __ldcg(src + part_rows / 4) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    }
 #pragma unroll
-                    for (int j = 0; j < 9; ++j) {
+                    for (int j = 0; j < BATCH; ++j) {
                         if (j0 + j >= kk) break;
                         const float g = j0 + j < k ? s.gate[t][j0 + j] : 1.0f;
-                        acc.x = __fmaf_rn(g, v[j].x, acc.x);
-                        acc.y = __fmaf_rn(g, v[j].y, acc.y);
-                        acc.z = __fmaf_rn(g, v[j].z, acc.z);
-                        acc.w = __fmaf_rn(g, v[j].w, acc.w);
+                        float4 y = make_float4(__fadd_rn(v[j].x, v1[j].x), __fadd_rn(v[j].y, v1[j].y),
+                                               __fadd_rn(v[j].z, v1[j].z), __fadd_rn(v[j].w, v1[j].w));
+                        if (np[j] > 2) {
+                            const float4 v2 = __ldcg(yr + static_cast<size_t>(j0 + j) * (d / 4) + 2 * (part_rows / 4));
+                            y = make_float4(__fadd_rn(y.x, v2.x), __fadd_rn(y.y, v2.y), __fadd_rn(y.z, v2.z), __fadd_rn(y.w, v2.w));
+                        }
+                        acc.x = __fmaf_rn(g, y.x, acc.x);
+                        acc.y = __fmaf_rn(g, y.y, acc.y);
+                        acc.z = __fmaf_rn(g, y.z, acc.z);
+                        acc.w = __fmaf_rn(g, y.w, acc.w);
                     }
                 }
                 const size_t at = static_cast<size_t>(t) * d + c;
-                if (p.pn.gamma) {
-                    const uint2 res = *reinterpret_cast<const uint2 *>(p.x + at);
+                if (p.residual) {
+                    const uint2 res = *reinterpret_cast<const uint2 *>(p.residual + at);
                     acc.x = __fadd_rn(acc.x, bf16_lo(res.x));
                     acc.y = __fadd_rn(acc.y, bf16_hi(res.x));
                     acc.z = __fadd_rn(acc.z, bf16_lo(res.y));
@@ -759,7 +864,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                 *reinterpret_cast<uint2 *>(p.out + at) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
             }
         }
-    } else if (warp >= 8 && ready) {
+    } else if (warp >= 8) {
         // -------------------------------------------------- exact routing
         // One lane a (token, expert) logit: sequential fused multiply-adds over
         // d.  The operands come through a ring in shared memory: read straight
@@ -767,21 +872,20 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
         // 7168 (a chain needs 15); and 45 us with the copies issued by the
         // warp that runs the chains.
         const int rt = tid - 256, rw = warp - 8;
-        const uint16_t *x = p.pn.gamma ? p.xn : p.x;
         const int ne = E > cta ? (E - 1 - cta) / G + 1 : 0;
         const int per_pass = min(RC_ROWS - T, 32 / T);  // experts a pass: a warp's lanes
         for (int e0 = 0; e0 < ne; e0 += per_pass) {
             const int n = min(per_pass, ne - e0), rows = n + T;
             auto load_chunk = [&](int c) {  // rows 0 .. n - 1: router, then the tokens
-                for (int v = rt - 32; v < rows * (RC / 8); v += ROUTE_THREADS - 32) {
+                for (int v = rt; v < rows * (RC / 8); v += ROUTE_THREADS - 32) {
                     const int row = v / (RC / 8), col = v % (RC / 8) * 8;
                     const uint16_t *src = row < n ? p.w_router + static_cast<size_t>(cta + (e0 + row) * G) * d
-                                                  : x + static_cast<size_t>(row - n) * d;
+                                                  : p.x + static_cast<size_t>(row - n) * d;
                     cp_async16(&s.chunk[c % RC_BUFS][row][col], src + c * RC + col, true);
                 }
             };
             const int nc = d / RC;
-            if (rw > 0) {  // three warps copy, chunk after chunk
+            if (rw < 3) {  // three warps copy, chunk after chunk; the fourth has its scheduler nearly to itself
 #pragma unroll
                 for (int c = 0; c < RC_BUFS - 1; ++c) {
                     if (c < nc) load_chunk(c);
@@ -840,7 +944,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                 topk_any(p.scores + static_cast<size_t>(t) * E, p.bias, E, k, lane, e, sc);
                 const float g = warp_gate(sc, k, p.routed_scale);
                 if (lane < k) {
-                    s.sel[t][lane] = static_cast<int16_t>(e);
+                    s.sel[t][lane] = static_cast<uint16_t>(e);  // becomes its index in used below
                     s.gate[t][lane] = g;
                     atomicOr(&s.exact_set[e >> 5], 1u << (e & 31));
                     if (cta == 0) {
@@ -851,7 +955,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
             }
         }
         named_bar_sync(2, ROUTE_THREADS);
-        if (rw == 0 && !*abort) {
+        if (rw == 0 && __all_sync(0xffffffffu, wait_bar(&s.selected, 0, p, abort)) && !*abort) {
             const int n = append_set(s.exact_set, s.rough_set, s.list, s.n_rough, lane);
             __syncwarp();
             // positions of the selected experts, in list order
@@ -863,6 +967,31 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                 const uint32_t m = __ballot_sync(0xffffffffu, use);
                 if (use) s.used[n_used + __popc(m & ((1u << lane) - 1))] = static_cast<uint16_t>(j);
                 n_used += __popc(m);
+            }
+            __syncwarp();
+            // each choice becomes its expert's index in used: the shared expert,
+            // the rough selection's that are selected, the missed, each ascending
+            const uint32_t m_in = s.exact_set[lane] & s.rough_set[lane], m_miss = s.exact_set[lane] & ~s.rough_set[lane];
+            int b_in = __popc(m_in), b_miss = __popc(m_miss);  // bits before this lane's word
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int o_in = __shfl_up_sync(0xffffffffu, b_in, off), o_miss = __shfl_up_sync(0xffffffffu, b_miss, off);
+                if (lane >= off) b_in += o_in, b_miss += o_miss;
+            }
+            const int all_in = __shfl_sync(0xffffffffu, b_in, 31);
+            b_in -= __popc(m_in);
+            b_miss += all_in - __popc(m_miss);
+            for (int j0 = 0; j0 < T * k; j0 += 32) {
+                const int j = min(j0 + lane, T * k - 1);
+                uint16_t &se = s.sel[j / k][j % k];
+                const int e = se, w = e >> 5;
+                __syncwarp();
+                const uint32_t below = (1u << (e & 31)) - 1;
+                const uint32_t w_in = __shfl_sync(0xffffffffu, m_in, w), w_miss = __shfl_sync(0xffffffffu, m_miss, w);
+                const int n_in = __shfl_sync(0xffffffffu, b_in, w), n_miss = __shfl_sync(0xffffffffu, b_miss, w);
+                const bool in = w_in >> (e & 31) & 1;
+                if (j0 + lane < T * k)
+                    se = static_cast<uint16_t>(p.n_shared + (in ? n_in + __popc(w_in & below) : n_miss + __popc(w_miss & below)));
             }
             __syncwarp();
             if (lane == 0) {
@@ -888,7 +1017,63 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
     }
 }
 
+// Pre-norm of the few tokens: x = bf16((h * rstd) * gamma), rstd as rstd_kernel
+// defines it (lane l of one warp sums the squares of columns l mod 32 in
+// order).  A block a token stages the row in shared memory for that warp: 3 us
+// at d = 7168, where the sum straight from L2 waits for it 28 times.
+constexpr int PN_THREADS = 256, PN_CHUNK = 8192;
+__global__ void __launch_bounds__(PN_THREADS)
+few_prenorm_kernel(const uint16_t *__restrict__ h, const uint16_t *__restrict__ gamma, int d, float eps,
+                   uint16_t *__restrict__ xn) {
+    __shared__ __align__(16) uint16_t row[PN_CHUNK];
+    __shared__ float rstd_sh;
+    const int tid = threadIdx.x;
+    const uint16_t *src = h + static_cast<size_t>(blockIdx.x) * d;
+    pdl_wait_and_trigger();
+    float acc = 0.0f;
+    for (int c = 0; c < d; c += PN_CHUNK) {
+        const int n = min(PN_CHUNK, d - c);  // d is a multiple of 256
+        for (int v = tid; v < n / 8; v += PN_THREADS)
+            reinterpret_cast<uint4 *>(row)[v] = reinterpret_cast<const uint4 *>(src + c)[v];
+        __syncthreads();
+        if (tid < 32) {
+#pragma unroll 8
+            for (int i = tid; i < n; i += 32) {
+                const float v = __uint_as_float(static_cast<uint32_t>(row[i]) << 16);
+                acc = __fmaf_rn(v, v, acc);
+            }
+        }
+        __syncthreads();
+    }
+    if (tid < 32) {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) acc = __fadd_rn(acc, __shfl_xor_sync(0xffffffffu, acc, off));
+        if (tid == 0)
+            rstd_sh = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(acc, static_cast<float>(d)), eps)));
+    }
+    __syncthreads();
+    const float rstd = rstd_sh;
+    for (int v = tid; v < d / 8; v += PN_THREADS) {
+        const uint4 raw = reinterpret_cast<const uint4 *>(src)[v], graw = reinterpret_cast<const uint4 *>(gamma)[v];
+        const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w}, g[4] = {graw.x, graw.y, graw.z, graw.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o[i] = pack_bf16x2(prenorm_elem(bf16_lo(r[i]), rstd, bf16_lo(g[i])),
+                               prenorm_elem(bf16_hi(r[i]), rstd, bf16_hi(g[i])));
+        reinterpret_cast<uint4 *>(xn + static_cast<size_t>(blockIdx.x) * d)[v] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
 }  // namespace
+
+cudaError_t launch_few_prenorm(const uint16_t *h, const uint16_t *gamma, int T, int d, float eps, uint16_t *xn,
+                               cudaStream_t st, int *launches) {
+    mark_launch(st, *launches, "few_prenorm");
+    LAUNCH_OR_RETURN(launch_pdl(few_prenorm_kernel, dim3(T), dim3(PN_THREADS), 0, st, h, gamma, d, eps, xn));
+    ++*launches;
+    return cudaGetLastError();
+}
 
 cudaError_t launch_few(const FewArgs &g, cudaStream_t st, int *launches) {
     const moe_shape &s = *g.shape;
@@ -901,7 +1086,7 @@ cudaError_t launch_few(const FewArgs &g, cudaStream_t st, int *launches) {
     const long long t13 = rm ? rows13 : rows13 * s.d_model * es / 128, t2 = rm ? rows2 : rows2 * s.d_expert * es / 128;
     if (t13 >= (1LL << 31) || t2 >= (1LL << 31)) return cudaErrorInvalidValue;
     const int per = 128 / es;
-    const void *xop = fp8 ? static_cast<const void *>(g.xq) : (g.pn.gamma ? g.xn : g.x);
+    const void *xop = fp8 ? static_cast<const void *>(g.xq) : g.x;
     if (!make_map_2d(&mx, xop, fp8, s.d_model, s.T, FT) ||
         !make_map_2d(&mh, g.h, fp8, s.d_expert, g.list_rows * FT, FT) ||
         !make_map_2d(&m13, g.w13, fp8, rm ? s.d_model : per, static_cast<int>(t13)) ||
@@ -909,7 +1094,7 @@ cudaError_t launch_few(const FewArgs &g, cudaStream_t st, int *launches) {
         return cudaErrorInvalidValue;
     FewParams p{};
     p.x = g.x;
-    p.pn = g.pn;
+    p.residual = g.residual;
     p.w_router = g.w_router;
     p.bias = g.bias;
     p.w13 = static_cast<const uint8_t *>(g.w13);
@@ -921,7 +1106,6 @@ cudaError_t launch_few(const FewArgs &g, cudaStream_t st, int *launches) {
     p.gates_out = g.gates;
     p.xq = g.xq;
     p.xs = g.xs;
-    p.xn = g.xn;
     p.rough = g.rough;
     p.scores = g.scores;
     p.h = g.h;

@@ -179,7 +179,7 @@ struct FewCounters {
 struct FewArgs {
     const moe_shape *shape;
     const uint16_t *x;
-    PreNorm pn;
+    const uint16_t *residual;  // [T, d] added to out, or NULL
     const uint16_t *w_router;
     const float *bias;
     const void *w13, *w2;
@@ -190,14 +190,16 @@ struct FewArgs {
     float *rough, *scores;  // [T, E]
     uint8_t *xq;            // [T, d] (fp8)
     float *xs;              // [d/128][kFewTokens] (fp8)
-    uint16_t *xn;           // [T, d] (pre-norm)
     void *h;                // [list_rows][kFewTokens][de] e4m3 or bf16
     float *hs;              // [list_rows][de/128][kFewTokens] (fp8)
-    float *y;               // [T][k + n_shared][d]
+    float *y;               // [3][T][k + n_shared][d]
     int list_rows;
     FewCounters *counters;
     int *status;
 };
+// xn = bf16((h * rstd) * gamma) of T tokens, rstd as launch_rstd's.
+cudaError_t launch_few_prenorm(const uint16_t *h, const uint16_t *gamma, int T, int d, float eps, uint16_t *xn,
+                               cudaStream_t st, int *launches);
 cudaError_t launch_few(const FewArgs &g, cudaStream_t st, int *launches);
 
 // Block-scaled product of at most kLinearStreamRows rows of codes (linear.cu).

@@ -326,7 +326,7 @@ def test_launches_and_refusals():
     L.lib.forward_few(x)
     assert moe.moe_last_launch_names() == ["moe_few"]
     L.lib.forward_few_prenorm(x, gamma)
-    assert moe.moe_last_launch_names() == ["prenorm_rstd", "moe_few"]
+    assert moe.moe_last_launch_names() == ["few_prenorm", "moe_few"]
     L.lib.forward_few(x[:0])
     assert moe.moe_last_launch_count() == 0
     with pytest.raises(moe.MoeError, match="at most 16"):
