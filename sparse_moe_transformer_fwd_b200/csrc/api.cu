@@ -1049,7 +1049,7 @@ FewLayout few_layout(const moe_shape *s) {
     L.xn = take(T * d * 2);
     L.h = take(static_cast<size_t>(L.list_rows) * kFewTokens * de * (fp8 ? 1 : 2));
     L.hs = take(fp8 ? L.list_rows * (de / 128) * kFewTokens * 4 : 0);
-    L.y = take(3 * T * (k + s->n_shared) * d * 4);
+    L.y = take(2 * T * (k + s->n_shared) * d * 4);
     L.total = off;
     return L;
 }

@@ -60,6 +60,7 @@ static_assert(FEW_STAGES * 2 * FT <= TMEM_COLS, "accumulators of the ring's stag
 constexpr int MAIN_THREADS = 256;   // warps 0-7
 constexpr int ROUTE_THREADS = 128;  // warps 8-11
 constexpr int MAX_K = 32;
+constexpr int QUEUE = 4;  // work items between the producer and the other roles
 // Exact logits: chunks of RC columns of the router rows and tokens of one pass
 // (RC_ROWS in all) in a ring of RC_BUFS in shared memory; rows are padded by 16
 // bytes, so that lanes on different rows read different banks.
@@ -89,6 +90,8 @@ struct FewSmem {
     uint64_t full[FEW_STAGES];  // operands landed, and the accumulators drained (4 warps)
     uint64_t done[FEW_STAGES];  // MMAs done: accumulators to read, operands to overwrite
     uint64_t sfull[SC_RING], sempty[SC_RING];
+    int queue[QUEUE];
+    uint64_t qfull[QUEUE], qempty[QUEUE];
     uint64_t selected, routed;  // the rough selection; the exact one
     uint64_t mma_done;
     uint32_t tmem_base;
@@ -112,7 +115,7 @@ struct FewParams {
     float *rough, *scores;   // [T, E]
     void *h;                 // [list][16][de]
     float *hs;               // [list][de/128][16]
-    float *y;                // [3][T][k + n_shared][d] binary32: a part of the product each
+    float *y;                // [2][T][k + n_shared][d] binary32: a part of the product each
     FewCounters *ctr;
     int *status;
     int T, d, E, k, de, n_shared;
@@ -172,38 +175,9 @@ struct Item {
     int expert;  // weight slot
     int blk;     // 128-feature block of H, or 128-column block of the output
     int q0, stages;  // its stages: q0 .. q0 + stages - 1 (gate/up: all)
-    int used, seg;   // down: index of the expert among those selected, part of the product
+    int used, part;  // down: index of the expert among those selected, part of the product
 };
 
-// The down products' stages, all items in order, cut into one contiguous range
-// a CTA, so that all CTAs have the same work in all.  With g = gate/up items /
-// CTAs, the first gate/up items mod CTAs CTAs have one item more than the
-// others; where g >= 1 the others have been working on complete experts since,
-// and take that many stages more (and the first ranges: the experts that are
-// complete by then).  A range is at least half an item, so an item is cut into
-// three parts at most; each part's sums go to rows of their own.
-struct DownPlan {
-    int light, a, b;  // ranges 0 .. light - 1 have a stages, the rest b
-    int total;
-    __device__ int begin(int r) const { return min(r <= light ? r * a : light * a + (r - light) * b, total); }
-    __device__ int range_of(int u) const { return u < light * a ? u / a : light + (u - light * a) / b; }
-};
-__device__ __forceinline__ DownPlan down_plan(int gu_items, int gu_stages, int items, int S, int G) {
-    DownPlan d;
-    d.total = items * S;
-    const int g = gu_items / G, heavy = gu_items - g * G, least = (S + 1) / 2;
-    d.light = g >= 1 && heavy > 0 ? G - heavy : 0;
-    // light * a + (G - light) * b >= total, a = b + gu_stages where that leaves b any
-    const int extra = min(gu_stages, d.light ? d.total / d.light : 0);
-    d.b = max((d.total - d.light * extra + G - 1) / G, least);
-    d.a = max(d.b + extra, least);
-    return d;
-}
-
-// Top-k of one token's affinities by one warp, as warp_topk selects (s + bias
-// descending, lowest expert first; the affinities are positive, so the sums
-// order as integers once negative ones are turned over): k rounds of two warp
-// reductions.  0.5 us at 256 experts, k = 8, against 2 us for the shuffles.
 template <int PER_LANE>
 __device__ __forceinline__ void topk_keys(const float *row, const float *bias, int E, int k, int lane, int &my_e,
                                           float &my_s) {
@@ -286,6 +260,10 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
         for (int i = 0; i < SC_RING; ++i) {
             mbar_init(&s.sfull[i], 32);
             mbar_init(&s.sempty[i], 4);
+        }
+        for (int i = 0; i < QUEUE; ++i) {
+            mbar_init(&s.qfull[i], 1);
+            mbar_init(&s.qempty[i], FP8 ? 6 : 5);  // MMA, scales, four epilogue warps
         }
         mbar_init(&s.selected, 1);
         mbar_init(&s.routed, 1);
@@ -399,7 +377,6 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                 l2_prefetch(p.w2 + E * b2 + o, static_cast<uint32_t>(min(b2 - o, static_cast<size_t>(W_BYTES))));
         }
         fence_proxy_async_global();  // the codes of x are read by TMA
-        __threadfence();
         named_bar_sync(3, MAIN_THREADS);
         if (tid == 0) {
             red_release(&p.ctr->prepared, 1);
@@ -433,51 +410,56 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
     }
     const int gu_rough = warp < 8 ? s.n_rough * nf : 0;  // gate/up items of the rough selection
 
-    // Work items in one order for every role: gate/up of the list, item i by CTA
-    // i mod G, then the CTA's range of the down stages.  Past the rough
-    // selection's items the exact routing has to be known.
-    const int S2 = (KB2 + 1) / 2;  // stages of a down item
-    struct Walk {
-        int i, u, u1, r;  // next gate/up item; next down stage, end and number of the range
-        bool routed;
-    };
-    auto next_item = [&](Walk &w, Item &it) {
-        if (!ready) return false;
-        if (w.i >= gu_rough && !w.routed) {
+    // Work items, numbered: gate/up of the list (all of K), then the down
+    // products of the experts selected, in parts of half their K where that is
+    // four stages or more (a part's sums go to rows of their own).  A CTA's first
+    // is its own number, then it takes the next free one: CTAs that HBM serves
+    // faster do more (gate/up of one token ends between 38 and 53 us).  The
+    // producer takes it while it loads the one before and hands it to the other
+    // roles by a queue.  An item only waits for items of lower number, and a CTA
+    // holds one ahead only of a lower one, so the waits end.
+    const int S2 = (KB2 + 1) / 2, P2 = S2 >= 4 ? 2 : 1;
+    bool routed = false;
+    auto decode = [&](int id, Item &it) {
+        if (id >= gu_rough && !routed) {
             if (!wait_bar(&s.routed, 0, p, abort)) return false;
-            w.routed = true;
-            const int gu = s.n_list * nf, heavy = gu % G;
-            const DownPlan dp = down_plan(gu, KB1, s.n_used * nd, S2, G);
-            // CTAs heavy .. G - 1 have one gate/up item less
-            w.r = cta >= heavy ? cta - heavy : G - heavy + cta;
-            w.u = dp.begin(w.r);
-            w.u1 = dp.begin(w.r + 1);
+            routed = true;
         }
-        if (w.i < (w.routed ? s.n_list * nf : gu_rough)) {
-            it.down = false;
-            it.pos = w.i / nf;
-            it.blk = w.i - it.pos * nf;
+        const int gu = routed ? s.n_list * nf : gu_rough;
+        it.down = id >= gu;
+        if (!it.down) {
+            it.pos = id / nf;
+            it.blk = id - it.pos * nf;
             it.q0 = 0;
             it.stages = KB1;
-            w.i += G;
         } else {
-            if (w.u >= w.u1) return false;
-            const int j = w.u / S2;
-            it.down = true;
-            it.used = j / nd;
+            const int item = (id - gu) / P2;
+            it.used = item / nd;
+            if (it.used >= s.n_used) return false;
+            it.part = id - gu - item * P2;
             it.pos = s.used[it.used];
-            it.blk = j - it.used * nd;
-            it.q0 = w.u - j * S2;
-            it.stages = min(S2 - it.q0, w.u1 - w.u);
-            it.seg = 0;
-            if (it.q0 > 0) {  // begun by the range before this one, or the one before that
-                const DownPlan dp = down_plan(s.n_list * nf, KB1, s.n_used * nd, S2, G);
-                it.seg = dp.begin(w.r - 1) <= j * S2 ? 1 : 2;
-            }
-            w.u += it.stages;
+            it.blk = item - it.used * nd;
+            it.q0 = it.part * S2 / P2;
+            it.stages = (it.part + 1) * S2 / P2 - it.q0;
         }
         it.expert = s.list[it.pos];
         return true;
+    };
+    // the other roles' side of the queue (whole warps)
+    struct Taken {
+        int slot;
+        uint32_t phase;
+    };
+    auto take = [&](Taken &q, Item &it) {
+        const bool got = __all_sync(0xffffffffu, ready && wait_bar(&s.qfull[q.slot], q.phase, p, abort));
+        const int id = got ? s.queue[q.slot] : -1;
+        __syncwarp();
+        if (got && lane == 0) mbar_arrive(&s.qempty[q.slot]);
+        if (++q.slot == QUEUE) {
+            q.slot = 0;
+            q.phase ^= 1;
+        }
+        return id >= 0 && __all_sync(0xffffffffu, decode(id, it));
     };
 
     if (warp == 0) {
@@ -492,9 +474,25 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
             int stage = 0;
             uint32_t phase = 0, armed = 0, armed_phase = 0;
             bool ok = true;
-            Walk walk{cta, 0, 0, 0, false};
             Item it;
-            while (ok && next_item(walk, it)) {
+            int slot = 0, id = cta;
+            uint32_t qphase = 0;
+            auto publish = [&](int v) {
+                if (!wait_bar(&s.qempty[slot], qphase ^ 1, p, abort)) return false;
+                s.queue[slot] = v;
+                mbar_arrive(&s.qfull[slot]);
+                if (++slot == QUEUE) {
+                    slot = 0;
+                    qphase ^= 1;
+                }
+                return true;
+            };
+            while (ok && ready && decode(id, it)) {
+                if (!publish(id)) {
+                    ok = false;
+                    break;
+                }
+                id = G + atomicAdd(&p.ctr->next, 1);  // in flight while this item is loaded
                 // tiles a and b of a stage: gate and up rows of one K block, or
                 // two K blocks of the same rows
                 const CUtensorMap *wm = it.down ? &tmap_w2 : &tmap_w13, *xm = it.down ? &tmap_h : &tmap_x;
@@ -557,6 +555,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                 }
                 if (deferred > 0 && !flush(ok && odd)) ok = false;
             }
+            if (ok && ready) publish(-1);
             const long long t0 = clock64();
             for (int st = 0; st < FEW_STAGES; ++st) {
                 if (!(armed >> st & 1)) continue;
@@ -578,10 +577,10 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        Walk walk{cta, 0, 0, 0, false};
+        Taken taken{0, 0};
         Item it;
         const uint64_t wd0 = smem_desc_sw128(smem_u32(s.w[0][0])), xd0 = smem_desc_sw128(smem_u32(s.x[0][0]));
-        while (ok && __all_sync(0xffffffffu, next_item(walk, it))) {
+        while (ok && take(taken, it)) {
             // both tiles of a gate/up stage take the same tokens
             const uint64_t x_step = it.down ? X_BYTES >> 4 : 0;
             for (int q = it.q0; q < it.q0 + it.stages; ++q) {
@@ -628,11 +627,9 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
             int slot = 0;
             uint32_t phase = 0;
             bool ok = true;
-            Walk walk{cta, 0, 0, 0, false};
+            Taken taken{0, 0};
             Item it;
-            while (ok) {
-                const bool more = next_item(walk, it);
-                if (!__all_sync(0xffffffffu, more)) break;
+            while (ok && take(taken, it)) {
                 if (it.down && !__all_sync(0xffffffffu, wait_count(&p.ctr->h_done[it.pos], nf, p, abort))) break;
                 for (int q = it.q0; q < it.q0 + it.stages; ++q) {
                     if (!__all_sync(0xffffffffu, wait_bar(&s.sempty[slot], phase ^ 1, p, abort))) {
@@ -668,7 +665,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
         int stage = 0, slot = 0;
         uint32_t phase = 0, sphase = 0;
         bool ok = true;
-        Walk walk{cta, 0, 0, 0, false};
+        Taken taken{0, 0};
         Item it;
         if (lane < FEW_STAGES) mbar_arrive(&s.full[lane]);  // the accumulators are free
         __syncwarp();
@@ -682,7 +679,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
             return all != 0;
         };
         while (true) {
-            if (!all_ok(next_item(walk, it))) break;
+            if (!all_ok(take(taken, it))) break;
             float acc0[FT], acc1[FT];
 #pragma unroll
             for (int t = 0; t < FT; ++t) acc0[t] = acc1[t] = 0.0f;
@@ -772,8 +769,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                             static_cast<__nv_bfloat16 *>(p.h)[(row + t) * de + it.blk * 128 + r] = __float2bfloat16_rn(h[t]);
                 }
                 fence_proxy_async_global();  // H is read by TMA
-                __threadfence();
-                named_bar_sync(1, 128);
+                named_bar_sync(1, 128);      // (the release below covers what the barrier orders before it)
                 if (etid == 0) red_release(&p.ctr->h_done[it.pos], 1);
                 continue;
             }
@@ -795,9 +791,8 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                 if (t >= T) break;
                 const int j = s.rank[t];
                 if (j >= 0)
-                    p.y[it.seg * part_rows + (static_cast<size_t>(t) * kk + j) * d + it.blk * 128 + r] = __fadd_rn(acc0[t], acc1[t]);
+                    p.y[it.part * part_rows + (static_cast<size_t>(t) * kk + j) * d + it.blk * 128 + r] = __fadd_rn(acc0[t], acc1[t]);
             }
-            __threadfence();
             named_bar_sync(1, 128);
             if (etid == 0) red_release(&p.ctr->col_done[it.blk], it.stages);
         }
@@ -807,8 +802,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
         // expert's stages of its columns are counted (the last CTA to count
         // doing a whole column block left 16 CTAs with three or four each, 10
         // us at one token).  Lane l takes columns 4l .. 4l + 3.
-        if (ready && ok && walk.routed) {
-            const DownPlan dp = down_plan(s.n_list * nf, KB1, s.n_used * nd, S2, G);
+        if (ready && ok && __all_sync(0xffffffffu, wait_bar(&s.routed, 0, p, abort))) {
             const int kk = k + p.n_shared;
             const size_t part_rows = static_cast<size_t>(T) * kk * d;
             for (int piece = q4 * G + cta; piece < T * nd; piece += 4 * G) {
@@ -816,41 +810,25 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                 if (!__all_sync(0xffffffffu, wait_count(&p.ctr->col_done[blk], s.n_used * S2, p, abort))) break;
                 const int c = blk * 128 + lane * 4;
                 const float4 *yr = reinterpret_cast<const float4 *>(p.y + static_cast<size_t>(t) * kk * d + c);
-                // lane j: the parts of its rank's product (rank k, the shared
-                // expert's, is the first of used)
-                auto parts_of = [&](int used) {
-                    const int u = (used * nd + blk) * S2;
-                    return dp.range_of(u + S2 - 1) - dp.range_of(u) + 1;
-                };
-                const int parts = lane < k ? parts_of(s.sel[t][lane]) : 1, parts_shared = parts_of(0);
                 float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 constexpr int BATCH = 5;  // ranks whose loads are in flight together
                 for (int j0 = 0; j0 < kk; j0 += BATCH) {
                     float4 v[BATCH], v1[BATCH];
-                    int np[BATCH];
 #pragma unroll
                     for (int j = 0; j < BATCH; ++j) {
-                        np[j] = __shfl_sync(0xffffffffu, parts, (j0 + j) & 31);
-                        if (j0 + j == k) np[j] = parts_shared;
                         if (j0 + j >= kk) break;
                         const float4 *src = yr + static_cast<size_t>(j0 + j) * (d / 4);
                         v[j] = __ldcg(src);
-                        v1[j] = np[j] > 1 ? __ldcg(src + part_rows / 4) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        v1[j] = P2 > 1 ? __ldcg(src + part_rows / 4) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     }
 #pragma unroll
                     for (int j = 0; j < BATCH; ++j) {
                         if (j0 + j >= kk) break;
                         const float g = j0 + j < k ? s.gate[t][j0 + j] : 1.0f;
-                        float4 y = make_float4(__fadd_rn(v[j].x, v1[j].x), __fadd_rn(v[j].y, v1[j].y),
-                                               __fadd_rn(v[j].z, v1[j].z), __fadd_rn(v[j].w, v1[j].w));
-                        if (np[j] > 2) {
-                            const float4 v2 = __ldcg(yr + static_cast<size_t>(j0 + j) * (d / 4) + 2 * (part_rows / 4));
-                            y = make_float4(__fadd_rn(y.x, v2.x), __fadd_rn(y.y, v2.y), __fadd_rn(y.z, v2.z), __fadd_rn(y.w, v2.w));
-                        }
-                        acc.x = __fmaf_rn(g, y.x, acc.x);
-                        acc.y = __fmaf_rn(g, y.y, acc.y);
-                        acc.z = __fmaf_rn(g, y.z, acc.z);
-                        acc.w = __fmaf_rn(g, y.w, acc.w);
+                        acc.x = __fmaf_rn(g, __fadd_rn(v[j].x, v1[j].x), acc.x);
+                        acc.y = __fmaf_rn(g, __fadd_rn(v[j].y, v1[j].y), acc.y);
+                        acc.z = __fmaf_rn(g, __fadd_rn(v[j].z, v1[j].z), acc.z);
+                        acc.w = __fmaf_rn(g, __fadd_rn(v[j].w, v1[j].w), acc.w);
                     }
                 }
                 const size_t at = static_cast<size_t>(t) * d + c;
@@ -930,7 +908,6 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
             named_bar_sync(2, ROUTE_THREADS);
             if (mine) p.scores[static_cast<size_t>(t) * E + cta + (e0 + ei) * G] = sigmoid_cw(l, exp_consts());
         }
-        __threadfence();
         named_bar_sync(2, ROUTE_THREADS);
         if (rt == 0) {
             red_release(&p.ctr->scored, 1);

@@ -171,8 +171,8 @@ constexpr int kFewMaxList = 1025;  // experts worked on: n_experts + n_shared at
 constexpr int kFewMaxCols = 1024;  // 128-column blocks of d_model
 // Counters of one launch: zero before it, and left zero.
 struct FewCounters {
-    int prepared, scored, exited, abort;
-    int pad[60];
+    int prepared, scored, exited, abort, next;
+    int pad[59];
     int h_done[kFewMaxList + 63];  // [list position] gate/up items done
     int col_done[kFewMaxCols];     // [128-column block] experts' down items done
 };
@@ -192,7 +192,7 @@ struct FewArgs {
     float *xs;              // [d/128][kFewTokens] (fp8)
     void *h;                // [list_rows][kFewTokens][de] e4m3 or bf16
     float *hs;              // [list_rows][de/128][kFewTokens] (fp8)
-    float *y;               // [3][T][k + n_shared][d]
+    float *y;               // [2][T][k + n_shared][d]
     int list_rows;
     FewCounters *counters;
     int *status;
