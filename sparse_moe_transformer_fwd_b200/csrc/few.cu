@@ -31,9 +31,9 @@
 //   warp 1      TMEM allocator and MMA issuer (two accumulators of 16 columns
 //               a stage, NBUF stages in flight)
 //   warp 2      the stage's scales (e4m3), copied ahead with cp.async
-//   warp 3      idle after the setup
+//   warp 3      counts finished items for the other CTAs
 //   warps 4-7   epilogue: thread = weight row
-//   warps 8-11  exact routing
+//   warps 8-11  exact routing; then warp 9 watches for complete experts' H
 // The kernel is launched cooperatively (all CTAs resident), since CTAs wait for
 // one another.  Every wait is bounded: on expiry the CTA records
 // MOE_ERR_TIMEOUT, sets an abort word that ends the others' waits, drains what
@@ -60,6 +60,7 @@ static_assert(FEW_STAGES * 2 * FT <= TMEM_COLS, "accumulators of the ring's stag
 constexpr int MAIN_THREADS = 256;   // warps 0-7
 constexpr int ROUTE_THREADS = 128;  // warps 8-11
 constexpr int MAX_K = 32;
+constexpr int SIGNALS = 4;
 constexpr int QUEUE = 4;  // work items between the producer and the other roles
 // Exact logits: chunks of RC columns of the router rows and tokens of one pass
 // (RC_ROWS in all) in a ring of RC_BUFS in shared memory; rows are padded by 16
@@ -76,12 +77,9 @@ struct FewSmem {
         float pad[2];
     } sc[SC_RING];
     alignas(16) uint16_t chunk[RC_BUFS][RC_ROWS][RC_LD];
-    union {
-        float amax[4][FT];
-        float part[MAIN_THREADS / 32][8];  // rough logits of one pass
-    };
+    float amax[4][FT];
     float gate[FT][MAX_K];
-    uint16_t sel[FT][MAX_K];       // exact selection: its index in used
+    uint16_t sel[FT][MAX_K];       // exact selection
     uint16_t list[kFewMaxList];    // experts worked on: shared, predicted, missed
     uint16_t used[kFewMaxList];    // positions in list of the experts selected
     uint32_t rough_set[32], exact_set[32];
@@ -92,6 +90,11 @@ struct FewSmem {
     uint64_t sfull[SC_RING], sempty[SC_RING];
     int queue[QUEUE];
     uint64_t qfull[QUEUE], qempty[QUEUE];
+    // finished items between the epilogue and warp 3
+    int *sig_count[SIGNALS];
+    int sig_add[SIGNALS];
+    uint64_t sig_full[SIGNALS], sig_free[SIGNALS];
+    uint8_t h_ready[kFewMaxList + 7];  // [list position] the expert's H is complete
     uint64_t selected, routed;  // the rough selection; the exact one
     uint64_t mma_done;
     uint32_t tmem_base;
@@ -216,14 +219,17 @@ __device__ __forceinline__ void topk_keys(const float *row, const float *bias, i
         }
     }
 }
-__device__ __forceinline__ void topk_any(const float *row, const float *bias, int E, int k, int lane, int &e, float &s) {
+// Not inlined: the rough selection brings its code into the instruction cache,
+// from which the weight stream keeps everything away, before the exact one
+// runs it.
+__device__ __noinline__ void topk_any(const float *row, const float *bias, int E, int k, int lane, int &e, float &s) {
     if (E <= 256) topk_keys<8>(row, bias, E, k, lane, e, s);
     else topk_keys<kMaxPerLane>(row, bias, E, k, lane, e, s);
 }
 
 // One warp appends the set bits of `set` that `without` lacks, in ascending
 // order, to `list` from position n on; returns the new length.
-__device__ __forceinline__ int append_set(const uint32_t *set, const uint32_t *without, uint16_t *list, int n, int lane) {
+__device__ __noinline__ int append_set(const uint32_t *set, const uint32_t *without, uint16_t *list, int n, int lane) {
     const uint32_t m = set[lane] & (without ? ~without[lane] : 0xffffffffu);
     int before = __popc(m);
     const int mine = before;
@@ -265,6 +271,10 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
             mbar_init(&s.qfull[i], 1);
             mbar_init(&s.qempty[i], FP8 ? 6 : 5);  // MMA, scales, four epilogue warps
         }
+        for (int i = 0; i < SIGNALS; ++i) {
+            mbar_init(&s.sig_full[i], 128);
+            mbar_init(&s.sig_free[i], 1);
+        }
         mbar_init(&s.selected, 1);
         mbar_init(&s.routed, 1);
         mbar_init(&s.mma_done, 1);
@@ -276,6 +286,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
         prefetch_tmap(&tmap_w2);
     }
     if (tid < 32) s.rough_set[tid] = s.exact_set[tid] = 0;
+    for (int i = tid; i < static_cast<int>(sizeof s.h_ready) / 4; i += FEW_THREADS) reinterpret_cast<uint32_t *>(s.h_ready)[i] = 0;
     __syncthreads();
 
     // --------------- 1. x, rough logits, rough selection (warps 0-7; the exact
@@ -286,6 +297,15 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
         if (warp == 1) {
             tmem_alloc(&s.tmem_base, TMEM_COLS);
             tmem_relinquish();
+        }
+        // The shared expert's weights are needed whatever the routing: into L2
+        // while it is found.
+        if (tid == 96 && p.n_shared) {
+            const size_t es = FP8 ? 1 : 2, b13 = static_cast<size_t>(2) * de * d * es, b2 = static_cast<size_t>(d) * de * es;
+            for (size_t o = static_cast<size_t>(cta) * W_BYTES; o < b13; o += static_cast<size_t>(G) * W_BYTES)
+                l2_prefetch(p.w13 + E * b13 + o, static_cast<uint32_t>(min(b13 - o, static_cast<size_t>(W_BYTES))));
+            for (size_t o = static_cast<size_t>(cta) * W_BYTES; o < b2; o += static_cast<size_t>(G) * W_BYTES)
+                l2_prefetch(p.w2 + E * b2 + o, static_cast<uint32_t>(min(b2 - o, static_cast<size_t>(W_BYTES))));
         }
         if constexpr (FP8) {
             // half-warps over the (token, 128-column) tiles of all CTAs
@@ -304,77 +324,63 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                 }
             }
         }
-        // rough logits of experts cta, cta + G, ...: every thread a few columns
-        // of two experts and four tokens a pass, all of a pass's loads in flight
-        // together
+        // rough logits of experts cta, cta + G, ..., two at a time: a thread holds
+        // a few columns of both rows and goes through the tokens, the next
+        // token's loads in flight.  (The code is short because it runs once:
+        // unrolled over tokens as well it took 4 us for one token, most of
+        // them instruction fetches.)
         const int ne = E > cta ? (E - 1 - cta) / G + 1 : 0;
-        for (int e0 = 0; e0 < ne; e0 += 2)
-            for (int t0 = 0; t0 < T; t0 += 4) {
-                const uint4 *wr[2], *xr[4];
+        constexpr int NV = 4;
+        float(*part)[2 * FT] = reinterpret_cast<float(*)[2 * FT]>(s.sc);  // [warp][token][expert]
+        static_assert(sizeof s.sc >= MAIN_THREADS / 32 * 2 * FT * 4, "partial sums of the rough logits");
+        for (int e0 = 0; e0 < ne; e0 += 2) {
+            float mine = 0.0f;  // lane 2t + j: this warp's sum of (token t, expert j)
+            for (int v0 = tid; v0 < (d / 8 + MAIN_THREADS - 1) / MAIN_THREADS * MAIN_THREADS; v0 += NV * MAIN_THREADS) {
+                const uint4 *w0 = reinterpret_cast<const uint4 *>(p.w_router + static_cast<size_t>(cta + e0 * G) * d);
+                const uint4 *w1 = reinterpret_cast<const uint4 *>(p.w_router + static_cast<size_t>(cta + min(e0 + 1, ne - 1) * G) * d);
+                const uint4 *xr = reinterpret_cast<const uint4 *>(p.x);
+                uint4 a0[NV], a1[NV], b[NV];
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    wr[i] = reinterpret_cast<const uint4 *>(p.w_router + static_cast<size_t>(cta + min(e0 + i, ne - 1) * G) * d);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    xr[i] = reinterpret_cast<const uint4 *>(p.x + static_cast<size_t>(min(t0 + i, T - 1)) * d);
-                float acc[2][4] = {};
-                constexpr int NV = 4;
-                for (int v0 = tid; v0 < d / 8; v0 += NV * MAIN_THREADS) {
-                    uint4 a[NV][2], b[NV][4];
+                for (int c = 0; c < NV; ++c) {
+                    const int v = v0 + c * MAIN_THREADS;
+                    a0[c] = a1[c] = b[c] = make_uint4(0, 0, 0, 0);
+                    if (v < d / 8) a0[c] = __ldg(w0 + v), a1[c] = __ldg(w1 + v), b[c] = __ldg(xr + v);
+                }
+#pragma unroll 1
+                for (int t = 0; t < T; ++t) {
+                    float l0 = 0.0f, l1 = 0.0f;
 #pragma unroll
                     for (int c = 0; c < NV; ++c) {
                         const int v = v0 + c * MAIN_THREADS;
-                        const bool in = v < d / 8;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) a[c][i] = in ? __ldg(wr[i] + v) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) b[c][i] = in && t0 + i < T ? __ldg(xr[i] + v) : make_uint4(0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int c = 0; c < NV; ++c)
+                        const uint32_t xv[4] = {b[c].x, b[c].y, b[c].z, b[c].w}, u[4] = {a0[c].x, a0[c].y, a0[c].z, a0[c].w},
+                                       w[4] = {a1[c].x, a1[c].y, a1[c].z, a1[c].w};
+                        if (t + 1 < T && v < d / 8) b[c] = __ldg(xr + (t + 1) * (d / 8) + v);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            if (t0 + i >= T) break;
-                            const uint4 xv = b[c][i];
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                acc[j][i] = fmaf(bf16_lo(a[c][j].x), bf16_lo(xv.x), acc[j][i]);
-                                acc[j][i] = fmaf(bf16_hi(a[c][j].x), bf16_hi(xv.x), acc[j][i]);
-                                acc[j][i] = fmaf(bf16_lo(a[c][j].y), bf16_lo(xv.y), acc[j][i]);
-                                acc[j][i] = fmaf(bf16_hi(a[c][j].y), bf16_hi(xv.y), acc[j][i]);
-                                acc[j][i] = fmaf(bf16_lo(a[c][j].z), bf16_lo(xv.z), acc[j][i]);
-                                acc[j][i] = fmaf(bf16_hi(a[c][j].z), bf16_hi(xv.z), acc[j][i]);
-                                acc[j][i] = fmaf(bf16_lo(a[c][j].w), bf16_lo(xv.w), acc[j][i]);
-                                acc[j][i] = fmaf(bf16_hi(a[c][j].w), bf16_hi(xv.w), acc[j][i]);
-                            }
+                            l0 = fmaf(bf16_lo(u[i]), bf16_lo(xv[i]), l0);
+                            l1 = fmaf(bf16_lo(w[i]), bf16_lo(xv[i]), l1);
+                            l0 = fmaf(bf16_hi(u[i]), bf16_hi(xv[i]), l0);
+                            l1 = fmaf(bf16_hi(w[i]), bf16_hi(xv[i]), l1);
                         }
-                }
+                    }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float v = acc[i >> 2][i & 3];
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-                    if (lane == 0) s.part[warp][i] = v;
+                    for (int off = 16; off > 0; off >>= 1) {
+                        l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+                        l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+                    }
+                    if (lane == 2 * t) mine += l0;
+                    if (lane == 2 * t + 1) mine += l1;
                 }
-                named_bar_sync(3, MAIN_THREADS);
-                if (tid < 8 && e0 + (tid >> 2) < ne && t0 + (tid & 3) < T) {
-                    float l = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < MAIN_THREADS / 32; ++w) l += s.part[w][tid];
-                    p.rough[static_cast<size_t>(t0 + (tid & 3)) * E + cta + (e0 + (tid >> 2)) * G] =
-                        __fdividef(1.0f, 1.0f + __expf(-l));
-                }
-                named_bar_sync(3, MAIN_THREADS);
             }
-        // The shared expert's weights are needed whatever the routing: into L2
-        // while it is found (behind the router's own loads, which they would
-        // hold up).
-        if (tid == 32 && p.n_shared) {
-            const size_t es = FP8 ? 1 : 2, b13 = static_cast<size_t>(2) * de * d * es, b2 = static_cast<size_t>(d) * de * es;
-            for (size_t o = static_cast<size_t>(cta) * W_BYTES; o < b13; o += static_cast<size_t>(G) * W_BYTES)
-                l2_prefetch(p.w13 + E * b13 + o, static_cast<uint32_t>(min(b13 - o, static_cast<size_t>(W_BYTES))));
-            for (size_t o = static_cast<size_t>(cta) * W_BYTES; o < b2; o += static_cast<size_t>(G) * W_BYTES)
-                l2_prefetch(p.w2 + E * b2 + o, static_cast<uint32_t>(min(b2 - o, static_cast<size_t>(W_BYTES))));
+            part[warp][lane] = mine;
+            named_bar_sync(3, MAIN_THREADS);
+            if (tid < 2 * T && e0 + (tid & 1) < ne) {
+                float l = 0.0f;
+#pragma unroll
+                for (int w = 0; w < MAIN_THREADS / 32; ++w) l += part[w][tid];
+                p.rough[static_cast<size_t>(tid >> 1) * E + cta + (e0 + (tid & 1)) * G] = __fdividef(1.0f, 1.0f + __expf(-l));
+            }
+            if (e0 + 2 < ne) named_bar_sync(3, MAIN_THREADS);
         }
         fence_proxy_async_global();  // the codes of x are read by TMA
         named_bar_sync(3, MAIN_THREADS);
@@ -443,6 +449,23 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
             it.stages = (it.part + 1) * S2 / P2 - it.q0;
         }
         it.expert = s.list[it.pos];
+        return true;
+    };
+    // H of list position pos is complete: told by warp 9, whose polling keeps
+    // the L2 round trip (1.5 us under the weight stream) out of every item.
+    auto wait_h = [&](int pos) {
+        volatile uint8_t *flag = &s.h_ready[pos];
+        const long long t0 = clock64();
+        while (!*flag) {
+            if (*abort) return false;
+            if (clock64() - t0 > kWaitBudgetCycles) {
+                *abort = 1;
+                atomicExch(&p.ctr->abort, 1);
+                set_status(p.status, MOE_ERR_TIMEOUT);
+                return false;
+            }
+        }
+        __threadfence_block();
         return true;
     };
     // the other roles' side of the queue (whole warps)
@@ -522,7 +545,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                     if (two) tma_load_2d_policy(x_base + st * 2 * X_BYTES + X_BYTES, xm, x0 + KE, xy, f_base + st * 8, keep);
                 };
                 auto flush = [&](bool short_last) {  // the last `deferred` stages issued wait for their tokens
-                    have_x = wait_count(&p.ctr->h_done[it.pos], nf, p, abort);
+                    have_x = wait_h(it.pos);
                     fence_proxy_async_global();
                     // (given up: whatever H holds, so that the drain below ends)
                     for (; deferred > 0; --deferred)
@@ -630,7 +653,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
             Taken taken{0, 0};
             Item it;
             while (ok && take(taken, it)) {
-                if (it.down && !__all_sync(0xffffffffu, wait_count(&p.ctr->h_done[it.pos], nf, p, abort))) break;
+                if (it.down && !__all_sync(0xffffffffu, wait_h(it.pos))) break;
                 for (int q = it.q0; q < it.q0 + it.stages; ++q) {
                     if (!__all_sync(0xffffffffu, wait_bar(&s.sempty[slot], phase ^ 1, p, abort))) {
                         ok = false;
@@ -658,6 +681,24 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
             }
             cp_async_wait_all();
         }
+    } else if (warp == 3) {
+        // -------------------------------------------------------- signals
+        // The release to the other CTAs waits for the item's stores to arrive
+        // (1 to 2 us under the weight stream): here, not in the epilogue.
+        int slot = 0;
+        uint32_t phase = 0;
+        while (ready && __all_sync(0xffffffffu, wait_bar(&s.sig_full[slot], phase, p, abort))) {
+            int *count = s.sig_count[slot];
+            if (!count) break;
+            if (lane == 0) {
+                red_release(count, s.sig_add[slot]);
+                mbar_arrive(&s.sig_free[slot]);
+            }
+            if (++slot == SIGNALS) {
+                slot = 0;
+                phase ^= 1;
+            }
+        }
     } else if (warp >= 4 && warp < 8) {
         // ------------------------------------------------------- epilogue
         const int q4 = warp & 3, r = q4 * 32 + lane, etid = tid - 128;
@@ -669,6 +710,23 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
         Item it;
         if (lane < FEW_STAGES) mbar_arrive(&s.full[lane]);  // the accumulators are free
         __syncwarp();
+        int sig = 0;
+        uint32_t sig_phase = 0;
+        // *count += add once the stores that all four warps have made arrive
+        auto signal = [&](int *count, int add) {
+            bool free = true;
+            if (etid == 0) {
+                free = wait_bar(&s.sig_free[sig], sig_phase ^ 1, p, abort);
+                s.sig_count[sig] = count;
+                s.sig_add[sig] = add;
+            }
+            __syncwarp();
+            if (free) mbar_arrive(&s.sig_full[sig]);
+            if (++sig == SIGNALS) {
+                sig = 0;
+                sig_phase ^= 1;
+            }
+        };
         // the four warps agree on every step that has a barrier of theirs
         auto all_ok = [&](bool mine) {
             int all;
@@ -769,8 +827,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                             static_cast<__nv_bfloat16 *>(p.h)[(row + t) * de + it.blk * 128 + r] = __float2bfloat16_rn(h[t]);
                 }
                 fence_proxy_async_global();  // H is read by TMA
-                named_bar_sync(1, 128);      // (the release below covers what the barrier orders before it)
-                if (etid == 0) red_release(&p.ctr->h_done[it.pos], 1);
+                signal(&p.ctr->h_done[it.pos], 1);
                 continue;
             }
             // Y rows of the tokens that chose this expert (binary32: few rows),
@@ -782,7 +839,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                 if (it.expert == E) rank = k;
                 else if (etid < T)
                     for (int j = k - 1; j >= 0; --j)
-                        if (s.sel[etid][j] == it.used) rank = j;
+                        if (s.sel[etid][j] == it.expert) rank = j;
                 s.rank[etid] = static_cast<int8_t>(rank);
             }
             named_bar_sync(1, 128);
@@ -793,9 +850,9 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                 if (j >= 0)
                     p.y[it.part * part_rows + (static_cast<size_t>(t) * kk + j) * d + it.blk * 128 + r] = __fadd_rn(acc0[t], acc1[t]);
             }
-            named_bar_sync(1, 128);
-            if (etid == 0) red_release(&p.ctr->col_done[it.blk], it.stages);
+            signal(&p.ctr->col_done[it.blk], it.stages);
         }
+        signal(nullptr, 0);
         // ------------------------------------------------------- combine
         // out = sum_j g_j Y_j (rank order) + shared (+ residual): the (token,
         // 128-column) pieces over the warps of all CTAs, each when every
@@ -921,7 +978,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                 topk_any(p.scores + static_cast<size_t>(t) * E, p.bias, E, k, lane, e, sc);
                 const float g = warp_gate(sc, k, p.routed_scale);
                 if (lane < k) {
-                    s.sel[t][lane] = static_cast<uint16_t>(e);  // becomes its index in used below
+                    s.sel[t][lane] = static_cast<uint16_t>(e);
                     s.gate[t][lane] = g;
                     atomicOr(&s.exact_set[e >> 5], 1u << (e & 31));
                     if (cta == 0) {
@@ -946,35 +1003,29 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                 n_used += __popc(m);
             }
             __syncwarp();
-            // each choice becomes its expert's index in used: the shared expert,
-            // the rough selection's that are selected, the missed, each ascending
-            const uint32_t m_in = s.exact_set[lane] & s.rough_set[lane], m_miss = s.exact_set[lane] & ~s.rough_set[lane];
-            int b_in = __popc(m_in), b_miss = __popc(m_miss);  // bits before this lane's word
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int o_in = __shfl_up_sync(0xffffffffu, b_in, off), o_miss = __shfl_up_sync(0xffffffffu, b_miss, off);
-                if (lane >= off) b_in += o_in, b_miss += o_miss;
-            }
-            const int all_in = __shfl_sync(0xffffffffu, b_in, 31);
-            b_in -= __popc(m_in);
-            b_miss += all_in - __popc(m_miss);
-            for (int j0 = 0; j0 < T * k; j0 += 32) {
-                const int j = min(j0 + lane, T * k - 1);
-                uint16_t &se = s.sel[j / k][j % k];
-                const int e = se, w = e >> 5;
-                __syncwarp();
-                const uint32_t below = (1u << (e & 31)) - 1;
-                const uint32_t w_in = __shfl_sync(0xffffffffu, m_in, w), w_miss = __shfl_sync(0xffffffffu, m_miss, w);
-                const int n_in = __shfl_sync(0xffffffffu, b_in, w), n_miss = __shfl_sync(0xffffffffu, b_miss, w);
-                const bool in = w_in >> (e & 31) & 1;
-                if (j0 + lane < T * k)
-                    se = static_cast<uint16_t>(p.n_shared + (in ? n_in + __popc(w_in & below) : n_miss + __popc(w_miss & below)));
-            }
-            __syncwarp();
             if (lane == 0) {
                 s.n_list = n;
                 s.n_used = n_used;
                 mbar_arrive(&s.routed);
+            }
+        }
+        if (rw == 1 && __all_sync(0xffffffffu, wait_bar(&s.routed, 0, p, abort))) {
+            // watch the list's experts until every H is complete
+            const long long t0 = clock64();
+            bool all = false;
+            while (!all && !*abort) {
+                all = true;
+                for (int pos = lane; pos < s.n_list; pos += 32) {
+                    if (s.h_ready[pos]) continue;
+                    if (ld_acquire(&p.ctr->h_done[pos]) >= nf) {
+                        __threadfence_block();
+                        *static_cast<volatile uint8_t *>(&s.h_ready[pos]) = 1;
+                    } else {
+                        all = false;
+                    }
+                }
+                all = __all_sync(0xffffffffu, all);
+                if (!all && (ld_acquire(&p.ctr->abort) || clock64() - t0 > kWaitBudgetCycles)) break;
             }
         }
     }
