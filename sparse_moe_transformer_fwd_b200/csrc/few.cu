@@ -552,8 +552,9 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                         load_x((stage - deferred + FEW_STAGES) % FEW_STAGES, xx - deferred * 2 * KE, deferred > 1 || !short_last);
                     return have_x;
                 };
+                volatile uint8_t *h_flag = &s.h_ready[it.pos];
                 for (int q = it.q0; q <= last; ++q) {
-                    if (deferred == FEW_STAGES && !flush(false)) {
+                    if (!have_x && (deferred == FEW_STAGES || *h_flag) && !flush(false)) {
                         ok = false;
                         break;
                     }
