@@ -418,39 +418,32 @@ def alloc_few_workspace(shape: MoeShape, device="cuda") -> torch.Tensor:
 
 def _few_call(fn, shape, x, gamma, eps, w_router, bias, w13, w13_scales, w2, w2_scales, out, ws,
               topk_idx_out, stream):
-    """Checks sizes and devices and calls fn on the tensors' device."""
     T, d, E, de, S = shape.T, shape.d_model, shape.n_experts, shape.d_expert, shape.n_experts + shape.n_shared
     fp8 = shape.precision in (MOE_FP8_BLOCK, MOE_FP8_UE8M0)
-    wt, f32 = _FP8 if fp8 else _BF16, torch.float32
-    dev = _device_of(x=x, gamma=gamma, w_router=w_router, bias=bias, w13=w13, w13_scales=w13_scales, w2=w2,
-                     w2_scales=w2_scales, out=out, ws=ws, topk_idx_out=topk_idx_out)
-    n13, n2 = S * 2 * de * d, S * d * de
-    args = [_ptr(_sized(x, T * d, "x"), _BF16, "x")]
-    if fn is lib().moe_forward_few_prenorm:
-        args += [_ptr(_sized(gamma, d, "gamma"), _BF16, "gamma"), float(eps)]
-    args += [_ptr(_sized(w_router, E * d, "w_router"), _BF16, "w_router"), _ptr(_sized(bias, E, "bias"), f32, "bias"),
-             _ptr(_sized(w13, n13, "w13"), wt, "w13"),
-             _ptr(_sized(w13_scales, n13 // 16384 if fp8 else 0, "w13_scales"), f32, "w13_scales"),
-             _ptr(_sized(w2, n2, "w2"), wt, "w2"),
-             _ptr(_sized(w2_scales, n2 // 16384 if fp8 else 0, "w2_scales"), f32, "w2_scales"),
-             _ptr(_sized(out, T * d, "out"), _BF16, "out"),
-             _ptr(_sized(topk_idx_out, T * shape.top_k, "topk_idx_out"), torch.int32, "topk_idx_out"),
-             _ptr(ws, torch.uint8, "ws")]
-    with torch.cuda.device(dev):
-        _check(fn(ctypes.byref(shape), *args, ws.numel(), _stream(stream)))
+    wt, n13, n2 = _FP8 if fp8 else _BF16S, S * 2 * de * d, S * d * de
+    dev = _device(x, "x")
+    args = [_arg(x, _BF16S, T * d, dev, "x")]
+    if fn is _fn("moe_forward_few_prenorm"):
+        args += [_arg(gamma, _BF16S, d, dev, "gamma"), eps]
+    args += [_arg(w_router, _BF16S, E * d, dev, "w_router"), _arg(bias, _F32S, E, dev, "bias"),
+             _arg(w13, wt, n13, dev, "w13"), _arg(w13_scales, _F32S, n13 // 16384 if fp8 else 0, dev, "w13_scales"),
+             _arg(w2, wt, n2, dev, "w2"), _arg(w2_scales, _F32S, n2 // 16384 if fp8 else 0, dev, "w2_scales"),
+             _arg(out, _BF16S, T * d, dev, "out"), _arg(topk_idx_out, _I32S, T * shape.top_k, dev, "topk_idx_out"),
+             _arg(ws, _U8S, 0, dev, "ws"), ws.numel()]
+    _call_on(dev, stream, fn, shape, args)
 
 
 def moe_forward_few(shape, x, w_router, bias, w13, w13_scales, w2, w2_scales, out, ws,
                     topk_idx_out=None, stream=None):
     """The whole layer for at most MOE_FEW_MAX_TOKENS tokens, in one launch."""
-    _few_call(lib().moe_forward_few, shape, x, None, 0.0, w_router, bias, w13, w13_scales, w2, w2_scales, out,
+    _few_call(_fn("moe_forward_few"), shape, x, None, 0.0, w_router, bias, w13, w13_scales, w2, w2_scales, out,
               ws, topk_idx_out, stream)
 
 
 def moe_forward_few_prenorm(shape, h, gamma, eps, w_router, bias, w13, w13_scales, w2, w2_scales, out,
                             ws, topk_idx_out=None, stream=None):
     """out = h + MoE(bf16(RMSNorm(h) * gamma)) for at most MOE_FEW_MAX_TOKENS tokens."""
-    _few_call(lib().moe_forward_few_prenorm, shape, h, gamma, eps, w_router, bias, w13, w13_scales, w2,
+    _few_call(_fn("moe_forward_few_prenorm"), shape, h, gamma, eps, w_router, bias, w13, w13_scales, w2,
               w2_scales, out, ws, topk_idx_out, stream)
 
 
@@ -477,62 +470,89 @@ def alloc_linear_workspace(shape: MoeLinearShape, device="cuda") -> torch.Tensor
     return torch.zeros(moe_linear_workspace_size(shape), dtype=torch.uint8, device=device)
 
 
-def _sized(t, numel, name):
-    """t, checked to hold at least as many elements as the call reads or writes."""
-    if isinstance(t, torch.Tensor) and t.numel() < numel:
+_BF16S, _F32S, _I32S, _U8S = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.uint8,)
+_FNS = {}
+
+
+def _fn(name):
+    """The library's function, looked up once: these calls are made for a few
+    microseconds of GPU work, so their own cost is kept low (pointers as plain
+    integers, no context manager on the current device)."""
+    f = _FNS.get(name)
+    if f is None:
+        f = _FNS[name] = getattr(lib(), name)
+    return f
+
+
+def _device(t, name) -> torch.device:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    return t.device
+
+
+def _arg(t, dtypes, numel, dev, name):
+    """Address of a contiguous tensor of one of `dtypes` on `dev` with at least
+    `numel` elements (None stays None: a NULL pointer)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtypes if len(dtypes) > 1 else dtypes[0]}")
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, the call's other tensors on {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if t.numel() < numel:
         raise ValueError(f"{name}: {t.numel()} elements, the shape needs {numel}")
-    return t
+    return t.data_ptr()
 
 
-def _device_of(**tensors):
-    """The one device the call's tensors are on."""
-    dev = None
-    for name, t in tensors.items():
-        if isinstance(t, torch.Tensor):
-            dev = t.device if dev is None else dev
-            if t.device != dev:
-                raise ValueError(f"{name}: on {t.device}, other tensors on {dev}")
-    return dev
+def _call_on(dev, stream, fn, shape, args) -> None:
+    """fn(shape, *args, stream) with `dev` current, on `stream` or the current
+    stream of `dev`."""
+    if torch._C._cuda_getDevice() != dev.index:
+        with torch.cuda.device(dev):
+            return _call_on(dev, stream, fn, shape, args)
+    raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    rc = fn(ctypes.byref(shape), *args, raw)
+    if rc != MOE_OK:
+        _check(rc)
 
 
-def _linear_call(fn, shape, first, w, w_scales, residual, out, ws, stream, **more):
-    """Checks sizes and devices and calls fn(shape, *first, w, w_scales[, residual], out, ws ...) on the
-    tensors' device; `first` holds the leading arguments, `more` their tensors by name."""
-    T, K, N = shape.T, shape.K, shape.N
-    dev = _device_of(**more, w=w, w_scales=w_scales, residual=residual, out=out, ws=ws)
-    args = [_ptr(_sized(w, N * K, "w"), _FP8, "w"),
-            _ptr(_sized(w_scales, -(-N // 128) * (K // 128), "w_scales"), torch.float32, "w_scales")]
-    if fn is not lib().moe_linear_prenorm:
-        args.append(_ptr(_sized(residual, T * N, "residual"), _BF16, "residual"))
-    args.append(_ptr(_sized(out, T * N, "out"), torch.float32 if shape.out_f32 else _BF16, "out"))
-    if dev is None or dev.type != "cuda":
-        raise ValueError("w: must be a CUDA tensor")
-    with torch.cuda.device(dev):
-        _check(fn(ctypes.byref(shape), *first, *args, _ptr(ws, torch.uint8, "ws"), ws.numel(),
-                  _stream(stream)))
+def _linear_args(shape, w, w_scales, out, dev):
+    N, KB = shape.N, shape.K // 128
+    return (_arg(w, _FP8, N * shape.K, dev, "w"), _arg(w_scales, _F32S, (N + 127) // 128 * KB, dev, "w_scales"),
+            _arg(out, _F32S if shape.out_f32 else _BF16S, shape.T * N, dev, "out"))
 
 
 def fp8_block_gemm(shape, a, a_scales, w, w_scales, out, ws, residual=None, stream=None):
     """out = a W^T (+ residual) of e4m3 codes in 1x128 tiles (a) and 128x128 blocks (w)."""
-    T, K = shape.T, shape.K
-    _linear_call(lib().fp8_block_gemm, shape,
-                 [_ptr(_sized(a, T * K, "a"), _FP8, "a"),
-                  _ptr(_sized(a_scales, T * (K // 128), "a_scales"), torch.float32, "a_scales")],
-                 w, w_scales, residual, out, ws, stream, a=a, a_scales=a_scales)
+    T, K, dev = shape.T, shape.K, _device(a, "a")
+    wp, wsp, op = _linear_args(shape, w, w_scales, out, dev)
+    _call_on(dev, stream, _fn("fp8_block_gemm"), shape,
+             (_arg(a, _FP8, T * K, dev, "a"), _arg(a_scales, _F32S, T * (K // 128), dev, "a_scales"), wp, wsp,
+              _arg(residual, _BF16S, T * shape.N, dev, "residual"), op, _arg(ws, _U8S, 0, dev, "ws"), ws.numel()))
 
 
 def moe_linear(shape, x, w, w_scales, out, ws, residual=None, stream=None):
     """out = x W^T (+ residual) of a bf16 x, quantised 1x128 on the way."""
-    _linear_call(lib().moe_linear, shape, [_ptr(_sized(x, shape.T * shape.K, "x"), _BF16, "x")],
-                 w, w_scales, residual, out, ws, stream, x=x)
+    T, dev = shape.T, _device(x, "x")
+    wp, wsp, op = _linear_args(shape, w, w_scales, out, dev)
+    _call_on(dev, stream, _fn("moe_linear"), shape,
+             (_arg(x, _BF16S, T * shape.K, dev, "x"), wp, wsp, _arg(residual, _BF16S, T * shape.N, dev, "residual"),
+              op, _arg(ws, _U8S, 0, dev, "ws"), ws.numel()))
 
 
 def moe_linear_prenorm(shape, h, gamma, eps, w, w_scales, out, ws, stream=None):
     """out = bf16(RMSNorm(h) * gamma) W^T."""
-    _linear_call(lib().moe_linear_prenorm, shape,
-                 [_ptr(_sized(h, shape.T * shape.K, "h"), _BF16, "h"),
-                  _ptr(_sized(gamma, shape.K, "gamma"), _BF16, "gamma"), float(eps)],
-                 w, w_scales, None, out, ws, stream, h=h, gamma=gamma)
+    T, dev = shape.T, _device(h, "h")
+    wp, wsp, op = _linear_args(shape, w, w_scales, out, dev)
+    _call_on(dev, stream, _fn("moe_linear_prenorm"), shape,
+             (_arg(h, _BF16S, T * shape.K, dev, "h"), _arg(gamma, _BF16S, shape.K, dev, "gamma"), eps, wp, wsp, op,
+              _arg(ws, _U8S, 0, dev, "ws"), ws.numel()))
 
 
 def moe_check_status(ws, stream=None) -> int:
