@@ -1190,7 +1190,7 @@ int linear_ksplit(const moe_linear_shape *s) {
 }
 
 struct LinearLayout {
-    size_t status, counters, rstd, a, a_scales, partial, total;
+    size_t status, counters, a, a_scales, partial, total;
 };
 
 LinearLayout linear_layout(const moe_linear_shape *s) {
@@ -1204,7 +1204,6 @@ LinearLayout linear_layout(const moe_linear_shape *s) {
     };
     L.status = take(256);
     L.counters = take(kLinearCounterBytes);
-    L.rstd = take(T * 4);
     L.a = take(T * K);
     L.a_scales = take(T * (K / 128) * 4);
     if (s->T <= kLinearStreamRows)
@@ -1217,15 +1216,19 @@ LinearLayout linear_layout(const moe_linear_shape *s) {
     return L;
 }
 
-// out = a W^T (+ residual) of codes and scales: the weight-streaming kernel for
-// few tokens, the tiled GEMM (one segment, one slot) for more.  *n counts the
-// launches before and after; the first one of a call may not read W ahead.
-int linear_product(const moe_linear_shape *s, const void *a, const float *a_scales, const void *w,
+// out = a W^T (+ residual) of codes and scales, or of bf16 x (at most
+// kLinearQuantRows tokens): the weight-streaming kernel for few tokens, the
+// tiled GEMM (one segment, one slot) for more.  *n counts the launches before
+// and after; the first one of a call may not read W ahead.
+int linear_product(const moe_linear_shape *s, const uint16_t *x, const void *a, const float *a_scales, const void *w,
                    const float *w_scales, const uint16_t *residual, void *out, void *ws,
                    const LinearLayout &L, cudaStream_t st, int *n) {
     float *partial = at<float>(ws, L.partial);
     if (s->T <= kLinearStreamRows) {
         LinearStreamArgs g{};
+        g.x = x;
+        g.ue8m0 = s->precision == MOE_FP8_UE8M0;
+        g.early_w = *n > 0;
         g.a = a;
         g.a_scales = a_scales;
         g.w = w;
@@ -1303,21 +1306,16 @@ int linear_impl(const char *name, const moe_linear_shape *s, const uint16_t *x, 
     RETURN_IF(check_device());
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     int n = 0;
-    if (!codes) {
-        PreNorm pn{};
-        if (gamma) {
-            float *rstd = at<float>(ws, L.rstd);
-            LAUNCH(launch_rstd(x, s->T, s->K, eps, rstd, st, &n), "pre-norm statistics");
-            pn.rstd = rstd;
-            pn.gamma = gamma;
-        }
-        LAUNCH(launch_linear_quant(x, s->T, s->K, pn, s->precision == MOE_FP8_UE8M0, at<uint8_t>(ws, L.a),
-                                   at<float>(ws, L.a_scales), st, &n),
-               "quantise x");
-        codes = at<uint8_t>(ws, L.a);
-        code_scales = at<float>(ws, L.a_scales);
-    }
-    RETURN_IF(linear_product(s, codes, code_scales, w, w_scales, residual, out, ws, L, st, &n));
+    const bool ue = s->precision == MOE_FP8_UE8M0;
+    uint8_t *a = at<uint8_t>(ws, L.a);
+    float *a_scales = at<float>(ws, L.a_scales);
+    const bool in_product = !codes && !gamma && s->T <= kLinearQuantRows;
+    if (gamma)
+        LAUNCH(launch_linear_prenorm_quant(x, gamma, s->T, s->K, eps, ue, a, a_scales, st, &n), "pre-norm and quantise");
+    else if (!codes && !in_product)
+        LAUNCH(launch_linear_quant(x, s->T, s->K, ue, a, a_scales, st, &n), "quantise x");
+    RETURN_IF(linear_product(s, in_product ? x : nullptr, codes ? codes : a, codes ? code_scales : a_scales, w, w_scales,
+                             residual, out, ws, L, st, &n));
     mark_launch(st, n);
     g_launches = n;
     return MOE_OK;

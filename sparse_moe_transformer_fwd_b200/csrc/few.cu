@@ -315,7 +315,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                 const bool in = i < T * nd;
                 const int t = in ? i / nd : 0, kb = in ? i % nd : 0, c = kb * 128 + l16 * 8;
                 float v[8];
-                load_x8(p.x, t, c, d, PreNorm{}, v);
+                widen8(*reinterpret_cast<const uint4 *>(p.x + static_cast<size_t>(t) * d + c), v);
                 uint2 code;
                 const float sc = quant_tile8(v, p.ue, &code);
                 if (in) {
@@ -1046,51 +1046,20 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
     }
 }
 
-// Pre-norm of the few tokens: x = bf16((h * rstd) * gamma), rstd as rstd_kernel
-// defines it (lane l of one warp sums the squares of columns l mod 32 in
-// order).  A block a token stages the row in shared memory for that warp: 3 us
-// at d = 7168, where the sum straight from L2 waits for it 28 times.
-constexpr int PN_THREADS = 256, PN_CHUNK = 8192;
-__global__ void __launch_bounds__(PN_THREADS)
+// Pre-norm of the few tokens, a block each: x = bf16((h * rstd) * gamma).
+__global__ void __launch_bounds__(256)
 few_prenorm_kernel(const uint16_t *__restrict__ h, const uint16_t *__restrict__ gamma, int d, float eps,
                    uint16_t *__restrict__ xn) {
-    __shared__ __align__(16) uint16_t row[PN_CHUNK];
+    __shared__ __align__(16) uint16_t chunk[kRstdChunk];
     __shared__ float rstd_sh;
-    const int tid = threadIdx.x;
-    const uint16_t *src = h + static_cast<size_t>(blockIdx.x) * d;
+    const uint16_t *row = h + static_cast<size_t>(blockIdx.x) * d;
     pdl_wait_and_trigger();
-    float acc = 0.0f;
-    for (int c = 0; c < d; c += PN_CHUNK) {
-        const int n = min(PN_CHUNK, d - c);  // d is a multiple of 256
-        for (int v = tid; v < n / 8; v += PN_THREADS)
-            reinterpret_cast<uint4 *>(row)[v] = reinterpret_cast<const uint4 *>(src + c)[v];
-        __syncthreads();
-        if (tid < 32) {
-#pragma unroll 8
-            for (int i = tid; i < n; i += 32) {
-                const float v = __uint_as_float(static_cast<uint32_t>(row[i]) << 16);
-                acc = __fmaf_rn(v, v, acc);
-            }
-        }
-        __syncthreads();
-    }
-    if (tid < 32) {
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) acc = __fadd_rn(acc, __shfl_xor_sync(0xffffffffu, acc, off));
-        if (tid == 0)
-            rstd_sh = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(acc, static_cast<float>(d)), eps)));
-    }
-    __syncthreads();
-    const float rstd = rstd_sh;
-    for (int v = tid; v < d / 8; v += PN_THREADS) {
-        const uint4 raw = reinterpret_cast<const uint4 *>(src)[v], graw = reinterpret_cast<const uint4 *>(gamma)[v];
-        const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w}, g[4] = {graw.x, graw.y, graw.z, graw.w};
-        uint32_t o[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            o[i] = pack_bf16x2(prenorm_elem(bf16_lo(r[i]), rstd, bf16_lo(g[i])),
-                               prenorm_elem(bf16_hi(r[i]), rstd, bf16_hi(g[i])));
-        reinterpret_cast<uint4 *>(xn + static_cast<size_t>(blockIdx.x) * d)[v] = make_uint4(o[0], o[1], o[2], o[3]);
+    const float rstd = block_rstd(row, d, eps, chunk, &rstd_sh);
+    for (int v = threadIdx.x; v < d / 8; v += blockDim.x) {
+        float x[8];
+        prenorm8(row, gamma, v * 8, rstd, x);
+        reinterpret_cast<uint4 *>(xn + static_cast<size_t>(blockIdx.x) * d)[v] =
+            make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
     }
 }
 
@@ -1099,7 +1068,7 @@ few_prenorm_kernel(const uint16_t *__restrict__ h, const uint16_t *__restrict__ 
 cudaError_t launch_few_prenorm(const uint16_t *h, const uint16_t *gamma, int T, int d, float eps, uint16_t *xn,
                                cudaStream_t st, int *launches) {
     mark_launch(st, *launches, "few_prenorm");
-    LAUNCH_OR_RETURN(launch_pdl(few_prenorm_kernel, dim3(T), dim3(PN_THREADS), 0, st, h, gamma, d, eps, xn));
+    LAUNCH_OR_RETURN(launch_pdl(few_prenorm_kernel, dim3(T), dim3(256), 0, st, h, gamma, d, eps, xn));
     ++*launches;
     return cudaGetLastError();
 }

@@ -205,7 +205,9 @@ cudaError_t launch_few(const FewArgs &g, cudaStream_t st, int *launches);
 // Block-scaled product of at most kLinearStreamRows rows of codes (linear.cu).
 constexpr int kLinearStreamRows = 64;
 constexpr int kLinearMaxCtas = 160;  // CTAs of linear_stream (sizes its partial sums)
+constexpr int kLinearQuantRows = 16;  // and of bf16 x, quantised in the same kernel
 struct LinearStreamArgs {
+    const uint16_t *x;         // bf16 [T, K], or NULL: a and a_scales
     const void *a;             // e4m3 [T, K]
     const float *a_scales;     // [T, K/128]
     const void *w;             // e4m3 [N, K], row-major or tiled
@@ -217,14 +219,19 @@ struct LinearStreamArgs {
     int *status;
     int T, K, N;
     int out_f32, w_rowmajor;
+    int ue8m0;    // of x's scales
+    int early_w;  // an earlier launch of the same call has waited for the stream: W may be read ahead
 };
 inline size_t linear_partial_floats(int T) {
     return static_cast<size_t>(kLinearMaxCtas) * 2 * 128 * (T <= 16 ? 16 : (T <= 32 ? 32 : 64));
 }
 cudaError_t launch_linear_stream(const LinearStreamArgs &g, cudaStream_t st, int *launches);
-// x (behind the pre-norm) -> codes and scales, as moe_linear quantises it.
-cudaError_t launch_linear_quant(const uint16_t *x, int rows, int K, PreNorm pn, bool ue8m0, uint8_t *a,
-                                float *a_scales, cudaStream_t st, int *launches);
+// x -> codes and scales, as moe_linear quantises it; the same behind the
+// pre-norm x = bf16((h * rstd) * gamma), rstd as launch_rstd's.
+cudaError_t launch_linear_quant(const uint16_t *x, int rows, int K, bool ue8m0, uint8_t *a, float *a_scales,
+                                cudaStream_t st, int *launches);
+cudaError_t launch_linear_prenorm_quant(const uint16_t *h, const uint16_t *gamma, int rows, int K, float eps, bool ue8m0,
+                                        uint8_t *a, float *a_scales, cudaStream_t st, int *launches);
 // out [T, N] = sum of ksplit planes [T, ldp] in order (+ residual).
 cudaError_t launch_linear_finish(const float *partial, int ksplit, int T, int N, int ldp,
                                  const uint16_t *residual, void *out, int out_f32, cudaStream_t st,

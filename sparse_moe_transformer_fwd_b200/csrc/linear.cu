@@ -17,11 +17,15 @@
 //   warp 0      TMA producer: two K blocks a stage (two 16 KB boxes of W, two
 //               boxes of activations)
 //   warp 1      TMEM allocator and MMA issuer: a stage's two K blocks go to two
-//               adjacent accumulators of one of NBUF TMEM buffers
+//               adjacent accumulators; a stage is one wait and one commit
 //   warp 2      scales of each K block, copied to a ring in shared memory with
 //               cp.async (rows past T: zeros)
 //   warps 4-7   epilogue: thread = weight row; adds each accumulator, times its
 //               scale product, to the token sums in registers
+//   warps 8-12  (up to 16 tokens, bf16 input) quantise the stage's 1x128 tiles
+//               of x straight into the operand's swizzled rows; every CTA does
+//               it for the K blocks it reads, which costs less than a launch
+//               that writes the codes first
 // Every wait is bounded; on expiry the block records MOE_ERR_TIMEOUT, counts
 // itself in on its tiles without adding (so the counters return to zero),
 // drains its loads and MMAs, frees its TMEM and exits.
@@ -30,19 +34,21 @@
 #include "quant_math.cuh"
 
 #include <algorithm>
+#include <cstring>
 
 namespace moe {
 namespace {
 
-constexpr int LS_THREADS = 256;
 constexpr int W_BYTES = 128 * 128;  // one tile of weights
-constexpr int NBUF = 4;             // TMEM buffers of two accumulators
 constexpr int SC_RING = 8;          // scale slots (two K blocks each)
+constexpr int XQ_WARPS = 5;         // warps that quantise x
 
 template <int NT>
 struct LinearSmem {
     static constexpr int X_BYTES = NT * 128;
     static constexpr int STAGES = NT == 16 ? 6 : (NT == 32 ? 5 : 4);
+    static constexpr int TMEM_COLS = NT == 16 ? 256 : 512;  // two accumulators a stage
+    static_assert(STAGES * 2 * NT <= TMEM_COLS, "accumulators of the ring's stages");
     alignas(1024) uint8_t w[STAGES][2][W_BYTES];
     alignas(1024) uint8_t x[STAGES][2][X_BYTES];
     struct alignas(16) Scales {
@@ -50,9 +56,9 @@ struct LinearSmem {
         float w[2];
         float pad[2];
     } sc[SC_RING];
-    uint64_t full[STAGES], empty[STAGES];
+    uint64_t full[STAGES];  // operands landed, and the accumulators drained (4 warps)
+    uint64_t done[STAGES];  // MMAs done: accumulators to read, operands to overwrite
     uint64_t sfull[SC_RING], sempty[SC_RING];
-    uint64_t tfull[NBUF], tempty[NBUF];
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort;
@@ -60,6 +66,7 @@ struct LinearSmem {
 };
 
 struct LinearParams {
+    const uint16_t *x;         // [T, K] bf16, quantised here (with XQ)
     const float *a_scales, *w_scales;
     const uint16_t *residual;  // bf16 [T, N] or NULL
     void *out;                 // [T, N] bf16, or binary32 (out_f32)
@@ -69,6 +76,8 @@ struct LinearParams {
     int T, N, KB, tiles;
     int out_f32;
     int w_rowmajor;
+    int ue;       // power-of-two scales (with XQ)
+    int early_w;  // W may be read ahead of the kernel before this one
 };
 
 // K blocks [first, first + count) of one tile: a CTA's share of that tile.
@@ -93,56 +102,75 @@ __device__ __forceinline__ void store_out(const LinearParams &p, size_t at, floa
 }
 
 // Finishes a shared tile: the sums of its `shares` CTAs c0, c0 + 1, ... added
-// in that (K) order.  Warp q takes tokens q, q + 4, ..., lane l rows 4l .. 4l
-// + 3, and the loads of eight shares (or as many tokens) are in flight
-// together: one load at a time cost 0.5 us a share (6 us at one token, K =
-// 7168, N = 2112, against 3 us for the whole weight stream).
+// in that (K) order.  Warp q takes tokens q, q + 4, ... in groups of TG, lane l
+// rows 4l .. 4l + 3; 16 loads are in flight together, shares of one token or
+// tokens of a few shares (one at a time cost 0.5 us each: 6 us at one token, K
+// = 7168, N = 2112, against 3 us for the whole weight stream).
 template <int NT>
 __device__ __forceinline__ void add_shares(const LinearParams &p, long long U, int tile, int c0, int shares,
                                            int q, int lane) {
+    constexpr int TG = NT == 16 ? 2 : 4, SH = 16 / TG;
     const int KB = p.KB, G = gridDim.x;
     // Every share but the first one's begins on this tile: its first segment,
     // slot 0.  The first CTA's is its last segment unless it began here too.
     const int slot0 = share_begin(U, c0, G) / KB == tile ? 0 : 1;
     const float4 *base = reinterpret_cast<const float4 *>(p.partial) + static_cast<size_t>(c0) * 2 * NT * 32 + lane;
     const int n0 = tile * 128 + lane * 4;
-    for (int t = q; t < p.T; t += 4) {
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        uint16_t res[4] = {0, 0, 0, 0};
-        const size_t at = static_cast<size_t>(t) * p.N + n0;
-        if (p.residual)
+    for (int t0 = q; t0 < p.T; t0 += 4 * TG) {
+        float4 acc[TG];
+        uint16_t res[TG][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (n0 + i < p.N) res[i] = p.residual[at + i];
-        for (int c = 0; c < shares; c += 8) {
-            float4 v[8];
+        for (int g = 0; g < TG; ++g) {
+            acc[g] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (c + i < shares)
-                    v[i] = __ldcg(base + (static_cast<size_t>(c + i) * 2 + (c + i == 0 ? slot0 : 0)) * NT * 32 + t * 32);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (c + i >= shares) break;
-                acc.x = __fadd_rn(acc.x, v[i].x);
-                acc.y = __fadd_rn(acc.y, v[i].y);
-                acc.z = __fadd_rn(acc.z, v[i].z);
-                acc.w = __fadd_rn(acc.w, v[i].w);
+            for (int i = 0; i < 4; ++i) {
+                res[g][i] = 0;
+                if (p.residual && t0 + 4 * g < p.T && n0 + i < p.N)
+                    res[g][i] = p.residual[static_cast<size_t>(t0 + 4 * g) * p.N + n0 + i];
             }
         }
-        const float f[4] = {acc.x, acc.y, acc.z, acc.w};
+        for (int c = 0; c < shares; c += SH) {
+            float4 v[TG][SH];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (n0 + i < p.N) store_out(p, at + i, f[i], bf16_f(res[i]));
+            for (int g = 0; g < TG; ++g)
+#pragma unroll
+                for (int i = 0; i < SH; ++i)
+                    v[g][i] = t0 + 4 * g < p.T && c + i < shares
+                                  ? __ldcg(base + (static_cast<size_t>(c + i) * 2 + (c + i == 0 ? slot0 : 0)) * NT * 32 +
+                                           (t0 + 4 * g) * 32)
+                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int g = 0; g < TG; ++g)
+#pragma unroll
+                for (int i = 0; i < SH; ++i) {
+                    acc[g].x = __fadd_rn(acc[g].x, v[g][i].x);
+                    acc[g].y = __fadd_rn(acc[g].y, v[g][i].y);
+                    acc[g].z = __fadd_rn(acc[g].z, v[g][i].z);
+                    acc[g].w = __fadd_rn(acc[g].w, v[g][i].w);
+                }
+        }
+#pragma unroll
+        for (int g = 0; g < TG; ++g) {
+            if (t0 + 4 * g >= p.T) break;
+            const float f[4] = {acc[g].x, acc[g].y, acc[g].z, acc[g].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (n0 + i < p.N) store_out(p, static_cast<size_t>(t0 + 4 * g) * p.N + n0 + i, f[i], bf16_f(res[g][i]));
+        }
     }
 }
 
-template <int NT>
-__global__ void __launch_bounds__(LS_THREADS, 1)
+template <int NT, bool XQ>
+constexpr int ls_threads() { return XQ ? (8 + XQ_WARPS) * 32 : 256; }
+
+// NT token columns; XQ: x is given in bf16 and quantised here
+template <int NT, bool XQ>
+__global__ void __launch_bounds__((ls_threads<NT, XQ>()), 1)
 linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                      const __grid_constant__ CUtensorMap tmap_w, const LinearParams p) {
+    static_assert(!XQ || NT == 16, "x is quantised here for at most 16 tokens");
     using S = LinearSmem<NT>;
     constexpr int STAGES = S::STAGES;
-    constexpr int TMEM_COLS = NBUF * 2 * NT;  // 128, 256 or 512
     extern __shared__ uint8_t smem_raw[];
     S &s = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -152,16 +180,12 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
-            mbar_init(&s.full[i], 1);
-            mbar_init(&s.empty[i], 1);
+            mbar_init(&s.full[i], 1 + 4 + (XQ ? XQ_WARPS : 0));
+            mbar_init(&s.done[i], 1);
         }
         for (int i = 0; i < SC_RING; ++i) {
-            mbar_init(&s.sfull[i], 32);
+            mbar_init(&s.sfull[i], 32 + (XQ ? XQ_WARPS : 0));
             mbar_init(&s.sempty[i], 4);
-        }
-        for (int i = 0; i < NBUF; ++i) {
-            mbar_init(&s.tfull[i], 1);
-            mbar_init(&s.tempty[i], 4);
         }
         mbar_init(&s.mma_done, 1);
         s.abort = 0;
@@ -170,15 +194,18 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
         prefetch_tmap(&tmap_w);
     }
     if (warp == 1) {
-        tmem_alloc(&s.tmem_base, TMEM_COLS);
+        tmem_alloc(&s.tmem_base, S::TMEM_COLS);
         tmem_relinquish();
     }
-    pdl_wait_and_trigger();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem_base = s.tmem_base;
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, s.tmem_base, 0);
     volatile int *abort = &s.abort;
+    // The kernel before this one has finished when this returns; the producer
+    // alone may read W ahead of it (early_w).
+    if (!(warp == 0 && p.early_w)) pdl_wait();
+    pdl_trigger();
 
     auto next_segment = [&](long long &u, Segment &g) {
         if (u >= u1) return false;
@@ -190,27 +217,46 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
     };
 
     if (warp == 0) {
+        // One lane: coordinates advance by constants (every instruction of this
+        // loop costs a lone thread about five clocks).
         if (lane == 0) {
+            const uint32_t w_base = smem_u32(s.w[0][0]), x_base = smem_u32(s.x[0][0]), f_base = smem_u32(&s.full[0]);
+            const uint64_t policy = l2_evict_normal();
             int stage = 0;
             uint32_t phase = 0, armed = 0, armed_phase = 0;
-            bool ok = true;
+            bool ok = true, waited = !p.early_w;
+            int first_x[STAGES], first_n[STAGES], behind = 0;  // stages whose activations wait for the kernel before
+            auto load_x = [&](int st, int x0, int n) {
+                for (int j = 0; j < n; ++j)
+                    tma_load_2d_policy(x_base + (2 * st + j) * S::X_BYTES, &tmap_x, x0 + j * 128, 0, f_base + st * 8, policy);
+            };
+            auto catch_up = [&] {
+                pdl_wait();
+                waited = true;
+                for (int i = 0; i < behind; ++i) load_x(i, first_x[i], first_n[i]);
+            };
             long long u = u0;
             Segment g;
             while (ok && next_segment(u, g)) {
-                for (int kb = g.kb0; kb < g.kb0 + g.nk; kb += 2) {
-                    const int n = min(2, g.kb0 + g.nk - kb);
-                    if (!mbar_wait(&s.empty[stage], phase ^ 1, abort, p.status)) {
+                int wx = p.w_rowmajor ? g.kb0 * 128 : 0, wy = p.w_rowmajor ? g.tile * 128 : (g.tile * KB + g.kb0) * 128;
+                const int dx = p.w_rowmajor ? 128 : 0, dy = p.w_rowmajor ? 0 : 128;
+                int xx = g.kb0 * 128;
+                for (int left = g.nk; left > 0; left -= 2) {
+                    if (!waited && behind == STAGES) catch_up();
+                    if (!mbar_wait(&s.done[stage], phase ^ 1, abort, p.status)) {
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&s.full[stage], n * (W_BYTES + S::X_BYTES));
-                    for (int j = 0; j < n; ++j) {
-                        if (p.w_rowmajor)
-                            tma_load_2d(s.w[stage][j], &tmap_w, (kb + j) * 128, g.tile * 128, &s.full[stage]);
-                        else
-                            tma_load_2d(s.w[stage][j], &tmap_w, 0, (g.tile * KB + kb + j) * 128, &s.full[stage]);
-                        tma_load_2d(s.x[stage][j], &tmap_x, (kb + j) * 128, 0, &s.full[stage]);
+                    const int n = min(2, left);
+                    const uint32_t bar = f_base + stage * 8, w = w_base + stage * 2 * W_BYTES;
+                    mbar_arrive_expect_tx(&s.full[stage], n * (W_BYTES + (XQ ? 0 : S::X_BYTES)));
+                    tma_load_2d_policy(w, &tmap_w, wx, wy, bar, policy);
+                    if (n == 2) tma_load_2d_policy(w + W_BYTES, &tmap_w, wx + dx, wy + dy, bar, policy);
+                    if constexpr (!XQ) {
+                        if (waited) load_x(stage, xx, n);
+                        else first_x[behind] = xx, first_n[behind] = n, ++behind;  // the ring's first round: slot = behind
                     }
+                    wx += 2 * dx, wy += 2 * dy, xx += 256;
                     armed |= 1u << stage;
                     armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
                     if (++stage == STAGES) {
@@ -219,6 +265,7 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                     }
                 }
             }
+            if (!waited) catch_up();
             // drain: every load issued has landed before the block exits
             const long long t0 = clock64();
             for (int i = 0; i < STAGES; ++i) {
@@ -232,54 +279,52 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = instr_desc<true>(128, NT);
-            int stage = 0, tb = 0;
-            uint32_t phase = 0, tphase = 0;
-            bool ok = true;
-            long long u = u0;
-            Segment g;
-            while (ok && next_segment(u, g)) {
-                for (int i = 0; i < g.nk; i += 2) {
-                    const int n = min(2, g.nk - i);
-                    if (!mbar_wait(&s.tempty[tb], tphase ^ 1, abort, p.status) ||
-                        !mbar_wait(&s.full[stage], phase, abort, p.status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    for (int j = 0; j < n; ++j) {
-                        const uint32_t d = tmem_base + (2 * tb + j) * NT;
-                        const uint64_t wd = smem_desc_sw128(smem_u32(s.w[stage][j]));
-                        const uint64_t xd = smem_desc_sw128(smem_u32(s.x[stage][j]));
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) tc_mma<true>(d, wd + 2 * kk, xd + 2 * kk, idesc, kk != 0);
-                    }
-                    tc_commit(&s.empty[stage]);
-                    tc_commit(&s.tfull[tb]);
-                    if (++tb == NBUF) {
-                        tb = 0;
-                        tphase ^= 1;
-                    }
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
-                }
-            }
-            // all MMAs issued are complete before TMEM is freed
-            tc_commit(&s.mma_done);
-            const long long t0 = clock64();
-            while (!mbar_try_wait(&s.mma_done, 0)) {
-                if (clock64() - t0 > kWaitBudgetCycles) {
-                    set_status(p.status, MOE_ERR_TIMEOUT);
+        constexpr uint32_t idesc = instr_desc<true>(128, NT);
+        const uint64_t wd0 = smem_desc_sw128(smem_u32(s.w[0][0])), xd0 = smem_desc_sw128(smem_u32(s.x[0][0]));
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        long long u = u0;
+        Segment g;
+        while (ok && next_segment(u, g)) {
+            for (int left = g.nk; left > 0; left -= 2) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&s.full[stage], phase, abort, p.status))) {
+                    ok = false;
                     break;
                 }
+                tc_fence_after();
+                const uint32_t d = tmem_base + 2 * stage * NT;
+                const uint64_t wd = wd0 + stage * (2 * W_BYTES >> 4), xd = xd0 + stage * (2 * S::X_BYTES >> 4);
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) tc_mma<true>(d, wd + 2 * kk, xd + 2 * kk, idesc, kk != 0);
+                    if (left > 1)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc_mma<true>(d + NT, wd + (W_BYTES >> 4) + 2 * kk, xd + (S::X_BYTES >> 4) + 2 * kk, idesc, kk != 0);
+                    tc_commit(&s.done[stage]);
+                }
+                __syncwarp();
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        // all MMAs issued are complete before TMEM is freed (the same lane is
+        // elected every time, and a commit covers that lane's MMAs)
+        if (elect_one()) tc_commit(&s.mma_done);
+        __syncwarp();
+        const long long t0 = clock64();
+        while (!mbar_try_wait(&s.mma_done, 0)) {
+            if (clock64() - t0 > kWaitBudgetCycles) {
+                set_status(p.status, MOE_ERR_TIMEOUT);
+                break;
             }
         }
     } else if (warp == 2) {
         // lane l copies the scales of tokens l, l + 32 (of both K blocks) and
-        // lanes 0, 1 the weights' (their barrier counts 32 arrivals, one a
+        // lanes 0, 1 the weights' (32 arrivals on the slot's barrier, one a
         // lane, each made when that lane's copies have landed)
         int slot = 0;
         uint32_t phase = 0;
@@ -289,19 +334,18 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
         while (ok && next_segment(u, g)) {
             for (int kb = g.kb0; kb < g.kb0 + g.nk; kb += 2) {
                 const int n = min(2, g.kb0 + g.nk - kb);
-                int go = 1;
-                if (lane == 0) go = mbar_wait(&s.sempty[slot], phase ^ 1, abort, p.status) ? 1 : 0;
-                if (__shfl_sync(0xffffffffu, go, 0) == 0) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&s.sempty[slot], phase ^ 1, abort, p.status))) {
                     ok = false;
                     break;
                 }
-                for (int j = 0; j < n; ++j) {
-                    for (int t = lane; t < NT; t += 32) {
-                        const bool in = t < p.T;
-                        cp_async4(&s.sc[slot].x[j][t],
-                                  p.a_scales + (in ? static_cast<size_t>(t) * KB + kb + j : 0), in);
+                if constexpr (!XQ)
+                    for (int j = 0; j < n; ++j) {
+                        for (int t = lane; t < NT; t += 32) {
+                            const bool in = t < p.T;
+                            cp_async4(&s.sc[slot].x[j][t],
+                                      p.a_scales + (in ? static_cast<size_t>(t) * KB + kb + j : 0), in);
+                        }
                     }
-                }
                 if (lane < n)
                     cp_async4(&s.sc[slot].w[lane], p.w_scales + static_cast<size_t>(g.tile) * KB + kb + lane, true);
                 cp_async_mbar_arrive(&s.sfull[slot]);
@@ -312,13 +356,95 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
             }
         }
         cp_async_wait_all();
-    } else if (warp >= 4) {
+    } else if (XQ && warp >= 8) {
+        // Half-warps over the stage's (K block, token) tiles, up to PER each;
+        // the next stage's vectors are loaded before this stage's are encoded.
+        // Lane l16 of a half writes codes 8 l16 .. 8 l16 + 7 of its token's
+        // 128-byte row, 16-byte chunks XOR-swizzled by the row as the TMA does.
+        constexpr int HALVES = 2 * XQ_WARPS, PER = (2 * 16 + HALVES - 1) / HALVES;
+        const int half = (warp - 8) * 2 + (lane >> 4), l16 = lane & 15, T = p.T;
+        struct Cursor {
+            long long u;
+            Segment g;
+            int i;
+            bool more;
+        } at{u0, {}, 0, true}, ahead{u0, {}, 0, true};
+        auto step = [&](Cursor &c) {  // to the next stage
+            c.i += 2;
+            if (c.i >= c.g.nk) {
+                c.i = 0;
+                c.more = next_segment(c.u, c.g);
+            }
+        };
+        at.more = next_segment(at.u, at.g);
+        ahead = at;
+        uint4 v[PER], next[PER];
+        int block[PER], token[PER];  // of tile half + i * HALVES of any stage
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            block[i] = (half + i * HALVES) / T;
+            token[i] = half + i * HALVES - block[i] * T;
+        }
+        auto load = [&](const Cursor &c, uint4 (&r)[PER]) {
+            const int n = c.more ? min(2, c.g.nk - c.i) * T : 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                if (half + i * HALVES < n)
+                    r[i] = __ldg(reinterpret_cast<const uint4 *>(
+                        p.x + static_cast<size_t>(token[i]) * (KB * 128) + (c.g.kb0 + c.i + block[i]) * 128 + l16 * 8));
+            }
+        };
+        load(ahead, next);
+        int stage = 0, slot = 0;
+        uint32_t phase = 0, sphase = 0;
+        while (at.more) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) v[i] = next[i];
+            step(ahead);
+            load(ahead, next);
+            const int n = min(2, at.g.nk - at.i) * T;
+            if (!__all_sync(0xffffffffu, mbar_wait(&s.sempty[slot], sphase ^ 1, abort, p.status) &&
+                                             mbar_wait(&s.done[stage], phase ^ 1, abort, p.status)))
+                break;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int tile = half + i * HALVES;
+                if ((half & ~1) + i * HALVES >= n) break;  // the whole warp
+                float f[8];
+                widen8(v[i], f);
+                uint2 code;
+                const float sc = quant_tile8(f, p.ue, &code);
+                if (tile < n) {
+                    const int j = block[i], t = token[i];
+                    *reinterpret_cast<uint2 *>(s.x[stage][j] + t * 128 + (((l16 >> 1) ^ (t & 7)) << 4) + (l16 & 1) * 8) = code;
+                    if (l16 == 0) s.sc[slot].x[j][t] = sc;
+                }
+            }
+            fence_proxy_async_smem();  // the MMA reads the codes
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&s.full[stage]);
+                mbar_arrive(&s.sfull[slot]);
+            }
+            step(at);
+            if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1;
+            }
+            if (++slot == SC_RING) {
+                slot = 0;
+                sphase ^= 1;
+            }
+        }
+    } else if (warp >= 4 && warp < 8) {
         const int q = warp & 3;
         const int r = q * 32 + lane;  // weight row of the tile
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-        int tb = 0, slot = 0;
-        uint32_t tphase = 0, sphase = 0;
+        int stage = 0, slot = 0;
+        uint32_t phase = 0, sphase = 0;
         bool ok = true, first = true;
+        if (lane < STAGES) mbar_arrive(&s.full[lane]);  // the accumulators are free
+        __syncwarp();
         long long u = u0;
         Segment g;
         while (next_segment(u, g)) {
@@ -328,18 +454,14 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
             for (int i = 0; i < g.nk && ok; i += 2) {
                 const bool both = i + 1 < g.nk;
                 const bool ready = mbar_wait(&s.sfull[slot], sphase, abort, p.status) &&
-                                   mbar_wait(&s.tfull[tb], tphase, abort, p.status);
+                                   mbar_wait(&s.done[stage], phase, abort, p.status);
                 if (!__all_sync(0xffffffffu, ready)) {  // the loads below are warp-wide
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const auto &sc = s.sc[slot];
-#pragma unroll
-                for (int c = 0; c < 2 * NT; c += 32) {
-                    float v[32];
-                    tmem_ld32(lane_base + 2 * tb * NT + c, v);
-                    tmem_wait_ld(v);
+                auto add = [&](const float (&v)[32], int c) {
                     // 32 columns: both K blocks' 16 tokens, or 32 tokens of one
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
@@ -353,16 +475,36 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                             acc[t + 3] = __fmaf_rn(v[e + 3], __fmul_rn(sx.w, sw), acc[t + 3]);
                         }
                     }
+                };
+                if constexpr (NT == 16) {
+                    float v[32];
+                    tmem_ld32(lane_base + 2 * stage * NT, v);
+                    tmem_wait_ld(v);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.full[stage]);
+                    add(v, 0);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 2 * NT; c += 64) {
+                        float v0[32], v1[32];
+                        tmem_ld32(lane_base + 2 * stage * NT + c, v0);
+                        tmem_ld32(lane_base + 2 * stage * NT + c + 32, v1);
+                        tmem_wait_ld(v0, v1);
+                        if (c + 64 == 2 * NT) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&s.full[stage]);
+                        }
+                        add(v0, c);
+                        add(v1, c + 32);
+                    }
                 }
-                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&s.tempty[tb]);
-                    mbar_arrive(&s.sempty[slot]);
-                }
-                if (++tb == NBUF) {
-                    tb = 0;
-                    tphase ^= 1;
+                if (lane == 0) mbar_arrive(&s.sempty[slot]);
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1;
                 }
                 if (++slot == SC_RING) {
                     slot = 0;
@@ -395,18 +537,16 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                     for (int t = 0; t < NT; ++t)
                         if (t < p.T) mine[t * 128] = acc[t];
                 }
-                __threadfence();
                 named_bar_sync(1, 128);
                 if (threadIdx.x == 128) {
+                    __threadfence();  // (covers what the barrier orders before it)
                     const int last = atomicAdd(p.counters + g.tile, 1) == shares - 1;
                     if (last) p.counters[g.tile] = 0;  // everyone has counted: zero for the next launch
+                    __threadfence();
                     s.last = last;
                 }
                 named_bar_sync(1, 128);
-                if (ok && s.last) {
-                    __threadfence();
-                    add_shares<NT>(p, U, g.tile, c0, shares, q, lane);
-                }
+                if (ok && s.last) add_shares<NT>(p, U, g.tile, c0, shares, q, lane);
                 named_bar_sync(1, 128);  // s.last is rewritten by the next shared tile
             }
             first = false;
@@ -417,15 +557,15 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, TMEM_COLS);
+        tmem_dealloc(tmem_base, S::TMEM_COLS);
     }
 }
 
-// x [rows, K] bf16 (behind the pre-norm, with rstd set) -> codes and scales of
-// its 1x128 tiles, 16 lanes a tile (tile_scale has the arithmetic).
+// x [rows, K] bf16 -> codes and scales of its 1x128 tiles, 16 lanes a tile
+// (tile_scale has the arithmetic).
 __global__ void __launch_bounds__(256)
-linear_quant_kernel(const uint16_t *__restrict__ x, int rows, int K, PreNorm pn, int ue,
-                    uint8_t *__restrict__ a, float *__restrict__ a_scales) {
+linear_quant_kernel(const uint16_t *__restrict__ x, int rows, int K, int ue, uint8_t *__restrict__ a,
+                    float *__restrict__ a_scales) {
     pdl_wait_and_trigger();
     const int KB = K / 128, l16 = threadIdx.x % 16;
     const long long tiles = static_cast<long long>(rows) * KB;
@@ -434,15 +574,36 @@ linear_quant_kernel(const uint16_t *__restrict__ x, int rows, int K, PreNorm pn,
     for (long long i0 = static_cast<long long>(blockIdx.x) * 16 + (threadIdx.x / 32) * 2; i0 < tiles; i0 += step) {
         const long long i = i0 + (threadIdx.x / 16 & 1);
         const bool in = i < tiles;
-        const int t = in ? static_cast<int>(i / KB) : 0;
-        const int c = (in ? static_cast<int>(i - static_cast<long long>(t) * KB) : 0) * 128 + l16 * 8;
         float v[8];
-        load_x8(x, t, c, K, pn, v);
+        widen8(in ? *reinterpret_cast<const uint4 *>(x + i * 128 + l16 * 8) : make_uint4(0, 0, 0, 0), v);
         uint2 code;
         const float sc = quant_tile8(v, ue, &code);
         if (!in) continue;
-        *reinterpret_cast<uint2 *>(a + static_cast<size_t>(t) * K + c) = code;
+        *reinterpret_cast<uint2 *>(a + i * 128 + l16 * 8) = code;
         if (l16 == 0) a_scales[i] = sc;
+    }
+}
+
+// The same behind the pre-norm, a block a token: x = bf16((h * rstd) * gamma).
+__global__ void __launch_bounds__(256)
+linear_prenorm_quant_kernel(const uint16_t *__restrict__ h, const uint16_t *__restrict__ gamma, int K, float eps, int ue,
+                            uint8_t *__restrict__ a, float *__restrict__ a_scales) {
+    __shared__ __align__(16) uint16_t chunk[kRstdChunk];
+    __shared__ float rstd_sh;
+    const size_t t = blockIdx.x;
+    const uint16_t *row = h + t * K;
+    pdl_wait_and_trigger();
+    const float rstd = block_rstd(row, K, eps, chunk, &rstd_sh);
+    const int KB = K / 128, l16 = threadIdx.x % 16;
+    for (int i0 = threadIdx.x / 32 * 2; i0 < KB; i0 += 16) {
+        const int i = i0 + (threadIdx.x / 16 & 1);
+        float v[8] = {};
+        if (i < KB) prenorm8(row, gamma, i * 128 + l16 * 8, rstd, v);
+        uint2 code;
+        const float sc = quant_tile8(v, ue, &code);
+        if (i >= KB) continue;
+        *reinterpret_cast<uint2 *>(a + t * K + i * 128 + l16 * 8) = code;
+        if (l16 == 0) a_scales[t * KB + i] = sc;
     }
 }
 
@@ -502,23 +663,25 @@ linear_finish_kernel(const float *__restrict__ partial, int ksplit, int T, int N
     }
 }
 
-template <int NT>
+template <int NT, bool XQ>
 cudaError_t launch_stream_t(const LinearStreamArgs &g, cudaStream_t st) {
     CUtensorMap mx, mw;
     const int tiles = (g.N + 127) / 128, KB = g.K / 128;
-    if (!make_map_2d(&mx, g.a, true, g.K, g.T, NT)) return cudaErrorInvalidValue;
+    std::memset(&mx, 0, sizeof mx);
+    if (!XQ && !make_map_2d(&mx, g.a, true, g.K, g.T, NT)) return cudaErrorInvalidValue;
     if (g.w_rowmajor ? !make_map_2d(&mw, g.w, true, g.K, g.N) : !make_map_2d(&mw, g.w, true, 128, tiles * KB * 128))
         return cudaErrorInvalidValue;
     constexpr size_t smem = sizeof(LinearSmem<NT>) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory budget of one CTA");
     static DeviceConfigured configured{};
     if (first_use_on_device(configured)) {
-        const cudaError_t e = cudaFuncSetAttribute(linear_stream_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t e = cudaFuncSetAttribute(linear_stream_kernel<NT, XQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(smem));
         if (e != cudaSuccess) return e;
         mark_used_on_device(configured);
     }
     LinearParams p{};
+    p.x = g.x;
     p.a_scales = g.a_scales;
     p.w_scales = g.w_scales;
     p.residual = g.residual;
@@ -532,28 +695,42 @@ cudaError_t launch_stream_t(const LinearStreamArgs &g, cudaStream_t st) {
     p.tiles = tiles;
     p.out_f32 = g.out_f32;
     p.w_rowmajor = g.w_rowmajor;
+    p.ue = g.ue8m0;
+    p.early_w = g.early_w;
     const long long units = static_cast<long long>(tiles) * KB;
     const int grid = static_cast<int>(std::min<long long>(units, std::min(num_sms(), kLinearMaxCtas)));
-    return launch_pdl(linear_stream_kernel<NT>, dim3(grid), dim3(LS_THREADS), smem, st, mx, mw, p);
+    return launch_pdl(linear_stream_kernel<NT, XQ>, dim3(grid), dim3(ls_threads<NT, XQ>()), smem, st, mx, mw, p);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_stream(const LinearStreamArgs &g, cudaStream_t st, int *launches) {
-    if (g.T < 1 || g.T > kLinearStreamRows) return cudaErrorInvalidValue;
+    if (g.T < 1 || g.T > (g.x ? kLinearQuantRows : kLinearStreamRows)) return cudaErrorInvalidValue;
     mark_launch(st, *launches, "linear_stream");
-    LAUNCH_OR_RETURN(g.T <= 16 ? launch_stream_t<16>(g, st)
-                               : (g.T <= 32 ? launch_stream_t<32>(g, st) : launch_stream_t<64>(g, st)));
+    cudaError_t e;
+    if (g.x) e = launch_stream_t<16, true>(g, st);
+    else if (g.T <= 16) e = launch_stream_t<16, false>(g, st);
+    else if (g.T <= 32) e = launch_stream_t<32, false>(g, st);
+    else e = launch_stream_t<64, false>(g, st);
+    LAUNCH_OR_RETURN(e);
     ++*launches;
     return cudaGetLastError();
 }
 
-cudaError_t launch_linear_quant(const uint16_t *x, int rows, int K, PreNorm pn, bool ue8m0, uint8_t *a,
-                                float *a_scales, cudaStream_t st, int *launches) {
+cudaError_t launch_linear_quant(const uint16_t *x, int rows, int K, bool ue8m0, uint8_t *a, float *a_scales,
+                                cudaStream_t st, int *launches) {
     mark_launch(st, *launches, "linear_quant");
     const long long want = (static_cast<long long>(rows) * (K / 128) + 15) / 16;
     const int grid = static_cast<int>(std::min<long long>(want, num_sms() * 16LL));
-    LAUNCH_OR_RETURN(launch_pdl(linear_quant_kernel, dim3(grid), dim3(256), 0, st, x, rows, K, pn, ue8m0 ? 1 : 0, a,
+    LAUNCH_OR_RETURN(launch_pdl(linear_quant_kernel, dim3(grid), dim3(256), 0, st, x, rows, K, ue8m0 ? 1 : 0, a, a_scales));
+    ++*launches;
+    return cudaGetLastError();
+}
+
+cudaError_t launch_linear_prenorm_quant(const uint16_t *h, const uint16_t *gamma, int rows, int K, float eps, bool ue8m0,
+                                        uint8_t *a, float *a_scales, cudaStream_t st, int *launches) {
+    mark_launch(st, *launches, "linear_prenorm_quant");
+    LAUNCH_OR_RETURN(launch_pdl(linear_prenorm_quant_kernel, dim3(rows), dim3(256), 0, st, h, gamma, K, eps, ue8m0 ? 1 : 0, a,
                                 a_scales));
     ++*launches;
     return cudaGetLastError();

@@ -27,24 +27,13 @@ __device__ __forceinline__ float tile_scale(float amax, bool ue, float *inv) {
     return __fmul_rn(amax, static_cast<float>(1.0 / 448.0));
 }
 
-// Eight consecutive columns c .. c + 7 of token t: bf16 inputs, or the pre-norm
-// of the residual stream.
-__device__ __forceinline__ void load_x8(const uint16_t *x, int t, int c, int K, const PreNorm &pn, float (&v)[8]) {
-    const uint4 raw = *reinterpret_cast<const uint4 *>(x + static_cast<size_t>(t) * K + c);
+// Eight consecutive bf16 columns, widened.
+__device__ __forceinline__ void widen8(const uint4 &raw, float (&v)[8]) {
     const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         v[2 * i] = bf16_lo(r[i]);
         v[2 * i + 1] = bf16_hi(r[i]);
-    }
-    if (!pn.gamma) return;
-    const float rs = pn.rstd[t];
-    const uint4 graw = *reinterpret_cast<const uint4 *>(pn.gamma + c);
-    const uint32_t g[4] = {graw.x, graw.y, graw.z, graw.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = prenorm_elem(v[2 * i], rs, bf16_lo(g[i]));
-        v[2 * i + 1] = prenorm_elem(v[2 * i + 1], rs, bf16_hi(g[i]));
     }
 }
 
@@ -63,6 +52,50 @@ __device__ __forceinline__ float quant_tile8(const float (&v)[8], bool ue, uint2
     for (int i = 0; i < 4; ++i) c[i] = e4m3x2(__fmul_rn(v[2 * i], inv), __fmul_rn(v[2 * i + 1], inv));
     *code = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
     return sc;
+}
+
+// 1 / sqrt(mean of the squares of a row + eps) as rstd_kernel defines it: lane l
+// of one warp sums the squares of columns l mod 32 in order, five butterfly
+// rounds add the lanes.  The block stages the row in shared memory for that
+// warp (chunk: kRstdChunk columns; d a multiple of 128): 1 us at d = 7168,
+// where the warp's own loads from L2 take ten.  Every thread returns it; the
+// row's last chunk stays in `chunk`.
+constexpr int kRstdChunk = 8192;
+__device__ __forceinline__ float block_rstd(const uint16_t *row, int d, float eps, uint16_t *chunk, float *shared) {
+    float acc = 0.0f;
+    for (int c = 0; c < d; c += kRstdChunk) {
+        const int n = min(kRstdChunk, d - c);
+        for (int v = threadIdx.x; v < n / 8; v += blockDim.x)
+            reinterpret_cast<uint4 *>(chunk)[v] = reinterpret_cast<const uint4 *>(row + c)[v];
+        __syncthreads();
+        if (threadIdx.x < 32) {
+#pragma unroll 8
+            for (int i = threadIdx.x; i < n; i += 32) {
+                const float v = __uint_as_float(static_cast<uint32_t>(chunk[i]) << 16);
+                acc = __fmaf_rn(v, v, acc);
+            }
+        }
+        if (c + kRstdChunk < d) __syncthreads();
+    }
+    if (threadIdx.x < 32) {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) acc = __fadd_rn(acc, __shfl_xor_sync(0xffffffffu, acc, off));
+        if (threadIdx.x == 0)
+            *shared = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(acc, static_cast<float>(d)), eps)));
+    }
+    __syncthreads();
+    return *shared;
+}
+
+// Eight pre-normed columns of a row.
+__device__ __forceinline__ void prenorm8(const uint16_t *row, const uint16_t *gamma, int c, float rstd, float (&v)[8]) {
+    const uint4 raw = *reinterpret_cast<const uint4 *>(row + c), graw = *reinterpret_cast<const uint4 *>(gamma + c);
+    const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w}, g[4] = {graw.x, graw.y, graw.z, graw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = prenorm_elem(bf16_lo(r[i]), rstd, bf16_lo(g[i]));
+        v[2 * i + 1] = prenorm_elem(bf16_hi(r[i]), rstd, bf16_hi(g[i]));
+    }
 }
 
 }  // namespace moe

@@ -230,7 +230,11 @@ def test_weights_written_just_before():
 
 def test_launches():
     x, lin, w, _ = _inputs(8, 512, 640, "fp8", "tiled", seed=1)
-    lin(x.to(DEV))
+    lin(x.to(DEV))  # up to 16 tokens: quantised in the product's kernel
+    assert moe.moe_last_launch_names() == ["linear_stream"]
+    lin.forward_prenorm(x.to(DEV), torch.ones(512, dtype=torch.bfloat16, device=DEV))
+    assert moe.moe_last_launch_names() == ["linear_prenorm_quant", "linear_stream"]
+    lin(torch.zeros(17, 512, dtype=torch.bfloat16, device=DEV))
     assert moe.moe_last_launch_names() == ["linear_quant", "linear_stream"]
     lin(x.to(DEV)[:0])
     assert moe.moe_last_launch_count() == 0
