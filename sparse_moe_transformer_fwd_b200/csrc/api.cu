@@ -1149,7 +1149,7 @@ namespace {
 // zero-filled workspace serves linears of any shapes: each launch leaves the
 // counters zero, and no other region of another shape reaches them.
 constexpr int kLinearMaxN = 1 << 20;
-constexpr size_t kLinearCounterBytes = kLinearMaxN / 128 * sizeof(int);
+constexpr size_t kLinearCounterBytes = kLinearMaxCtas * sizeof(int);
 constexpr int kLinearSplitRows = 256;  // as the dense down GEMM: K split up to here
 
 int check_linear_shape(const moe_linear_shape *s) {
@@ -1178,6 +1178,16 @@ int linear_padded_n(const moe_linear_shape *s) { return (s->N + 255) / 256 * 256
 // Sums in binary32 and a finishing kernel where the tiled GEMM cannot store
 // the output itself (256 bf16 columns a tile).
 bool linear_direct(const moe_linear_shape *s) { return s->N % 256 == 0 && !s->out_f32; }
+
+// x is quantised in the product's kernel for at most kLinearQuantRows tokens
+// and shares of at most 16 K blocks a CTA: every CTA quantises what it reads,
+// which a long stream waits for (7 tokens, 7168 x 64007: 189 blocks a CTA, 91 us
+// so against 81) and a short one hides (one launch less).
+bool linear_quantises(const moe_linear_shape *s) {
+    const int tiles = (s->N + 127) / 128, KB = s->K / 128;
+    return s->T <= kLinearQuantRows &&
+           static_cast<long long>(tiles) * KB <= 16LL * linear_plan(s->T, tiles, KB).grid;
+}
 
 // K ranges of the tiled GEMM, by the dense down GEMM's rule: few output tiles
 // leave SMs idle, so up to kMaxSplitK ranges of at least two K blocks.
@@ -1309,7 +1319,7 @@ int linear_impl(const char *name, const moe_linear_shape *s, const uint16_t *x, 
     const bool ue = s->precision == MOE_FP8_UE8M0;
     uint8_t *a = at<uint8_t>(ws, L.a);
     float *a_scales = at<float>(ws, L.a_scales);
-    const bool in_product = !codes && !gamma && s->T <= kLinearQuantRows;
+    const bool in_product = !codes && !gamma && linear_quantises(s);
     if (gamma)
         LAUNCH(launch_linear_prenorm_quant(x, gamma, s->T, s->K, eps, ue, a, a_scales, st, &n), "pre-norm and quantise");
     else if (!codes && !in_product)

@@ -1057,7 +1057,7 @@ few_prenorm_kernel(const uint16_t *__restrict__ h, const uint16_t *__restrict__ 
     const float rstd = block_rstd(row, d, eps, chunk, &rstd_sh);
     for (int v = threadIdx.x; v < d / 8; v += blockDim.x) {
         float x[8];
-        prenorm8(row, gamma, v * 8, rstd, x);
+        prenorm8(reinterpret_cast<const uint4 *>(row)[v], reinterpret_cast<const uint4 *>(gamma)[v], rstd, x);
         reinterpret_cast<uint4 *>(xn + static_cast<size_t>(blockIdx.x) * d)[v] =
             make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
     }

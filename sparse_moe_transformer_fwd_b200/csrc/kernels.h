@@ -202,9 +202,15 @@ cudaError_t launch_few_prenorm(const uint16_t *h, const uint16_t *gamma, int T, 
                                cudaStream_t st, int *launches);
 cudaError_t launch_few(const FewArgs &g, cudaStream_t st, int *launches);
 
-// Block-scaled product of at most kLinearStreamRows rows of codes (linear.cu).
+// Block-scaled product that streams the weights, for at most kLinearStreamRows
+// tokens (linear.cu).
 constexpr int kLinearStreamRows = 64;
 constexpr int kLinearMaxCtas = 160;  // CTAs of linear_stream (sizes its partial sums)
+// rounds of whole tiles, one a CTA; then `rest` tiles of `parts` parts each.
+struct LinearPlan {
+    int grid, rounds, rest, parts;
+};
+LinearPlan linear_plan(int T, int tiles, int KB);
 constexpr int kLinearQuantRows = 16;  // and of bf16 x, quantised in the same kernel
 struct LinearStreamArgs {
     const uint16_t *x;         // bf16 [T, K], or NULL: a and a_scales
@@ -215,7 +221,7 @@ struct LinearStreamArgs {
     const uint16_t *residual;  // bf16 [T, N] or NULL
     void *out;                 // [T, N] bf16, or binary32 with out_f32
     float *partial;            // linear_partial_floats(T)
-    int *counters;             // [ceil(N/128)], zero; left zero
+    int *counters;             // [kLinearMaxCtas], zero; left zero
     int *status;
     int T, K, N;
     int out_f32, w_rowmajor;
@@ -223,7 +229,7 @@ struct LinearStreamArgs {
     int early_w;  // an earlier launch of the same call has waited for the stream: W may be read ahead
 };
 inline size_t linear_partial_floats(int T) {
-    return static_cast<size_t>(kLinearMaxCtas) * 2 * 128 * (T <= 16 ? 16 : (T <= 32 ? 32 : 64));
+    return static_cast<size_t>(kLinearMaxCtas) * 128 * (T <= 16 ? 16 : (T <= 32 ? 32 : 64));
 }
 cudaError_t launch_linear_stream(const LinearStreamArgs &g, cudaStream_t st, int *launches);
 // x -> codes and scales, as moe_linear quantises it; the same behind the

@@ -5,27 +5,26 @@
 // K block accumulated by the tensor core and added in binary32, as in the
 // grouped expert GEMMs.
 //
-// Up to 64 tokens the product reads each weight byte for at most 128 FLOP, so
-// it is bound by HBM: N*K bytes of weights.  The weights are therefore the M
-// operand of the MMA (128 rows of W a tile, tokens the N operand: 16, 32 or 64
-// columns), and what is split over the SMs is the weight stream itself: its
-// (tile, K block) pairs are numbered tile by tile and every CTA takes an equal,
-// contiguous share, whatever N and K are.  A tile that several CTAs share is
-// finished by whichever of them is last: each stores its binary32 partial sums
-// in the workspace and counts itself in; the last one adds them in K order, so
-// the result does not depend on timing.
-//   warp 0      TMA producer: two K blocks a stage (two 16 KB boxes of W, two
+// Few tokens read each weight byte for few FLOP, so the product is bound by
+// HBM: N*K bytes of weights.  The weights are therefore the M operand of the MMA
+// (128 rows of W a tile, tokens the N operand: 16, 32 or 64 columns), and the
+// tiles go to the CTAs in turn.  The tiles of the last, partial round (all of
+// them, where there are fewer than SMs) are cut into equal parts of K, as many
+// as pay (linear_plan); each part's CTA stores its binary32 partial sums in the
+// workspace and counts itself in, and the last one adds them in K order, so the
+// result does not depend on timing.
+//   warp 0      TMA producer: a stage is two K blocks (two 16 KB boxes of W, two
 //               boxes of activations)
-//   warp 1      TMEM allocator and MMA issuer: a stage's two K blocks go to two
-//               adjacent accumulators; a stage is one wait and one commit
+//   warp 1      TMEM allocator and MMA issuer: a stage's K blocks go to adjacent
+//               accumulators; a stage is one wait and one commit
 //   warp 2      scales of each K block, copied to a ring in shared memory with
 //               cp.async (rows past T: zeros)
 //   warps 4-7   epilogue: thread = weight row; adds each accumulator, times its
 //               scale product, to the token sums in registers
-//   warps 8-12  (up to 16 tokens, bf16 input) quantise the stage's 1x128 tiles
-//               of x straight into the operand's swizzled rows; every CTA does
-//               it for the K blocks it reads, which costs less than a launch
-//               that writes the codes first
+//   warps 8-12  (at most 16 tokens of bf16 input, short shares) quantise the
+//               stage's 1x128 tiles of x straight into the operand's swizzled
+//               rows; every CTA does it for the K blocks it reads, which costs
+//               less than a launch that writes the codes first
 // Every wait is bounded; on expiry the block records MOE_ERR_TIMEOUT, counts
 // itself in on its tiles without adding (so the counters return to zero),
 // drains its loads and MMAs, frees its TMEM and exits.
@@ -70,75 +69,64 @@ struct LinearParams {
     const float *a_scales, *w_scales;
     const uint16_t *residual;  // bf16 [T, N] or NULL
     void *out;                 // [T, N] bf16, or binary32 (out_f32)
-    float *partial;            // [gridDim.x][2][NT][128]
-    int *counters;             // [tiles], zero between launches
+    float *partial;            // [gridDim.x][NT][128]
+    int *counters;             // [gridDim.x], zero between launches
     int *status;
-    int T, N, KB, tiles;
+    int T, N, KB;
+    int rounds;   // whole tiles of every CTA: tile round * gridDim.x + CTA
+    int rest;     // tiles of the last round
+    int parts;    // parts of K of each of those
     int out_f32;
     int w_rowmajor;
     int ue;       // power-of-two scales (with XQ)
     int early_w;  // W may be read ahead of the kernel before this one
 };
 
-// K blocks [first, first + count) of one tile: a CTA's share of that tile.
+// K blocks kb0 .. kb0 + nk - 1 of one tile.
 struct Segment {
     int tile, kb0, nk;
 };
 
-// The share [u0, u1) of CTA c among G: (tile, K block) pairs in tile order.
-__device__ __forceinline__ long long share_begin(long long U, int c, int G) { return U * c / G; }
-// The CTA whose share holds pair u.
-__device__ __forceinline__ int share_of(long long U, long long u, int G) {
-    return static_cast<int>(((u + 1) * G + U - 1) / U) - 1;
-}
-
 __device__ __forceinline__ float bf16_f(uint16_t v) {
     return __uint_as_float(static_cast<uint32_t>(v) << 16);
 }
-__device__ __forceinline__ void store_out(const LinearParams &p, size_t at, float v, float res) {
-    if (p.residual) v = __fadd_rn(v, res);
-    if (p.out_f32) static_cast<float *>(p.out)[at] = v;
-    else static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(v);
-}
+// Where a tile's sums go.
+struct LinearOut {
+    const uint16_t *residual;
+    void *out;
+    int T, N, f32;
+    __device__ __forceinline__ void store(size_t at, float v, float res) const {
+        if (residual) v = __fadd_rn(v, res);
+        if (f32) static_cast<float *>(out)[at] = v;
+        else static_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(v);
+    }
+};
 
-// Finishes a shared tile: the sums of its `shares` CTAs c0, c0 + 1, ... added
-// in that (K) order.  Warp q takes tokens q, q + 4, ... in groups of TG, lane l
-// rows 4l .. 4l + 3; 16 loads are in flight together, shares of one token or
-// tokens of a few shares (one at a time cost 0.5 us each: 6 us at one token, K
-// = 7168, N = 2112, against 3 us for the whole weight stream).
+// Finishes a tile cut into parts: the sums of its CTAs c0, c0 + 1, ... added in
+// that (K) order.  Warp q takes tokens q, q + 4, ..., TG at a time, lane l rows
+// 4l .. 4l + 3; TG x SH loads are in flight together (one load at a time cost
+// 0.5 us a part: 6 us at one token, K = 7168, N = 2112, against 3 us for the
+// whole weight stream).  By value: fields read through a pointer to the kernel's
+// parameters cost a trip to memory each (16 tokens, 7168 x 2112: 16.2 us).
 template <int NT>
-__device__ __forceinline__ void add_shares(const LinearParams &p, long long U, int tile, int c0, int shares,
-                                           int q, int lane) {
-    constexpr int TG = NT == 16 ? 2 : 4, SH = 16 / TG;
-    const int KB = p.KB, G = gridDim.x;
-    // Every share but the first one's begins on this tile: its first segment,
-    // slot 0.  The first CTA's is its last segment unless it began here too.
-    const int slot0 = share_begin(U, c0, G) / KB == tile ? 0 : 1;
-    const float4 *base = reinterpret_cast<const float4 *>(p.partial) + static_cast<size_t>(c0) * 2 * NT * 32 + lane;
-    const int n0 = tile * 128 + lane * 4;
-    for (int t0 = q; t0 < p.T; t0 += 4 * TG) {
+__device__ __noinline__ void add_parts(const float *partial, int parts, const LinearOut o, int n_first, int q, int lane) {
+    constexpr int TG = NT == 16 ? 1 : (NT == 32 ? 2 : 4), SH = NT == 16 ? 8 : 4;
+    const float4 *base = reinterpret_cast<const float4 *>(partial) + lane;
+    const int n0 = n_first + lane * 4;
+#pragma unroll 1
+    for (int t0 = q; t0 < o.T; t0 += 4 * TG) {
         float4 acc[TG];
-        uint16_t res[TG][4];
 #pragma unroll
-        for (int g = 0; g < TG; ++g) {
-            acc[g] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                res[g][i] = 0;
-                if (p.residual && t0 + 4 * g < p.T && n0 + i < p.N)
-                    res[g][i] = p.residual[static_cast<size_t>(t0 + 4 * g) * p.N + n0 + i];
-            }
-        }
-        for (int c = 0; c < shares; c += SH) {
+        for (int g = 0; g < TG; ++g) acc[g] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+        for (int c = 0; c < parts; c += SH) {
             float4 v[TG][SH];
 #pragma unroll
             for (int g = 0; g < TG; ++g)
 #pragma unroll
                 for (int i = 0; i < SH; ++i)
-                    v[g][i] = t0 + 4 * g < p.T && c + i < shares
-                                  ? __ldcg(base + (static_cast<size_t>(c + i) * 2 + (c + i == 0 ? slot0 : 0)) * NT * 32 +
-                                           (t0 + 4 * g) * 32)
-                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    v[g][i] = t0 + 4 * g < o.T && c + i < parts ? __ldcg(base + (c + i) * NT * 32 + (t0 + 4 * g) * 32)
+                                                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int g = 0; g < TG; ++g)
 #pragma unroll
@@ -151,23 +139,27 @@ __device__ __forceinline__ void add_shares(const LinearParams &p, long long U, i
         }
 #pragma unroll
         for (int g = 0; g < TG; ++g) {
-            if (t0 + 4 * g >= p.T) break;
+            if (t0 + 4 * g >= o.T) break;
             const float f[4] = {acc[g].x, acc[g].y, acc[g].z, acc[g].w};
+            const size_t at = static_cast<size_t>(t0 + 4 * g) * o.N + n0;
+            float res[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) res[i] = o.residual && n0 + i < o.N ? bf16_f(o.residual[at + i]) : 0.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (n0 + i < p.N) store_out(p, static_cast<size_t>(t0 + 4 * g) * p.N + n0 + i, f[i], bf16_f(res[g][i]));
+                if (n0 + i < o.N) o.store(at + i, f[i], res[i]);
         }
     }
 }
 
 template <int NT, bool XQ>
-constexpr int ls_threads() { return XQ ? (8 + XQ_WARPS) * 32 : 256; }
+constexpr int ls_threads() { return (XQ ? 8 + XQ_WARPS : 8) * 32; }
 
 // NT token columns; XQ: x is given in bf16 and quantised here
 template <int NT, bool XQ>
 __global__ void __launch_bounds__((ls_threads<NT, XQ>()), 1)
 linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
-                     const __grid_constant__ CUtensorMap tmap_w, const LinearParams p) {
+                     const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ LinearParams p) {
     static_assert(!XQ || NT == 16, "x is quantised here for at most 16 tokens");
     using S = LinearSmem<NT>;
     constexpr int STAGES = S::STAGES;
@@ -175,8 +167,6 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
     S &s = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int KB = p.KB;
-    const long long U = static_cast<long long>(p.tiles) * KB;
-    const long long u0 = share_begin(U, blockIdx.x, gridDim.x), u1 = share_begin(U, blockIdx.x + 1, gridDim.x);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
@@ -207,12 +197,19 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
     if (!(warp == 0 && p.early_w)) pdl_wait();
     pdl_trigger();
 
-    auto next_segment = [&](long long &u, Segment &g) {
-        if (u >= u1) return false;
-        g.tile = static_cast<int>(u / KB);
-        g.kb0 = static_cast<int>(u - static_cast<long long>(g.tile) * KB);
-        g.nk = static_cast<int>(min(static_cast<long long>(KB - g.kb0), u1 - u));
-        u += g.nk;
+    auto next_segment = [&](int &i, Segment &g) {
+        if (i < p.rounds) {
+            g.tile = i * gridDim.x + blockIdx.x;
+            g.kb0 = 0;
+            g.nk = KB;
+        } else {
+            if (i > p.rounds || static_cast<int>(blockIdx.x) >= p.rest * p.parts) return false;
+            const int tile = blockIdx.x / p.parts, part = blockIdx.x - tile * p.parts;
+            g.tile = p.rounds * gridDim.x + tile;
+            g.kb0 = part * KB / p.parts;
+            g.nk = (part + 1) * KB / p.parts - g.kb0;
+        }
+        ++i;
         return true;
     };
 
@@ -235,9 +232,9 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                 waited = true;
                 for (int i = 0; i < behind; ++i) load_x(i, first_x[i], first_n[i]);
             };
-            long long u = u0;
+            int item = 0;
             Segment g;
-            while (ok && next_segment(u, g)) {
+            while (ok && next_segment(item, g)) {
                 int wx = p.w_rowmajor ? g.kb0 * 128 : 0, wy = p.w_rowmajor ? g.tile * 128 : (g.tile * KB + g.kb0) * 128;
                 const int dx = p.w_rowmajor ? 128 : 0, dy = p.w_rowmajor ? 0 : 128;
                 int xx = g.kb0 * 128;
@@ -256,7 +253,7 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                         if (waited) load_x(stage, xx, n);
                         else first_x[behind] = xx, first_n[behind] = n, ++behind;  // the ring's first round: slot = behind
                     }
-                    wx += 2 * dx, wy += 2 * dy, xx += 256;
+                    wx += 2 * dx, wy += 2 * dy, xx += 2 * 128;
                     armed |= 1u << stage;
                     armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
                     if (++stage == STAGES) {
@@ -284,9 +281,9 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        long long u = u0;
+        int item = 0;
         Segment g;
-        while (ok && next_segment(u, g)) {
+        while (ok && next_segment(item, g)) {
             for (int left = g.nk; left > 0; left -= 2) {
                 if (!__all_sync(0xffffffffu, mbar_wait(&s.full[stage], phase, abort, p.status))) {
                     ok = false;
@@ -329,9 +326,9 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
         int slot = 0;
         uint32_t phase = 0;
         bool ok = true;
-        long long u = u0;
+        int item = 0;
         Segment g;
-        while (ok && next_segment(u, g)) {
+        while (ok && next_segment(item, g)) {
             for (int kb = g.kb0; kb < g.kb0 + g.nk; kb += 2) {
                 const int n = min(2, g.kb0 + g.nk - kb);
                 if (!__all_sync(0xffffffffu, mbar_wait(&s.sempty[slot], phase ^ 1, abort, p.status))) {
@@ -364,19 +361,19 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
         constexpr int HALVES = 2 * XQ_WARPS, PER = (2 * 16 + HALVES - 1) / HALVES;
         const int half = (warp - 8) * 2 + (lane >> 4), l16 = lane & 15, T = p.T;
         struct Cursor {
-            long long u;
+            int item;
             Segment g;
             int i;
             bool more;
-        } at{u0, {}, 0, true}, ahead{u0, {}, 0, true};
+        } at{0, {}, 0, true}, ahead;
         auto step = [&](Cursor &c) {  // to the next stage
             c.i += 2;
             if (c.i >= c.g.nk) {
                 c.i = 0;
-                c.more = next_segment(c.u, c.g);
+                c.more = next_segment(c.item, c.g);
             }
         };
-        at.more = next_segment(at.u, at.g);
+        at.more = next_segment(at.item, at.g);
         ahead = at;
         uint4 v[PER], next[PER];
         int block[PER], token[PER];  // of tile half + i * HALVES of any stage
@@ -442,15 +439,16 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
         int stage = 0, slot = 0;
         uint32_t phase = 0, sphase = 0;
-        bool ok = true, first = true;
+        bool ok = true;
+        const LinearOut out{p.residual, p.out, p.T, p.N, p.out_f32};
         if (lane < STAGES) mbar_arrive(&s.full[lane]);  // the accumulators are free
         __syncwarp();
-        long long u = u0;
+        int item = 0;
         Segment g;
-        while (next_segment(u, g)) {
-            float acc[NT];
+        while (next_segment(item, g)) {
+            float2 acc[NT / 2];
 #pragma unroll
-            for (int i = 0; i < NT; ++i) acc[i] = 0.0f;
+            for (int i = 0; i < NT / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
             for (int i = 0; i < g.nk && ok; i += 2) {
                 const bool both = i + 1 < g.nk;
                 const bool ready = mbar_wait(&s.sfull[slot], sphase, abort, p.status) &&
@@ -461,41 +459,40 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                 }
                 tc_fence_after();
                 const auto &sc = s.sc[slot];
+                const uint32_t base = lane_base + 2 * stage * NT;
+                // columns c .. c + 31 of the stage's accumulators (16 tokens: of both)
                 auto add = [&](const float (&v)[32], int c) {
-                    // 32 columns: both K blocks' 16 tokens, or 32 tokens of one
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
                         const int j = (c + e) / NT, t = (c + e) % NT;
                         if (j == 0 || both) {
                             const float4 sx = *reinterpret_cast<const float4 *>(&sc.x[j][t]);
-                            const float sw = sc.w[j];
-                            acc[t] = __fmaf_rn(v[e], __fmul_rn(sx.x, sw), acc[t]);
-                            acc[t + 1] = __fmaf_rn(v[e + 1], __fmul_rn(sx.y, sw), acc[t + 1]);
-                            acc[t + 2] = __fmaf_rn(v[e + 2], __fmul_rn(sx.z, sw), acc[t + 2]);
-                            acc[t + 3] = __fmaf_rn(v[e + 3], __fmul_rn(sx.w, sw), acc[t + 3]);
+                            const float2 sw = make_float2(sc.w[j], sc.w[j]);
+                            const float2 s0 = __fmul2_rn(make_float2(sx.x, sx.y), sw), s1 = __fmul2_rn(make_float2(sx.z, sx.w), sw);
+                            acc[t / 2] = __ffma2_rn(make_float2(v[e], v[e + 1]), s0, acc[t / 2]);
+                            acc[t / 2 + 1] = __ffma2_rn(make_float2(v[e + 2], v[e + 3]), s1, acc[t / 2 + 1]);
                         }
                     }
                 };
-                if constexpr (NT == 16) {
-                    float v[32];
-                    tmem_ld32(lane_base + 2 * stage * NT, v);
-                    tmem_wait_ld(v);
+                auto drained = [&] {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s.full[stage]);
+                };
+                if constexpr (NT == 16) {
+                    float v[32];
+                    tmem_ld32(base, v);
+                    tmem_wait_ld(v);
+                    drained();
                     add(v, 0);
                 } else {
 #pragma unroll
                     for (int c = 0; c < 2 * NT; c += 64) {
                         float v0[32], v1[32];
-                        tmem_ld32(lane_base + 2 * stage * NT + c, v0);
-                        tmem_ld32(lane_base + 2 * stage * NT + c + 32, v1);
+                        tmem_ld32(base + c, v0);
+                        tmem_ld32(base + c + 32, v1);
                         tmem_wait_ld(v0, v1);
-                        if (c + 64 == 2 * NT) {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&s.full[stage]);
-                        }
+                        if (c + 64 >= 2 * NT) drained();
                         add(v0, c);
                         add(v1, c + 32);
                     }
@@ -511,45 +508,43 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                     sphase ^= 1;
                 }
             }
+            auto sum = [&](int t) { return t & 1 ? acc[t >> 1].y : acc[t >> 1].x; };
             if (g.nk == KB) {
                 const int n = g.tile * 128 + r;
                 if (ok && n < p.N) {
 #pragma unroll
                     for (int t0 = 0; t0 < NT; t0 += 16) {
+                        const size_t at = static_cast<size_t>(t0) * p.N + n;
                         float res[16];
 #pragma unroll
                         for (int t = 0; t < 16; ++t)
-                            res[t] = p.residual && t0 + t < p.T
-                                         ? bf16_f(p.residual[static_cast<size_t>(t0 + t) * p.N + n]) : 0.0f;
+                            res[t] = p.residual && t0 + t < p.T ? bf16_f(p.residual[at + static_cast<size_t>(t) * p.N]) : 0.0f;
 #pragma unroll
                         for (int t = 0; t < 16; ++t)
-                            if (t0 + t < p.T) store_out(p, static_cast<size_t>(t0 + t) * p.N + n, acc[t0 + t], res[t]);
+                            if (t0 + t < p.T) out.store(at + static_cast<size_t>(t) * p.N, sum(t0 + t), res[t]);
                     }
                 }
             } else {
-                // shared tile: partial sums to the workspace, [token][128 rows];
-                // the last CTA adds them all, its own among them, in K order
-                const long long tu = static_cast<long long>(g.tile) * KB;
-                const int c0 = share_of(U, tu, gridDim.x), shares = share_of(U, tu + KB - 1, gridDim.x) - c0 + 1;
-                float *mine = p.partial + (static_cast<size_t>(blockIdx.x) * 2 + (first ? 0 : 1)) * NT * 128 + r;
+                // one part of a tile: partial sums to the workspace, [token][128
+                // rows]; the last CTA adds them all, its own among them
+                float *mine = p.partial + static_cast<size_t>(blockIdx.x) * NT * 128 + r;
                 if (ok) {
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
-                        if (t < p.T) mine[t * 128] = acc[t];
+                        if (t < p.T) mine[t * 128] = sum(t);
                 }
                 named_bar_sync(1, 128);
+                const int tile = blockIdx.x / p.parts;
                 if (threadIdx.x == 128) {
                     __threadfence();  // (covers what the barrier orders before it)
-                    const int last = atomicAdd(p.counters + g.tile, 1) == shares - 1;
-                    if (last) p.counters[g.tile] = 0;  // everyone has counted: zero for the next launch
+                    const int last = atomicAdd(p.counters + tile, 1) == p.parts - 1;
+                    if (last) p.counters[tile] = 0;  // everyone has counted: zero for the next launch
                     __threadfence();
                     s.last = last;
                 }
                 named_bar_sync(1, 128);
-                if (ok && s.last) add_shares<NT>(p, U, g.tile, c0, shares, q, lane);
-                named_bar_sync(1, 128);  // s.last is rewritten by the next shared tile
+                if (ok && s.last) add_parts<NT>(p.partial + static_cast<size_t>(tile) * p.parts * NT * 128, p.parts, out, g.tile * 128, q, lane);
             }
-            first = false;
         }
     }
 
@@ -585,26 +580,39 @@ linear_quant_kernel(const uint16_t *__restrict__ x, int rows, int K, int ue, uin
 }
 
 // The same behind the pre-norm, a block a token: x = bf16((h * rstd) * gamma).
-__global__ void __launch_bounds__(256)
+// The row is read from shared memory where it fits (its statistics staged it),
+// and gamma is on its way meanwhile.
+constexpr int PQ_THREADS = 512;
+__global__ void __launch_bounds__(PQ_THREADS)
 linear_prenorm_quant_kernel(const uint16_t *__restrict__ h, const uint16_t *__restrict__ gamma, int K, float eps, int ue,
                             uint8_t *__restrict__ a, float *__restrict__ a_scales) {
     __shared__ __align__(16) uint16_t chunk[kRstdChunk];
     __shared__ float rstd_sh;
+    constexpr int HALVES = PQ_THREADS / 16, AHEAD = kRstdChunk / 128 / HALVES;
     const size_t t = blockIdx.x;
     const uint16_t *row = h + t * K;
+    const int KB = K / 128, half = threadIdx.x / 16, l16 = threadIdx.x % 16;
     pdl_wait_and_trigger();
+    uint4 g[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        if (half + i * HALVES < KB) g[i] = __ldg(reinterpret_cast<const uint4 *>(gamma + (half + i * HALVES) * 128 + l16 * 8));
     const float rstd = block_rstd(row, K, eps, chunk, &rstd_sh);
-    const int KB = K / 128, l16 = threadIdx.x % 16;
-    for (int i0 = threadIdx.x / 32 * 2; i0 < KB; i0 += 16) {
-        const int i = i0 + (threadIdx.x / 16 & 1);
+    const uint16_t *src = K <= kRstdChunk ? chunk : row;
+    auto encode = [&](int kb, const uint4 &gv) {  // both halves of a warp (the shuffles)
         float v[8] = {};
-        if (i < KB) prenorm8(row, gamma, i * 128 + l16 * 8, rstd, v);
+        if (kb < KB) prenorm8(*reinterpret_cast<const uint4 *>(src + kb * 128 + l16 * 8), gv, rstd, v);
         uint2 code;
         const float sc = quant_tile8(v, ue, &code);
-        if (i >= KB) continue;
-        *reinterpret_cast<uint2 *>(a + t * K + i * 128 + l16 * 8) = code;
-        if (l16 == 0) a_scales[t * KB + i] = sc;
-    }
+        if (kb >= KB) return;
+        *reinterpret_cast<uint2 *>(a + t * K + kb * 128 + l16 * 8) = code;
+        if (l16 == 0) a_scales[t * KB + kb] = sc;
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        if ((half & ~1) + i * HALVES < KB) encode(half + i * HALVES, g[i]);
+    for (int kb = half + AHEAD * HALVES; (kb & ~1) < KB; kb += HALVES)
+        encode(kb, kb < KB ? __ldg(reinterpret_cast<const uint4 *>(gamma + kb * 128 + l16 * 8)) : make_uint4(0, 0, 0, 0));
 }
 
 // out[t, n] = sum of the ksplit binary32 planes [ksplit][T][ldp] in order
@@ -692,17 +700,38 @@ cudaError_t launch_stream_t(const LinearStreamArgs &g, cudaStream_t st) {
     p.T = g.T;
     p.N = g.N;
     p.KB = KB;
-    p.tiles = tiles;
+    const LinearPlan plan = linear_plan(g.T, tiles, KB);
+    p.rounds = plan.rounds;
+    p.rest = plan.rest;
+    p.parts = plan.parts;
     p.out_f32 = g.out_f32;
     p.w_rowmajor = g.w_rowmajor;
     p.ue = g.ue8m0;
     p.early_w = g.early_w;
-    const long long units = static_cast<long long>(tiles) * KB;
-    const int grid = static_cast<int>(std::min<long long>(units, std::min(num_sms(), kLinearMaxCtas)));
-    return launch_pdl(linear_stream_kernel<NT, XQ>, dim3(grid), dim3(ls_threads<NT, XQ>()), smem, st, mx, mw, p);
+    return launch_pdl(linear_stream_kernel<NT, XQ>, dim3(plan.grid), dim3(ls_threads<NT, XQ>()), smem, st, mx, mw, p);
 }
 
 }  // namespace
+
+// One CTA a SM.  The rest tiles are cut into the number of parts that ends
+// first, by two measured costs: a CTA alone streams a K block of a tile in 0.15
+// us, and storing, counting and adding parts takes 3 us and 4.5 ns a token and
+// part.  Parts of all tiles together (equal shares of the whole stream, two cut
+// tiles a CTA) took 17.4 us for one token at 1536 x 24576 and 9.6 at 7168 x 2112.
+LinearPlan linear_plan(int T, int tiles, int KB) {
+    const int most = std::min(num_sms(), kLinearMaxCtas);
+    LinearPlan p;
+    p.rounds = tiles / most;
+    p.rest = tiles - p.rounds * most;
+    p.parts = 1;
+    float best = 0.15f * KB;
+    for (int k = 2; p.rest && k <= std::min(most / p.rest, KB); ++k) {
+        const float t = 0.15f * ((KB + k - 1) / k) + 3.0f + 0.0045f * T * k;
+        if (t < best) best = t, p.parts = k;
+    }
+    p.grid = p.rounds ? most : p.rest * p.parts;
+    return p;
+}
 
 cudaError_t launch_linear_stream(const LinearStreamArgs &g, cudaStream_t st, int *launches) {
     if (g.T < 1 || g.T > (g.x ? kLinearQuantRows : kLinearStreamRows)) return cudaErrorInvalidValue;
@@ -730,7 +759,7 @@ cudaError_t launch_linear_quant(const uint16_t *x, int rows, int K, bool ue8m0, 
 cudaError_t launch_linear_prenorm_quant(const uint16_t *h, const uint16_t *gamma, int rows, int K, float eps, bool ue8m0,
                                         uint8_t *a, float *a_scales, cudaStream_t st, int *launches) {
     mark_launch(st, *launches, "linear_prenorm_quant");
-    LAUNCH_OR_RETURN(launch_pdl(linear_prenorm_quant_kernel, dim3(rows), dim3(256), 0, st, h, gamma, K, eps, ue8m0 ? 1 : 0, a,
+    LAUNCH_OR_RETURN(launch_pdl(linear_prenorm_quant_kernel, dim3(rows), dim3(PQ_THREADS), 0, st, h, gamma, K, eps, ue8m0 ? 1 : 0, a,
                                 a_scales));
     ++*launches;
     return cudaGetLastError();

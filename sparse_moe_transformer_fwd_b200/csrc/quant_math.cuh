@@ -87,9 +87,8 @@ __device__ __forceinline__ float block_rstd(const uint16_t *row, int d, float ep
     return *shared;
 }
 
-// Eight pre-normed columns of a row.
-__device__ __forceinline__ void prenorm8(const uint16_t *row, const uint16_t *gamma, int c, float rstd, float (&v)[8]) {
-    const uint4 raw = *reinterpret_cast<const uint4 *>(row + c), graw = *reinterpret_cast<const uint4 *>(gamma + c);
+// Eight pre-normed columns.
+__device__ __forceinline__ void prenorm8(const uint4 &raw, const uint4 &graw, float rstd, float (&v)[8]) {
     const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w}, g[4] = {graw.x, graw.y, graw.z, graw.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
