@@ -11,13 +11,15 @@
 // tiles go to the CTAs in turn.  The tiles of the last, partial round (all of
 // them, where there are fewer than SMs) are cut into equal parts of K, as many
 // as pay (linear_plan); each part's CTA stores its binary32 partial sums in the
-// workspace and counts itself in, and the last one adds them in K order, so the
-// result does not depend on timing.
+// workspace.  They are added in K order, so the result does not depend on
+// timing: for a few tokens by the last of a tile's CTAs, which count themselves
+// in, else by a second kernel, all SMs of it (64 tokens in two parts: 3 us, and
+// 13 by one CTA a tile).
 //   warp 0      TMA producer: a stage is two K blocks (two 16 KB boxes of W, two
 //               boxes of activations)
 //   warp 1      TMEM allocator and MMA issuer: a stage's K blocks go to adjacent
 //               accumulators; a stage is one wait and one commit
-//   warp 2      scales of each K block, copied to a ring in shared memory with
+//   warps 2-3   scales of a K block each, copied to a ring in shared memory with
 //               cp.async (rows past T: zeros)
 //   warps 4-7   epilogue: thread = weight row; adds each accumulator, times its
 //               scale product, to the token sums in registers
@@ -41,6 +43,7 @@ namespace {
 constexpr int W_BYTES = 128 * 128;  // one tile of weights
 constexpr int SC_RING = 8;          // scale slots (two K blocks each)
 constexpr int XQ_WARPS = 5;         // warps that quantise x
+constexpr int kSumHere = 4;         // tokens up to which a tile's last CTA adds its parts
 
 template <int NT>
 struct LinearSmem {
@@ -76,6 +79,7 @@ struct LinearParams {
     int rounds;   // whole tiles of every CTA: tile round * gridDim.x + CTA
     int rest;     // tiles of the last round
     int parts;    // parts of K of each of those
+    int sum_here; // the last of a tile's CTAs adds its parts (else a kernel after this one)
     int out_f32;
     int w_rowmajor;
     int ue;       // power-of-two scales (with XQ)
@@ -102,54 +106,64 @@ struct LinearOut {
     }
 };
 
-// Finishes a tile cut into parts: the sums of its CTAs c0, c0 + 1, ... added in
-// that (K) order.  Warp q takes tokens q, q + 4, ..., TG at a time, lane l rows
-// 4l .. 4l + 3; TG x SH loads are in flight together (one load at a time cost
-// 0.5 us a part: 6 us at one token, K = 7168, N = 2112, against 3 us for the
-// whole weight stream).  By value: fields read through a pointer to the kernel's
-// parameters cost a trip to memory each (16 tokens, 7168 x 2112: 16.2 us).
+// Four rows n0 .. n0 + 3 of token t: the sums of `parts` CTAs added in that (K)
+// order, eight loads in flight (one at a time cost 0.5 us each).  partial: the
+// first part's piece, the next NT * 128 values on.
 template <int NT>
-__device__ __noinline__ void add_parts(const float *partial, int parts, const LinearOut o, int n_first, int q, int lane) {
-    constexpr int TG = NT == 16 ? 1 : (NT == 32 ? 2 : 4), SH = NT == 16 ? 8 : 4;
-    const float4 *base = reinterpret_cast<const float4 *>(partial) + lane;
-    const int n0 = n_first + lane * 4;
-#pragma unroll 1
-    for (int t0 = q; t0 < o.T; t0 += 4 * TG) {
-        float4 acc[TG];
-#pragma unroll
-        for (int g = 0; g < TG; ++g) acc[g] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 1
-        for (int c = 0; c < parts; c += SH) {
-            float4 v[TG][SH];
-#pragma unroll
-            for (int g = 0; g < TG; ++g)
-#pragma unroll
-                for (int i = 0; i < SH; ++i)
-                    v[g][i] = t0 + 4 * g < o.T && c + i < parts ? __ldcg(base + (c + i) * NT * 32 + (t0 + 4 * g) * 32)
-                                                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int g = 0; g < TG; ++g)
-#pragma unroll
-                for (int i = 0; i < SH; ++i) {
-                    acc[g].x = __fadd_rn(acc[g].x, v[g][i].x);
-                    acc[g].y = __fadd_rn(acc[g].y, v[g][i].y);
-                    acc[g].z = __fadd_rn(acc[g].z, v[g][i].z);
-                    acc[g].w = __fadd_rn(acc[g].w, v[g][i].w);
-                }
-        }
-#pragma unroll
-        for (int g = 0; g < TG; ++g) {
-            if (t0 + 4 * g >= o.T) break;
-            const float f[4] = {acc[g].x, acc[g].y, acc[g].z, acc[g].w};
-            const size_t at = static_cast<size_t>(t0 + 4 * g) * o.N + n0;
-            float res[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) res[i] = o.residual && n0 + i < o.N ? bf16_f(o.residual[at + i]) : 0.0f;
+__device__ __forceinline__ void add_parts(const float4 *partial, int parts, const LinearOut &o, int t, int n0) {
+    const size_t at = static_cast<size_t>(t) * o.N + n0;
+    const bool vec = o.N % 4 == 0;  // whole 8- or 16-byte pieces (n0 is a multiple of 4)
+    float res[4] = {};
+    if (o.residual) {
+        if (vec && n0 < o.N) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(o.residual + at);
+            res[0] = bf16_lo(w.x), res[1] = bf16_hi(w.x), res[2] = bf16_lo(w.y), res[3] = bf16_hi(w.y);
+        } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (n0 + i < o.N) o.store(at + i, f[i], res[i]);
+                if (n0 + i < o.N) res[i] = bf16_f(o.residual[at + i]);
         }
     }
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+    for (int c = 0; c < parts; c += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = c + i < parts ? __ldcg(partial + (c + i) * (NT * 32)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            acc.x = __fadd_rn(acc.x, v[i].x);
+            acc.y = __fadd_rn(acc.y, v[i].y);
+            acc.z = __fadd_rn(acc.z, v[i].z);
+            acc.w = __fadd_rn(acc.w, v[i].w);
+        }
+    }
+    float f[4] = {acc.x, acc.y, acc.z, acc.w};
+    if (!vec) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n0 + i < o.N) o.store(at + i, f[i], res[i]);
+        return;
+    }
+    if (n0 >= o.N) return;
+    if (o.residual)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = __fadd_rn(f[i], res[i]);
+    if (o.f32) *reinterpret_cast<float4 *>(static_cast<float *>(o.out) + at) = make_float4(f[0], f[1], f[2], f[3]);
+    else *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(o.out) + at) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+}
+
+// The parts of all cut tiles, a thread four rows of a token.
+template <int NT>
+__global__ void __launch_bounds__(256)
+linear_sum_kernel(const float *__restrict__ partial, int first_tile, int rest, int parts, const LinearOut o) {
+    pdl_wait_and_trigger();
+    const int i = blockIdx.x * 256 + threadIdx.x;  // (tile, token, four rows)
+    const int lane = i & 31, t = (i >> 5) % o.T, tile = (i >> 5) / o.T;
+    if (tile >= rest) return;
+    add_parts<NT>(reinterpret_cast<const float4 *>(partial) + (static_cast<size_t>(tile) * parts * NT + t) * 32 + lane, parts, o,
+                  t, (first_tile + tile) * 128 + lane * 4);
 }
 
 template <int NT, bool XQ>
@@ -174,7 +188,7 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
             mbar_init(&s.done[i], 1);
         }
         for (int i = 0; i < SC_RING; ++i) {
-            mbar_init(&s.sfull[i], 32 + (XQ ? XQ_WARPS : 0));
+            mbar_init(&s.sfull[i], 64 + (XQ ? XQ_WARPS : 0));
             mbar_init(&s.sempty[i], 4);
         }
         mbar_init(&s.mma_done, 1);
@@ -319,32 +333,30 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                 break;
             }
         }
-    } else if (warp == 2) {
-        // lane l copies the scales of tokens l, l + 32 (of both K blocks) and
-        // lanes 0, 1 the weights' (32 arrivals on the slot's barrier, one a
-        // lane, each made when that lane's copies have landed)
+    } else if (warp == 2 || warp == 3) {
+        // Warp 2 + j copies the scales of the stage's K block j: lane l those of
+        // tokens l, l + 32, lane 0 the weights' (every lane arrives on the slot's
+        // barrier when its copies have landed).
+        const int j = warp - 2;
         int slot = 0;
         uint32_t phase = 0;
         bool ok = true;
         int item = 0;
         Segment g;
         while (ok && next_segment(item, g)) {
-            for (int kb = g.kb0; kb < g.kb0 + g.nk; kb += 2) {
-                const int n = min(2, g.kb0 + g.nk - kb);
+            const float *ws = p.w_scales + static_cast<size_t>(g.tile) * KB;
+            for (int kb = g.kb0 + j; kb - j < g.kb0 + g.nk; kb += 2) {
                 if (!__all_sync(0xffffffffu, mbar_wait(&s.sempty[slot], phase ^ 1, abort, p.status))) {
                     ok = false;
                     break;
                 }
-                if constexpr (!XQ)
-                    for (int j = 0; j < n; ++j) {
-                        for (int t = lane; t < NT; t += 32) {
-                            const bool in = t < p.T;
-                            cp_async4(&s.sc[slot].x[j][t],
-                                      p.a_scales + (in ? static_cast<size_t>(t) * KB + kb + j : 0), in);
-                        }
-                    }
-                if (lane < n)
-                    cp_async4(&s.sc[slot].w[lane], p.w_scales + static_cast<size_t>(g.tile) * KB + kb + lane, true);
+                if (kb < g.kb0 + g.nk) {
+                    if constexpr (!XQ)
+#pragma unroll
+                        for (int t = lane; t < NT; t += 32)
+                            cp_async4(&s.sc[slot].x[j][t], p.a_scales + (t < p.T ? static_cast<size_t>(t) * KB + kb : 0), t < p.T);
+                    if (lane == 0) cp_async4(&s.sc[slot].w[j], ws + kb, true);
+                }
                 cp_async_mbar_arrive(&s.sfull[slot]);
                 if (++slot == SC_RING) {
                     slot = 0;
@@ -533,6 +545,7 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                     for (int t = 0; t < NT; ++t)
                         if (t < p.T) mine[t * 128] = sum(t);
                 }
+                if (!p.sum_here) continue;
                 named_bar_sync(1, 128);
                 const int tile = blockIdx.x / p.parts;
                 if (threadIdx.x == 128) {
@@ -543,7 +556,11 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                     s.last = last;
                 }
                 named_bar_sync(1, 128);
-                if (ok && s.last) add_parts<NT>(p.partial + static_cast<size_t>(tile) * p.parts * NT * 128, p.parts, out, g.tile * 128, q, lane);
+                if (ok && s.last)
+                    for (int t = q; t < p.T; t += 4)
+                        add_parts<NT>(reinterpret_cast<const float4 *>(p.partial) +
+                                          (static_cast<size_t>(tile) * p.parts * NT + t) * 32 + lane,
+                                      p.parts, out, t, g.tile * 128 + lane * 4);
             }
         }
     }
@@ -672,7 +689,7 @@ linear_finish_kernel(const float *__restrict__ partial, int ksplit, int T, int N
 }
 
 template <int NT, bool XQ>
-cudaError_t launch_stream_t(const LinearStreamArgs &g, cudaStream_t st) {
+cudaError_t launch_stream_t(const LinearStreamArgs &g, cudaStream_t st, int *launches) {
     CUtensorMap mx, mw;
     const int tiles = (g.N + 127) / 128, KB = g.K / 128;
     std::memset(&mx, 0, sizeof mx);
@@ -704,19 +721,32 @@ cudaError_t launch_stream_t(const LinearStreamArgs &g, cudaStream_t st) {
     p.rounds = plan.rounds;
     p.rest = plan.rest;
     p.parts = plan.parts;
+    p.sum_here = g.T <= kSumHere;
     p.out_f32 = g.out_f32;
     p.w_rowmajor = g.w_rowmajor;
     p.ue = g.ue8m0;
     p.early_w = g.early_w;
-    return launch_pdl(linear_stream_kernel<NT, XQ>, dim3(plan.grid), dim3(ls_threads<NT, XQ>()), smem, st, mx, mw, p);
+    mark_launch(st, *launches, "linear_stream");
+    const auto kernel = linear_stream_kernel<NT, XQ>;
+    constexpr int threads = ls_threads<NT, XQ>();
+    LAUNCH_OR_RETURN(launch_pdl(kernel, dim3(plan.grid), dim3(threads), smem, st, mx, mw, p));
+    ++*launches;
+    if (plan.parts == 1 || p.sum_here) return cudaSuccess;
+    mark_launch(st, *launches, "linear_sum");
+    const LinearOut out{g.residual, g.out, g.T, g.N, g.out_f32};
+    LAUNCH_OR_RETURN(launch_pdl(linear_sum_kernel<NT>, dim3((plan.rest * g.T * 32 + 255) / 256), dim3(256), 0, st, g.partial,
+                                plan.rounds * plan.grid, plan.rest, plan.parts, out));
+    ++*launches;
+    return cudaSuccess;
 }
 
 }  // namespace
 
 // One CTA a SM.  The rest tiles are cut into the number of parts that ends
 // first, by two measured costs: a CTA alone streams a K block of a tile in 0.15
-// us, and storing, counting and adding parts takes 3 us and 4.5 ns a token and
-// part.  Parts of all tiles together (equal shares of the whole stream, two cut
+// us (0.2 with 32 columns; 0.38 with 64, whose scales every epilogue warp reads
+// from shared memory: with the operands 1300 clk of its bandwidth a stage), and
+// storing, counting and adding parts takes 3 us and 4.5 ns a token and part.  Parts of all tiles together (equal shares of the whole stream, two cut
 // tiles a CTA) took 17.4 us for one token at 1536 x 24576 and 9.6 at 7168 x 2112.
 LinearPlan linear_plan(int T, int tiles, int KB) {
     const int most = std::min(num_sms(), kLinearMaxCtas);
@@ -724,9 +754,10 @@ LinearPlan linear_plan(int T, int tiles, int KB) {
     p.rounds = tiles / most;
     p.rest = tiles - p.rounds * most;
     p.parts = 1;
-    float best = 0.15f * KB;
+    const float block = T <= 16 ? 0.15f : (T <= 32 ? 0.2f : 0.38f);
+    float best = block * KB;
     for (int k = 2; p.rest && k <= std::min(most / p.rest, KB); ++k) {
-        const float t = 0.15f * ((KB + k - 1) / k) + 3.0f + 0.0045f * T * k;
+        const float t = block * ((KB + k - 1) / k) + 3.0f + 0.0045f * T * k;
         if (t < best) best = t, p.parts = k;
     }
     p.grid = p.rounds ? most : p.rest * p.parts;
@@ -735,14 +766,12 @@ LinearPlan linear_plan(int T, int tiles, int KB) {
 
 cudaError_t launch_linear_stream(const LinearStreamArgs &g, cudaStream_t st, int *launches) {
     if (g.T < 1 || g.T > (g.x ? kLinearQuantRows : kLinearStreamRows)) return cudaErrorInvalidValue;
-    mark_launch(st, *launches, "linear_stream");
     cudaError_t e;
-    if (g.x) e = launch_stream_t<16, true>(g, st);
-    else if (g.T <= 16) e = launch_stream_t<16, false>(g, st);
-    else if (g.T <= 32) e = launch_stream_t<32, false>(g, st);
-    else e = launch_stream_t<64, false>(g, st);
+    if (g.x) e = launch_stream_t<16, true>(g, st, launches);
+    else if (g.T <= 16) e = launch_stream_t<16, false>(g, st, launches);
+    else if (g.T <= 32) e = launch_stream_t<32, false>(g, st, launches);
+    else e = launch_stream_t<64, false>(g, st, launches);
     LAUNCH_OR_RETURN(e);
-    ++*launches;
     return cudaGetLastError();
 }
 
