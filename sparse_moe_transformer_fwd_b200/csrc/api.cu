@@ -1149,7 +1149,6 @@ namespace {
 // zero-filled workspace serves linears of any shapes: each launch leaves the
 // counters zero, and no other region of another shape reaches them.
 constexpr int kLinearMaxN = 1 << 20;
-constexpr size_t kLinearCounterBytes = kLinearMaxCtas * sizeof(int);
 constexpr int kLinearSplitRows = 256;  // as the dense down GEMM: K split up to here
 
 int check_linear_shape(const moe_linear_shape *s) {
@@ -1213,7 +1212,7 @@ LinearLayout linear_layout(const moe_linear_shape *s) {
         return at;
     };
     L.status = take(256);
-    L.counters = take(kLinearCounterBytes);
+    L.counters = take(sizeof(LinearCounters));
     L.a = take(T * K);
     L.a_scales = take(T * (K / 128) * 4);
     if (s->T <= kLinearStreamRows)
@@ -1246,7 +1245,7 @@ int linear_product(const moe_linear_shape *s, const uint16_t *x, const void *a, 
         g.residual = residual;
         g.out = out;
         g.partial = partial;
-        g.counters = at<int>(ws, L.counters);
+        g.counters = at<LinearCounters>(ws, L.counters);
         g.status = at<int>(ws, L.status);
         g.T = s->T;
         g.K = s->K;
@@ -1257,6 +1256,8 @@ int linear_product(const moe_linear_shape *s, const uint16_t *x, const void *a, 
         return MOE_OK;
     }
     const int ks = linear_ksplit(s);
+    // binary32 outputs of whole tiles without a residual are the sums themselves
+    const bool in_place = ks == 1 && s->out_f32 && s->N % 256 == 0 && !residual;
     const bool sums = ks > 1 || !linear_direct(s);
     GemmArgs g{};
     g.fp8 = true;
@@ -1280,11 +1281,11 @@ int linear_product(const moe_linear_shape *s, const uint16_t *x, const void *a, 
     g.tile_m = kTileM;
     g.early_b = *n > 0;
     g.ksplit = ks;
-    g.partial = sums ? partial : nullptr;
+    g.partial = in_place ? static_cast<float *>(out) : (sums ? partial : nullptr);
     g.b_rows_valid = g.N_out != s->N ? s->N : 0;
     g.residual = sums ? nullptr : residual;
     LAUNCH(launch_grouped_gemm(g, st, n), "linear GEMM");
-    if (sums)
+    if (sums && !in_place)
         LAUNCH(launch_linear_finish(partial, ks, s->T, s->N, g.N_out, residual, out, s->out_f32, st, n),
                "linear finish");
     return MOE_OK;

@@ -206,9 +206,14 @@ cudaError_t launch_few(const FewArgs &g, cudaStream_t st, int *launches);
 // tokens (linear.cu).
 constexpr int kLinearStreamRows = 64;
 constexpr int kLinearMaxCtas = 160;  // CTAs of linear_stream (sizes its partial sums)
-// rounds of whole tiles, one a CTA; then `rest` tiles of `parts` parts each.
+// `whole` tiles (a multiple of the CTAs), then `rest` tiles of `parts` parts each.
 struct LinearPlan {
-    int grid, rounds, rest, parts;
+    int grid, whole, rest, parts;
+};
+// Counters of one launch: zero before it, and left zero.
+struct LinearCounters {
+    int next, exited;
+    int parts[kLinearMaxCtas];  // [cut tile] parts stored
 };
 LinearPlan linear_plan(int T, int tiles, int KB);
 constexpr int kLinearQuantRows = 16;  // and of bf16 x, quantised in the same kernel
@@ -221,7 +226,7 @@ struct LinearStreamArgs {
     const uint16_t *residual;  // bf16 [T, N] or NULL
     void *out;                 // [T, N] bf16, or binary32 with out_f32
     float *partial;            // linear_partial_floats(T)
-    int *counters;             // [kLinearMaxCtas], zero; left zero
+    LinearCounters *counters;
     int *status;
     int T, K, N;
     int out_f32, w_rowmajor;

@@ -7,9 +7,11 @@
 //
 // Few tokens read each weight byte for few FLOP, so the product is bound by
 // HBM: N*K bytes of weights.  The weights are therefore the M operand of the MMA
-// (128 rows of W a tile, tokens the N operand: 16, 32 or 64 columns), and the
-// tiles go to the CTAs in turn.  The tiles of the last, partial round (all of
-// them, where there are fewer than SMs) are cut into equal parts of K, as many
+// (128 rows of W a tile, tokens the N operand: 16, 32 or 64 columns).  A CTA's
+// first tile is its own number, then it takes the next free one (HBM serves some
+// SMs faster: of 7168 x 64007 in equal shares the first CTA ended after 58 us,
+// the last after 76).  The tiles past the last whole round (all of them, where
+// there are fewer than SMs) are cut into equal parts of K, as many
 // as pay (linear_plan); each part's CTA stores its binary32 partial sums in the
 // workspace.  They are added in K order, so the result does not depend on
 // timing: for a few tokens by the last of a tile's CTAs, which count themselves
@@ -42,6 +44,7 @@ namespace {
 
 constexpr int W_BYTES = 128 * 128;  // one tile of weights
 constexpr int SC_RING = 8;          // scale slots (two K blocks each)
+constexpr int QUEUE = 4;            // work items between the producer and the other roles
 constexpr int XQ_WARPS = 5;         // warps that quantise x
 constexpr int kSumHere = 4;         // tokens up to which a tile's last CTA adds its parts
 
@@ -61,6 +64,8 @@ struct LinearSmem {
     uint64_t full[STAGES];  // operands landed, and the accumulators drained (4 warps)
     uint64_t done[STAGES];  // MMAs done: accumulators to read, operands to overwrite
     uint64_t sfull[SC_RING], sempty[SC_RING];
+    int queue[QUEUE];
+    uint64_t qfull[QUEUE], qempty[QUEUE];
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort;
@@ -72,12 +77,12 @@ struct LinearParams {
     const float *a_scales, *w_scales;
     const uint16_t *residual;  // bf16 [T, N] or NULL
     void *out;                 // [T, N] bf16, or binary32 (out_f32)
-    float *partial;            // [gridDim.x][NT][128]
-    int *counters;             // [gridDim.x], zero between launches
+    float *partial;            // [rest * parts][NT][128]
+    LinearCounters *counters;  // zero between launches
     int *status;
     int T, N, KB;
-    int rounds;   // whole tiles of every CTA: tile round * gridDim.x + CTA
-    int rest;     // tiles of the last round
+    int whole;    // tiles worked on whole: the first ones
+    int rest;     // tiles after them
     int parts;    // parts of K of each of those
     int sum_here; // the last of a tile's CTAs adds its parts (else a kernel after this one)
     int out_f32;
@@ -89,6 +94,7 @@ struct LinearParams {
 // K blocks kb0 .. kb0 + nk - 1 of one tile.
 struct Segment {
     int tile, kb0, nk;
+    int part;  // of the cut tiles' parts, all of them
 };
 
 __device__ __forceinline__ float bf16_f(uint16_t v) {
@@ -191,6 +197,10 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
             mbar_init(&s.sfull[i], 64 + (XQ ? XQ_WARPS : 0));
             mbar_init(&s.sempty[i], 4);
         }
+        for (int i = 0; i < QUEUE; ++i) {
+            mbar_init(&s.qfull[i], 1);
+            mbar_init(&s.qempty[i], 7 + (XQ ? XQ_WARPS : 0));  // MMA, scales, epilogue, quantisers
+        }
         mbar_init(&s.mma_done, 1);
         s.abort = 0;
         fence_mbar_init();
@@ -211,20 +221,42 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
     if (!(warp == 0 && p.early_w)) pdl_wait();
     pdl_trigger();
 
-    auto next_segment = [&](int &i, Segment &g) {
-        if (i < p.rounds) {
-            g.tile = i * gridDim.x + blockIdx.x;
+    const int items = p.whole + p.rest * p.parts;
+    auto decode = [&](int id, Segment &g) {
+        if (id < 0 || id >= items) return false;
+        if (id < p.whole) {
+            g.tile = id;
             g.kb0 = 0;
             g.nk = KB;
+            g.part = -1;
         } else {
-            if (i > p.rounds || static_cast<int>(blockIdx.x) >= p.rest * p.parts) return false;
-            const int tile = blockIdx.x / p.parts, part = blockIdx.x - tile * p.parts;
-            g.tile = p.rounds * gridDim.x + tile;
-            g.kb0 = part * KB / p.parts;
-            g.nk = (part + 1) * KB / p.parts - g.kb0;
+            g.part = id - p.whole;
+            const int tile = g.part / p.parts, k = g.part - tile * p.parts;
+            g.tile = p.whole + tile;
+            g.kb0 = k * KB / p.parts;
+            g.nk = (k + 1) * KB / p.parts - g.kb0;
         }
-        ++i;
         return true;
+    };
+    // A role's items (whole warps): the CTA's number, then what the producer hands
+    // on; in turn where there are less than two rounds of whole tiles, which end
+    // before taking them evens anything out (24576 x 1536: 10.8 us, taken 12.1).
+    const bool taken = p.whole >= 2 * static_cast<int>(gridDim.x);
+    struct Taken {
+        int n = 0, slot = 0;
+        uint32_t phase = 0;
+    };
+    auto next_segment = [&](Taken &q, Segment &g) {
+        if (q.n == 0 || !taken) return decode(blockIdx.x + q.n++ * gridDim.x, g);
+        const bool got = __all_sync(0xffffffffu, mbar_wait(&s.qfull[q.slot], q.phase, abort, p.status));
+        const int id = got ? s.queue[q.slot] : -1;
+        __syncwarp();
+        if (got && lane == 0) mbar_arrive(&s.qempty[q.slot]);
+        if (++q.slot == QUEUE) {
+            q.slot = 0;
+            q.phase ^= 1;
+        }
+        return decode(id, g);
     };
 
     if (warp == 0) {
@@ -246,9 +278,25 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                 waited = true;
                 for (int i = 0; i < behind; ++i) load_x(i, first_x[i], first_n[i]);
             };
-            int item = 0;
+            // the next free item is asked for while the one before is loaded, and
+            // handed on once known
+            int id = blockIdx.x, slot = 0;
+            uint32_t qphase = 0;
+            auto hand_on = [&](int v) {
+                if (!mbar_wait(&s.qempty[slot], qphase ^ 1, abort, p.status)) return false;
+                s.queue[slot] = v;
+                mbar_arrive(&s.qfull[slot]);
+                if (++slot == QUEUE) {
+                    slot = 0;
+                    qphase ^= 1;
+                }
+                return true;
+            };
             Segment g;
-            while (ok && next_segment(item, g)) {
+            while (ok && decode(id, g)) {
+                int next = id + gridDim.x;
+                const bool ask = taken && waited;  // (the launch before may hold the counter until then)
+                if (ask) next = gridDim.x + atomicAdd(&p.counters->next, 1);
                 int wx = p.w_rowmajor ? g.kb0 * 128 : 0, wy = p.w_rowmajor ? g.tile * 128 : (g.tile * KB + g.kb0) * 128;
                 const int dx = p.w_rowmajor ? 128 : 0, dy = p.w_rowmajor ? 0 : 128;
                 int xx = g.kb0 * 128;
@@ -275,6 +323,12 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                         phase ^= 1;
                     }
                 }
+                if (taken && !ask) {
+                    if (!waited) catch_up();
+                    next = gridDim.x + atomicAdd(&p.counters->next, 1);
+                }
+                id = next < items ? next : -1;
+                if (ok && taken && !hand_on(id)) ok = false;
             }
             if (!waited) catch_up();
             // drain: every load issued has landed before the block exits
@@ -295,7 +349,7 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        int item = 0;
+        Taken item;
         Segment g;
         while (ok && next_segment(item, g)) {
             for (int left = g.nk; left > 0; left -= 2) {
@@ -341,7 +395,7 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
         int slot = 0;
         uint32_t phase = 0;
         bool ok = true;
-        int item = 0;
+        Taken item;
         Segment g;
         while (ok && next_segment(item, g)) {
             const float *ws = p.w_scales + static_cast<size_t>(g.tile) * KB;
@@ -372,21 +426,13 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
         // 128-byte row, 16-byte chunks XOR-swizzled by the row as the TMA does.
         constexpr int HALVES = 2 * XQ_WARPS, PER = (2 * 16 + HALVES - 1) / HALVES;
         const int half = (warp - 8) * 2 + (lane >> 4), l16 = lane & 15, T = p.T;
-        struct Cursor {
-            int item;
+        Taken item;
+        struct Cursor {  // a stage: K blocks i, i + 1 of a segment
             Segment g;
             int i;
             bool more;
-        } at{0, {}, 0, true}, ahead;
-        auto step = [&](Cursor &c) {  // to the next stage
-            c.i += 2;
-            if (c.i >= c.g.nk) {
-                c.i = 0;
-                c.more = next_segment(c.item, c.g);
-            }
-        };
-        at.more = next_segment(at.item, at.g);
-        ahead = at;
+        } ahead{{}, 0, false}, at;
+        ahead.more = next_segment(item, ahead.g);
         uint4 v[PER], next[PER];
         int block[PER], token[PER];  // of tile half + i * HALVES of any stage
 #pragma unroll
@@ -406,10 +452,15 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
         load(ahead, next);
         int stage = 0, slot = 0;
         uint32_t phase = 0, sphase = 0;
-        while (at.more) {
+        while (ahead.more) {
+            at = ahead;
 #pragma unroll
             for (int i = 0; i < PER; ++i) v[i] = next[i];
-            step(ahead);
+            ahead.i += 2;
+            if (ahead.i >= ahead.g.nk) {
+                ahead.i = 0;
+                ahead.more = next_segment(item, ahead.g);
+            }
             load(ahead, next);
             const int n = min(2, at.g.nk - at.i) * T;
             if (!__all_sync(0xffffffffu, mbar_wait(&s.sempty[slot], sphase ^ 1, abort, p.status) &&
@@ -435,7 +486,6 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                 mbar_arrive(&s.full[stage]);
                 mbar_arrive(&s.sfull[slot]);
             }
-            step(at);
             if (++stage == STAGES) {
                 stage = 0;
                 phase ^= 1;
@@ -455,7 +505,7 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
         const LinearOut out{p.residual, p.out, p.T, p.N, p.out_f32};
         if (lane < STAGES) mbar_arrive(&s.full[lane]);  // the accumulators are free
         __syncwarp();
-        int item = 0;
+        Taken item;
         Segment g;
         while (next_segment(item, g)) {
             float2 acc[NT / 2];
@@ -539,7 +589,7 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
             } else {
                 // one part of a tile: partial sums to the workspace, [token][128
                 // rows]; the last CTA adds them all, its own among them
-                float *mine = p.partial + static_cast<size_t>(blockIdx.x) * NT * 128 + r;
+                float *mine = p.partial + static_cast<size_t>(g.part) * NT * 128 + r;
                 if (ok) {
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
@@ -547,11 +597,11 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                 }
                 if (!p.sum_here) continue;
                 named_bar_sync(1, 128);
-                const int tile = blockIdx.x / p.parts;
+                const int tile = g.tile - p.whole;
                 if (threadIdx.x == 128) {
                     __threadfence();  // (covers what the barrier orders before it)
-                    const int last = atomicAdd(p.counters + tile, 1) == p.parts - 1;
-                    if (last) p.counters[tile] = 0;  // everyone has counted: zero for the next launch
+                    const int last = atomicAdd(p.counters->parts + tile, 1) == p.parts - 1;
+                    if (last) p.counters->parts[tile] = 0;  // everyone has counted: zero for the next launch
                     __threadfence();
                     s.last = last;
                 }
@@ -561,6 +611,7 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                         add_parts<NT>(reinterpret_cast<const float4 *>(p.partial) +
                                           (static_cast<size_t>(tile) * p.parts * NT + t) * 32 + lane,
                                       p.parts, out, t, g.tile * 128 + lane * 4);
+                named_bar_sync(1, 128);  // s.last is rewritten by the next part
             }
         }
     }
@@ -570,6 +621,11 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, S::TMEM_COLS);
+    }
+    // the last CTA out zeroes the item counter for the next launch
+    if (threadIdx.x == 0 && taken) {
+        __threadfence();
+        if (atomicAdd(&p.counters->exited, 1) == static_cast<int>(gridDim.x) - 1) p.counters->next = p.counters->exited = 0;
     }
 }
 
@@ -718,7 +774,7 @@ cudaError_t launch_stream_t(const LinearStreamArgs &g, cudaStream_t st, int *lau
     p.N = g.N;
     p.KB = KB;
     const LinearPlan plan = linear_plan(g.T, tiles, KB);
-    p.rounds = plan.rounds;
+    p.whole = plan.whole;
     p.rest = plan.rest;
     p.parts = plan.parts;
     p.sum_here = g.T <= kSumHere;
@@ -735,7 +791,7 @@ cudaError_t launch_stream_t(const LinearStreamArgs &g, cudaStream_t st, int *lau
     mark_launch(st, *launches, "linear_sum");
     const LinearOut out{g.residual, g.out, g.T, g.N, g.out_f32};
     LAUNCH_OR_RETURN(launch_pdl(linear_sum_kernel<NT>, dim3((plan.rest * g.T * 32 + 255) / 256), dim3(256), 0, st, g.partial,
-                                plan.rounds * plan.grid, plan.rest, plan.parts, out));
+                                plan.whole, plan.rest, plan.parts, out));
     ++*launches;
     return cudaSuccess;
 }
@@ -746,21 +802,21 @@ cudaError_t launch_stream_t(const LinearStreamArgs &g, cudaStream_t st, int *lau
 // first, by two measured costs: a CTA alone streams a K block of a tile in 0.15
 // us (0.2 with 32 columns; 0.38 with 64, whose scales every epilogue warp reads
 // from shared memory: with the operands 1300 clk of its bandwidth a stage), and
-// storing, counting and adding parts takes 3 us and 4.5 ns a token and part.  Parts of all tiles together (equal shares of the whole stream, two cut
+// storing and adding parts takes 3 us.  Parts of all tiles together (equal shares of the whole stream, two cut
 // tiles a CTA) took 17.4 us for one token at 1536 x 24576 and 9.6 at 7168 x 2112.
 LinearPlan linear_plan(int T, int tiles, int KB) {
     const int most = std::min(num_sms(), kLinearMaxCtas);
     LinearPlan p;
-    p.rounds = tiles / most;
-    p.rest = tiles - p.rounds * most;
+    p.whole = tiles / most * most;
+    p.rest = tiles - p.whole;
     p.parts = 1;
     const float block = T <= 16 ? 0.15f : (T <= 32 ? 0.2f : 0.38f);
     float best = block * KB;
     for (int k = 2; p.rest && k <= std::min(most / p.rest, KB); ++k) {
-        const float t = block * ((KB + k - 1) / k) + 3.0f + 0.0045f * T * k;
+        const float t = block * ((KB + k - 1) / k) + 3.0f;
         if (t < best) best = t, p.parts = k;
     }
-    p.grid = p.rounds ? most : p.rest * p.parts;
+    p.grid = p.whole ? most : p.rest * p.parts;
     return p;
 }
 
