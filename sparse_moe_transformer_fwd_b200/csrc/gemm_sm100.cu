@@ -454,7 +454,12 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA
-        if (lane == 0) {
+        // One lane; the block-scaled MMA's instance runs the loop as a whole warp
+        // and issues from an elected lane, so the descriptors live in uniform
+        // registers (its MMA thread sets the pace: dense prefill 1750 -> 1540 us;
+        // the promotion's instances are paced by their epilogue, and lost 2 %).
+        auto all = [](bool ok) { return MX ? __all_sync(0xffffffffu, ok) != 0 : ok; };
+        if (MX || lane == 0) {
             constexpr uint32_t idesc = MX ? instr_desc_mx(BM, BN) : instr_desc<FP8>(TM, BN);
             int stage = 0;
             uint32_t phase = 0;
@@ -470,18 +475,18 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const bool chunk_first = (kb % SPC) == 0;
                     const bool chunk_last = (kb % SPC) == SPC - 1 || kb == nk - 1;
                     if (chunk_first) {
-                        if (!mbar_wait(&s.tempty[tb], tphase ^ 1, abort, p.status)) {
+                        if (!all(mbar_wait(&s.tempty[tb], tphase ^ 1, abort, p.status))) {
                             ok = false;
                             break;
                         }
                     }
                     const bool group_first = MX && (kb % SF_GROUP) == 0;
                     if (group_first &&
-                        !mbar_wait(&s.sf_ready[gq % SF_BUFS], (gq / SF_BUFS) & 1, abort, p.status)) {
+                        !all(mbar_wait(&s.sf_ready[gq % SF_BUFS], (gq / SF_BUFS) & 1, abort, p.status))) {
                         ok = false;
                         break;
                     }
-                    if (!mbar_wait(&s.full[stage], phase, abort, p.status)) {
+                    if (!all(mbar_wait(&s.full[stage], phase, abort, p.status))) {
                         ok = false;
                         break;
                     }
@@ -491,41 +496,42 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                                             (M64 ? static_cast<uint32_t>((kb & 1) * 16) << 16 : 0u);
                     const uint64_t adesc = smem_desc_sw128(smem_u32(s.a[stage]));
                     const uint64_t bdesc = smem_desc_sw128(smem_u32(s.b[stage]));
-                    if (group_first) {
-                        // the group's scale block into TMEM, ordered before its MMAs
-                        // and after the previous group's, which read the same columns;
-                        // the commit frees the shared-memory block once it is copied
-                        const int buf = gq % SF_BUFS;
-                        const uint32_t sf = smem_u32(s.sf[buf]);
-                        tc_cp_32x128b_warpx4(tmem_base + SF_COL, smem_desc_plain(sf, 128));
-                        tc_cp_32x128b_warpx4(tmem_base + SF_COL + 4, smem_desc_plain(sf + 512, 128));
-                        tc_cp_32x128b_warpx4(tmem_base + SF_COL + 8, smem_desc_plain(sf + 1024, 128));
-                        tc_commit(&s.sf_free[buf]);
-                        ++gq;
-                    }
-                    // MX: this K block's scales are byte kb % 4 of each scale column
-                    // (the id in the instruction descriptor and in the TMEM address)
-                    const uint32_t sid = static_cast<uint32_t>(kb % SF_GROUP);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        // +32 bytes of K per instruction: +2 in the >>4 address field;
-                        // each K chunk (M64: each K step) starts a fresh partial sum
-                        const uint32_t acc = ((M64 || chunk_first) && kk == 0) ? 0u : 1u;
-                        if constexpr (MX)
-                            tc_mma_mx(d_tmem, adesc + 2 * kk, bdesc + 2 * kk,
-                                      idesc | (sid << 29) | (sid << 4),
-                                      (tmem_base + SF_COL) | (sid << 30),
-                                      (tmem_base + SF_COL + 4) | (sid << 30), acc);
-                        else
-                            tc_mma<FP8>(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, idesc, acc);
-                    }
-                    tc_commit(&s.empty[stage]);
-                    if (chunk_last) {
-                        tc_commit(&s.tfull[tb]);
-                        if (++tb == R::NBUF) {
-                            tb = 0;
-                            tphase ^= 1;
+                    if (!MX || elect_one()) {
+                        if (group_first) {
+                            // the group's scale block into TMEM, ordered before its MMAs
+                            // and after the previous group's, which read the same columns;
+                            // the commit frees the shared-memory block once it is copied
+                            const int buf = gq % SF_BUFS;
+                            const uint32_t sf = smem_u32(s.sf[buf]);
+                            tc_cp_32x128b_warpx4(tmem_base + SF_COL, smem_desc_plain(sf, 128));
+                            tc_cp_32x128b_warpx4(tmem_base + SF_COL + 4, smem_desc_plain(sf + 512, 128));
+                            tc_cp_32x128b_warpx4(tmem_base + SF_COL + 8, smem_desc_plain(sf + 1024, 128));
+                            tc_commit(&s.sf_free[buf]);
                         }
+                        // MX: this K block's scales are byte kb % 4 of each scale column
+                        // (the id in the instruction descriptor and in the TMEM address)
+                        const uint32_t sid = static_cast<uint32_t>(kb % SF_GROUP);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            // +32 bytes of K per instruction: +2 in the >>4 address field;
+                            // each K chunk (M64: each K step) starts a fresh partial sum
+                            const uint32_t acc = ((M64 || chunk_first) && kk == 0) ? 0u : 1u;
+                            if constexpr (MX)
+                                tc_mma_mx(d_tmem, adesc + 2 * kk, bdesc + 2 * kk,
+                                          idesc | (sid << 29) | (sid << 4),
+                                          (tmem_base + SF_COL) | (sid << 30),
+                                          (tmem_base + SF_COL + 4) | (sid << 30), acc);
+                            else
+                                tc_mma<FP8>(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, idesc, acc);
+                        }
+                        tc_commit(&s.empty[stage]);
+                        if (chunk_last) tc_commit(&s.tfull[tb]);
+                    }
+                    if constexpr (MX) __syncwarp();
+                    if (group_first) ++gq;
+                    if (chunk_last && ++tb == R::NBUF) {
+                        tb = 0;
+                        tphase ^= 1;
                     }
                     if (++stage == STAGES) {
                         stage = 0;
@@ -534,7 +540,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 }
             }
             // all MMAs issued by this thread are complete before TMEM is freed
-            tc_commit(&s.mma_done);
+            if (!MX || elect_one()) tc_commit(&s.mma_done);
             long long t0 = clock64();
             while (!mbar_try_wait(&s.mma_done, 0)) {
                 if (clock64() - t0 > kWaitBudgetCycles) {

@@ -7,7 +7,9 @@
 //
 // Few tokens read each weight byte for few FLOP, so the product is bound by
 // HBM: N*K bytes of weights.  The weights are therefore the M operand of the MMA
-// (128 rows of W a tile, tokens the N operand: 16, 32 or 64 columns).  A CTA's
+// (128 rows of W a tile, tokens the N operand: 16, 32 or 64 columns; more tokens
+// take several groups of columns, tiles of their own that read the same weights
+// from L2 at about the same time).  A CTA's
 // first tile is its own number, then it takes the next free one (HBM serves some
 // SMs faster: of 7168 x 64007 in equal shares the first CTA ended after 58 us,
 // the last after 76).  The tiles past the last whole round (all of them, where
@@ -81,6 +83,7 @@ struct LinearParams {
     LinearCounters *counters;  // zero between launches
     int *status;
     int T, N, KB;
+    int groups;   // of NT tokens: tile = (128 rows of W) * groups + group
     int whole;    // tiles worked on whole: the first ones
     int rest;     // tiles after them
     int parts;    // parts of K of each of those
@@ -91,9 +94,9 @@ struct LinearParams {
     int early_w;  // W may be read ahead of the kernel before this one
 };
 
-// K blocks kb0 .. kb0 + nk - 1 of one tile.
+// K blocks kb0 .. kb0 + nk - 1 of one tile: 128 rows of W from n0, NT tokens from t0.
 struct Segment {
-    int tile, kb0, nk;
+    int tile, n0, t0, kb0, nk;
     int part;  // of the cut tiles' parts, all of them
 };
 
@@ -163,13 +166,14 @@ __device__ __forceinline__ void add_parts(const float4 *partial, int parts, cons
 // The parts of all cut tiles, a thread four rows of a token.
 template <int NT>
 __global__ void __launch_bounds__(256)
-linear_sum_kernel(const float *__restrict__ partial, int first_tile, int rest, int parts, const LinearOut o) {
+linear_sum_kernel(const float *__restrict__ partial, int first_tile, int rest, int parts, int groups, const LinearOut o) {
     pdl_wait_and_trigger();
-    const int i = blockIdx.x * 256 + threadIdx.x;  // (tile, token, four rows)
-    const int lane = i & 31, t = (i >> 5) % o.T, tile = (i >> 5) / o.T;
-    if (tile >= rest) return;
+    const int i = blockIdx.x * 256 + threadIdx.x;  // (tile, token of its group, four rows)
+    const int lane = i & 31, t = (i >> 5) % NT, tile = (i >> 5) / NT;
+    const int row = (first_tile + tile) / groups, token = (first_tile + tile - row * groups) * NT + t;
+    if (tile >= rest || token >= o.T) return;
     add_parts<NT>(reinterpret_cast<const float4 *>(partial) + (static_cast<size_t>(tile) * parts * NT + t) * 32 + lane, parts, o,
-                  t, (first_tile + tile) * 128 + lane * 4);
+                  token, row * 128 + lane * 4);
 }
 
 template <int NT, bool XQ>
@@ -236,6 +240,9 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
             g.kb0 = k * KB / p.parts;
             g.nk = (k + 1) * KB / p.parts - g.kb0;
         }
+        const int row = g.tile / p.groups;
+        g.n0 = row * 128;
+        g.t0 = (g.tile - row * p.groups) * NT;
         return true;
     };
     // A role's items (whole warps): the CTA's number, then what the producer hands
@@ -268,15 +275,15 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
             int stage = 0;
             uint32_t phase = 0, armed = 0, armed_phase = 0;
             bool ok = true, waited = !p.early_w;
-            int first_x[STAGES], first_n[STAGES], behind = 0;  // stages whose activations wait for the kernel before
-            auto load_x = [&](int st, int x0, int n) {
+            int first_x[STAGES], first_t[STAGES], first_n[STAGES], behind = 0;  // stages whose activations wait for the kernel before
+            auto load_x = [&](int st, int x0, int t0, int n) {
                 for (int j = 0; j < n; ++j)
-                    tma_load_2d_policy(x_base + (2 * st + j) * S::X_BYTES, &tmap_x, x0 + j * 128, 0, f_base + st * 8, policy);
+                    tma_load_2d_policy(x_base + (2 * st + j) * S::X_BYTES, &tmap_x, x0 + j * 128, t0, f_base + st * 8, policy);
             };
             auto catch_up = [&] {
                 pdl_wait();
                 waited = true;
-                for (int i = 0; i < behind; ++i) load_x(i, first_x[i], first_n[i]);
+                for (int i = 0; i < behind; ++i) load_x(i, first_x[i], first_t[i], first_n[i]);
             };
             // the next free item is asked for while the one before is loaded, and
             // handed on once known
@@ -297,7 +304,7 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                 int next = id + gridDim.x;
                 const bool ask = taken && waited;  // (the launch before may hold the counter until then)
                 if (ask) next = gridDim.x + atomicAdd(&p.counters->next, 1);
-                int wx = p.w_rowmajor ? g.kb0 * 128 : 0, wy = p.w_rowmajor ? g.tile * 128 : (g.tile * KB + g.kb0) * 128;
+                int wx = p.w_rowmajor ? g.kb0 * 128 : 0, wy = p.w_rowmajor ? g.n0 : g.n0 * KB + g.kb0 * 128;
                 const int dx = p.w_rowmajor ? 128 : 0, dy = p.w_rowmajor ? 0 : 128;
                 int xx = g.kb0 * 128;
                 for (int left = g.nk; left > 0; left -= 2) {
@@ -312,8 +319,8 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                     tma_load_2d_policy(w, &tmap_w, wx, wy, bar, policy);
                     if (n == 2) tma_load_2d_policy(w + W_BYTES, &tmap_w, wx + dx, wy + dy, bar, policy);
                     if constexpr (!XQ) {
-                        if (waited) load_x(stage, xx, n);
-                        else first_x[behind] = xx, first_n[behind] = n, ++behind;  // the ring's first round: slot = behind
+                        if (waited) load_x(stage, xx, g.t0, n);
+                        else first_x[behind] = xx, first_t[behind] = g.t0, first_n[behind] = n, ++behind;  // the ring's first round: slot = behind
                     }
                     wx += 2 * dx, wy += 2 * dy, xx += 2 * 128;
                     armed |= 1u << stage;
@@ -398,7 +405,7 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
         Taken item;
         Segment g;
         while (ok && next_segment(item, g)) {
-            const float *ws = p.w_scales + static_cast<size_t>(g.tile) * KB;
+            const float *ws = p.w_scales + static_cast<size_t>(g.n0 / 128) * KB;
             for (int kb = g.kb0 + j; kb - j < g.kb0 + g.nk; kb += 2) {
                 if (!__all_sync(0xffffffffu, mbar_wait(&s.sempty[slot], phase ^ 1, abort, p.status))) {
                     ok = false;
@@ -408,7 +415,8 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                     if constexpr (!XQ)
 #pragma unroll
                         for (int t = lane; t < NT; t += 32)
-                            cp_async4(&s.sc[slot].x[j][t], p.a_scales + (t < p.T ? static_cast<size_t>(t) * KB + kb : 0), t < p.T);
+                            cp_async4(&s.sc[slot].x[j][t], p.a_scales + (g.t0 + t < p.T ? static_cast<size_t>(g.t0 + t) * KB + kb : 0),
+                                      g.t0 + t < p.T);
                     if (lane == 0) cp_async4(&s.sc[slot].w[j], ws + kb, true);
                 }
                 cp_async_mbar_arrive(&s.sfull[slot]);
@@ -571,19 +579,20 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                 }
             }
             auto sum = [&](int t) { return t & 1 ? acc[t >> 1].y : acc[t >> 1].x; };
+            const int T = p.T - g.t0;  // tokens from the group's first on
             if (g.nk == KB) {
-                const int n = g.tile * 128 + r;
+                const int n = g.n0 + r;
                 if (ok && n < p.N) {
 #pragma unroll
                     for (int t0 = 0; t0 < NT; t0 += 16) {
-                        const size_t at = static_cast<size_t>(t0) * p.N + n;
+                        const size_t at = static_cast<size_t>(g.t0 + t0) * p.N + n;
                         float res[16];
 #pragma unroll
                         for (int t = 0; t < 16; ++t)
-                            res[t] = p.residual && t0 + t < p.T ? bf16_f(p.residual[at + static_cast<size_t>(t) * p.N]) : 0.0f;
+                            res[t] = p.residual && t0 + t < T ? bf16_f(p.residual[at + static_cast<size_t>(t) * p.N]) : 0.0f;
 #pragma unroll
                         for (int t = 0; t < 16; ++t)
-                            if (t0 + t < p.T) out.store(at + static_cast<size_t>(t) * p.N, sum(t0 + t), res[t]);
+                            if (t0 + t < T) out.store(at + static_cast<size_t>(t) * p.N, sum(t0 + t), res[t]);
                     }
                 }
             } else {
@@ -593,7 +602,7 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                 if (ok) {
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
-                        if (t < p.T) mine[t * 128] = sum(t);
+                        if (t < T) mine[t * 128] = sum(t);
                 }
                 if (!p.sum_here) continue;
                 named_bar_sync(1, 128);
@@ -610,7 +619,7 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                     for (int t = q; t < p.T; t += 4)
                         add_parts<NT>(reinterpret_cast<const float4 *>(p.partial) +
                                           (static_cast<size_t>(tile) * p.parts * NT + t) * 32 + lane,
-                                      p.parts, out, t, g.tile * 128 + lane * 4);
+                                      p.parts, out, t, g.n0 + lane * 4);
                 named_bar_sync(1, 128);  // s.last is rewritten by the next part
             }
         }
@@ -747,10 +756,10 @@ linear_finish_kernel(const float *__restrict__ partial, int ksplit, int T, int N
 template <int NT, bool XQ>
 cudaError_t launch_stream_t(const LinearStreamArgs &g, cudaStream_t st, int *launches) {
     CUtensorMap mx, mw;
-    const int tiles = (g.N + 127) / 128, KB = g.K / 128;
+    const int rows = (g.N + 127) / 128, KB = g.K / 128, groups = (g.T + NT - 1) / NT, tiles = rows * groups;
     std::memset(&mx, 0, sizeof mx);
     if (!XQ && !make_map_2d(&mx, g.a, true, g.K, g.T, NT)) return cudaErrorInvalidValue;
-    if (g.w_rowmajor ? !make_map_2d(&mw, g.w, true, g.K, g.N) : !make_map_2d(&mw, g.w, true, 128, tiles * KB * 128))
+    if (g.w_rowmajor ? !make_map_2d(&mw, g.w, true, g.K, g.N) : !make_map_2d(&mw, g.w, true, 128, rows * KB * 128))
         return cudaErrorInvalidValue;
     constexpr size_t smem = sizeof(LinearSmem<NT>) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory budget of one CTA");
@@ -774,6 +783,7 @@ cudaError_t launch_stream_t(const LinearStreamArgs &g, cudaStream_t st, int *lau
     p.N = g.N;
     p.KB = KB;
     const LinearPlan plan = linear_plan(g.T, tiles, KB);
+    p.groups = groups;
     p.whole = plan.whole;
     p.rest = plan.rest;
     p.parts = plan.parts;
@@ -790,8 +800,8 @@ cudaError_t launch_stream_t(const LinearStreamArgs &g, cudaStream_t st, int *lau
     if (plan.parts == 1 || p.sum_here) return cudaSuccess;
     mark_launch(st, *launches, "linear_sum");
     const LinearOut out{g.residual, g.out, g.T, g.N, g.out_f32};
-    LAUNCH_OR_RETURN(launch_pdl(linear_sum_kernel<NT>, dim3((plan.rest * g.T * 32 + 255) / 256), dim3(256), 0, st, g.partial,
-                                plan.whole, plan.rest, plan.parts, out));
+    LAUNCH_OR_RETURN(launch_pdl(linear_sum_kernel<NT>, dim3(plan.rest * NT / 8), dim3(256), 0, st, g.partial, plan.whole,
+                                plan.rest, plan.parts, groups, out));
     ++*launches;
     return cudaSuccess;
 }
