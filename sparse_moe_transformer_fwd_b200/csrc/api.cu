@@ -1149,7 +1149,6 @@ namespace {
 // zero-filled workspace serves linears of any shapes: each launch leaves the
 // counters zero, and no other region of another shape reaches them.
 constexpr int kLinearMaxN = 1 << 20;
-constexpr int kLinearSplitRows = 256;  // as the dense down GEMM: K split up to here
 
 int check_linear_shape(const moe_linear_shape *s) {
     if (!s) return fail(MOE_ERR_INVALID_ARG, "shape is NULL");
@@ -1188,14 +1187,51 @@ bool linear_quantises(const moe_linear_shape *s) {
            static_cast<long long>(tiles) * KB <= 16LL * linear_plan(s->T, tiles, KB).grid;
 }
 
-// K ranges of the tiled GEMM, by the dense down GEMM's rule: few output tiles
-// leave SMs idle, so up to kMaxSplitK ranges of at least two K blocks.
-int linear_ksplit(const moe_linear_shape *s) {
-    if (s->T > kLinearSplitRows) return 1;
+// Which kernel a batch takes, and the K ranges of the tiled GEMM: by the time
+// that each would need, in us, from measured parts.
+//   stream (linear_plan): 0.15, 0.2 or 0.38 a K block of a 128-row tile with 16,
+//     32 or 64 token columns; 4.5 to start and end; 3 where tiles are cut
+//   tiled: 0.58 a K block of a 128-token x 256-column tile; 4 to start and end;
+//     where sums are added or stored by a second kernel 5, and their bytes
+//     written and read at 4 TB/s
+//   both at least the weights, at 7 and 5.5 TB/s
+// The tiled GEMM needs enough tiles: 128 tokens, 7168 x 2112 (9 tiles) 23.7 us
+// against 11.4 in the stream kernel; 128 tokens, 16384 x 7168 39.6 against 52.
+struct LinearChoice {
+    bool stream;
+    int ksplit;
+};
+
+int linear_most_splits(const moe_linear_shape *s, int sms) {
     const int tiles = gemm_output_tiles(s->T, linear_padded_n(s));
-    int ks = std::min(num_sms() / std::max(tiles, 1), kMaxSplitK);
-    ks = std::min(ks, s->K / 256);
-    return std::max(ks, 1);
+    return std::max(1, std::min({kMaxSplitK, sms / std::max(tiles, 1), s->K / 256}));
+}
+
+LinearChoice linear_choice(const moe_linear_shape *s) {
+    LinearChoice c{s->T <= kLinearQuantRows, 1};
+    if (c.stream || s->T == 0) return c;
+    const int sms = std::min(num_sms(), kLinearMaxCtas), KB = s->K / 128;
+    const float bytes = static_cast<float>(s->N) * s->K;
+    const bool direct = linear_direct(s) || s->N % 256 == 0;  // binary32 sums may be the output (no residual)
+    const long long tiles = gemm_output_tiles(s->T, linear_padded_n(s));
+    const float plane = 8.0f * s->T * linear_padded_n(s) / 4e6f;  // binary32 sums written and read
+    float best = 0.0f;
+    for (int k = 1; k <= linear_most_splits(s, sms); ++k) {
+        const long long steps = (tiles * k + sms - 1) / sms * ((KB + k - 1) / k);
+        const float t = 4.0f + std::max(0.58f * steps, bytes / 5.5e6f) + (k > 1 || !direct ? 5.0f + plane * k : 0.0f);
+        if (k == 1 || t < best) best = t, c.ksplit = k;
+    }
+    if (s->T <= kLinearStreamRows) {
+        const int columns = s->T <= 32 ? 32 : 64;
+        const int rows = (s->N + 127) / 128, all = rows * ((s->T + columns - 1) / columns);
+        const LinearPlan p = linear_plan(s->T, all, KB);
+        const int whole = p.whole / sms + (p.rest && p.parts == 1 ? 1 : 0);
+        const float t = 4.5f + std::max(bytes / 7e6f, (columns == 32 ? 0.2f : 0.38f) *
+                                                   (whole * KB + (p.parts > 1 ? (KB + p.parts - 1) / p.parts : 0))) +
+                        (p.parts > 1 ? 3.0f : 0.0f);
+        c.stream = t <= best;
+    }
+    return c;
 }
 
 struct LinearLayout {
@@ -1215,12 +1251,13 @@ LinearLayout linear_layout(const moe_linear_shape *s) {
     L.counters = take(sizeof(LinearCounters));
     L.a = take(T * K);
     L.a_scales = take(T * (K / 128) * 4);
-    if (s->T <= kLinearStreamRows)
-        L.partial = take(linear_partial_floats(s->T) * 4);
-    else if (s->T <= kLinearSplitRows)
-        L.partial = take(kMaxSplitK * T * linear_padded_n(s) * 4);
-    else
-        L.partial = take(linear_direct(s) ? 0 : T * linear_padded_n(s) * 4);
+    // either kernel's partial sums, for any SM count
+    size_t partial = s->T <= kLinearStreamRows ? linear_partial_floats(s->T) : 0;
+    if (s->T > kLinearQuantRows) {
+        const int k = linear_most_splits(s, kLinearMaxCtas);
+        if (k > 1 || !linear_direct(s)) partial = std::max(partial, static_cast<size_t>(k) * T * linear_padded_n(s));
+    }
+    L.partial = take(partial * 4);
     L.total = off;
     return L;
 }
@@ -1233,7 +1270,8 @@ int linear_product(const moe_linear_shape *s, const uint16_t *x, const void *a, 
                    const float *w_scales, const uint16_t *residual, void *out, void *ws,
                    const LinearLayout &L, cudaStream_t st, int *n) {
     float *partial = at<float>(ws, L.partial);
-    if (s->T <= kLinearStreamRows) {
+    const LinearChoice choice = linear_choice(s);
+    if (choice.stream) {
         LinearStreamArgs g{};
         g.x = x;
         g.ue8m0 = s->precision == MOE_FP8_UE8M0;
@@ -1255,7 +1293,7 @@ int linear_product(const moe_linear_shape *s, const uint16_t *x, const void *a, 
         LAUNCH(launch_linear_stream(g, st, n), "linear");
         return MOE_OK;
     }
-    const int ks = linear_ksplit(s);
+    const int ks = choice.ksplit;
     // binary32 outputs of whole tiles without a residual are the sums themselves
     const bool in_place = ks == 1 && s->out_f32 && s->N % 256 == 0 && !residual;
     const bool sums = ks > 1 || !linear_direct(s);

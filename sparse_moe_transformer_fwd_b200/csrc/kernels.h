@@ -204,7 +204,7 @@ cudaError_t launch_few(const FewArgs &g, cudaStream_t st, int *launches);
 
 // Block-scaled product that streams the weights, for at most kLinearStreamRows
 // tokens (linear.cu).
-constexpr int kLinearStreamRows = 64;
+constexpr int kLinearStreamRows = 512;
 constexpr int kLinearMaxCtas = 160;  // CTAs of linear_stream (sizes its partial sums)
 // `whole` tiles (a multiple of the CTAs), then `rest` tiles of `parts` parts each.
 struct LinearPlan {

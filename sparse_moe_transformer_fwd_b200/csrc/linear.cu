@@ -240,9 +240,9 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
             g.kb0 = k * KB / p.parts;
             g.nk = (k + 1) * KB / p.parts - g.kb0;
         }
-        const int row = g.tile / p.groups;
+        const int row = NT == 64 ? g.tile / p.groups : g.tile;  // 16 and 32 columns hold the whole batch
         g.n0 = row * 128;
-        g.t0 = (g.tile - row * p.groups) * NT;
+        g.t0 = NT == 64 ? (g.tile - row * p.groups) * NT : 0;
         return true;
     };
     // A role's items (whole warps): the CTA's number, then what the producer hands
@@ -283,7 +283,7 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
             auto catch_up = [&] {
                 pdl_wait();
                 waited = true;
-                for (int i = 0; i < behind; ++i) load_x(i, first_x[i], first_t[i], first_n[i]);
+                for (int i = 0; i < behind; ++i) load_x(i, first_x[i], NT == 64 ? first_t[i] : 0, first_n[i]);
             };
             // the next free item is asked for while the one before is loaded, and
             // handed on once known
@@ -320,7 +320,7 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                     if (n == 2) tma_load_2d_policy(w + W_BYTES, &tmap_w, wx + dx, wy + dy, bar, policy);
                     if constexpr (!XQ) {
                         if (waited) load_x(stage, xx, g.t0, n);
-                        else first_x[behind] = xx, first_t[behind] = g.t0, first_n[behind] = n, ++behind;  // the ring's first round: slot = behind
+                        else first_x[behind] = xx, first_t[behind] = NT == 64 ? g.t0 : 0, first_n[behind] = n, ++behind;  // the ring's first round: slot = behind
                     }
                     wx += 2 * dx, wy += 2 * dy, xx += 2 * 128;
                     armed |= 1u << stage;
