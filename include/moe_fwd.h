@@ -460,8 +460,8 @@ int moe_forward_few_prenorm(const moe_shape *shape, const uint16_t *h, const uin
  *   out[t, n] = sum_kb s_a[t, kb] * s_w[n / 128, kb] *
  *                      (sum over the 128 columns of K block kb of a * w)
  *               (+ residual[t, n])
- * with a the codes of x in 1x128 tiles and w those of 128x128 blocks.  Sums are binary32; the residual is added before
- * the one rounding of a bf16 output.
+ * with a the codes of x in 1x128 tiles and w those of 128x128 blocks.  Sums
+ * are binary32; the residual is added before the one rounding of a bf16 output.
  * Shapes: K a multiple of 128; any N >= 1 (row-major weights: the last block
  * row may be short, as fp8_block_quant writes it) or a multiple of 128 (tiled
  * weights); K and N at most 2^20; T >= 0 (T = 0 enqueues nothing); precision

@@ -411,9 +411,21 @@ def moe_few_workspace_size(shape: MoeShape) -> int:
     return n
 
 
+def _zeroed(nbytes, device):
+    """A workspace whose counters are zero before any call reads them, on
+    whatever stream.  A capture would record the zeroing instead of doing it."""
+    cuda = torch.device(device).type == "cuda"
+    if cuda and torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("allocate the workspace (or make one call of this size) before the capture")
+    ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    if cuda:
+        torch.cuda.current_stream(ws.device).synchronize()
+    return ws
+
+
 def alloc_few_workspace(shape: MoeShape, device="cuda") -> torch.Tensor:
     """A zero-filled workspace of moe_few_workspace_size bytes."""
-    return torch.zeros(moe_few_workspace_size(shape), dtype=torch.uint8, device=device)
+    return _zeroed(moe_few_workspace_size(shape), device)
 
 
 def _few_call(fn, shape, x, gamma, eps, w_router, bias, w13, w13_scales, w2, w2_scales, out, ws,
@@ -429,7 +441,7 @@ def _few_call(fn, shape, x, gamma, eps, w_router, bias, w13, w13_scales, w2, w2_
              _arg(w13, wt, n13, dev, "w13"), _arg(w13_scales, _F32S, n13 // 16384 if fp8 else 0, dev, "w13_scales"),
              _arg(w2, wt, n2, dev, "w2"), _arg(w2_scales, _F32S, n2 // 16384 if fp8 else 0, dev, "w2_scales"),
              _arg(out, _BF16S, T * d, dev, "out"), _arg(topk_idx_out, _I32S, T * shape.top_k, dev, "topk_idx_out"),
-             _arg(ws, _U8S, 0, dev, "ws"), ws.numel()]
+             *_workspace(ws, dev)]
     _call_on(dev, stream, fn, shape, args)
 
 
@@ -467,7 +479,7 @@ def moe_linear_workspace_size(shape: MoeLinearShape) -> int:
 
 def alloc_linear_workspace(shape: MoeLinearShape, device="cuda") -> torch.Tensor:
     """A zero-filled workspace of moe_linear_workspace_size bytes."""
-    return torch.zeros(moe_linear_workspace_size(shape), dtype=torch.uint8, device=device)
+    return _zeroed(moe_linear_workspace_size(shape), device)
 
 
 _BF16S, _F32S, _I32S, _U8S = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.uint8,)
@@ -510,6 +522,12 @@ def _arg(t, dtypes, numel, dev, name):
     return t.data_ptr()
 
 
+def _workspace(ws, dev):
+    if ws is None:
+        raise TypeError("ws: expected a torch.Tensor")
+    return _arg(ws, _U8S, 0, dev, "ws"), ws.numel()
+
+
 def _call_on(dev, stream, fn, shape, args) -> None:
     """fn(shape, *args, stream) with `dev` current, on `stream` or the current
     stream of `dev`."""
@@ -534,7 +552,7 @@ def fp8_block_gemm(shape, a, a_scales, w, w_scales, out, ws, residual=None, stre
     wp, wsp, op = _linear_args(shape, w, w_scales, out, dev)
     _call_on(dev, stream, _fn("fp8_block_gemm"), shape,
              (_arg(a, _FP8, T * K, dev, "a"), _arg(a_scales, _F32S, T * (K // 128), dev, "a_scales"), wp, wsp,
-              _arg(residual, _BF16S, T * shape.N, dev, "residual"), op, _arg(ws, _U8S, 0, dev, "ws"), ws.numel()))
+              _arg(residual, _BF16S, T * shape.N, dev, "residual"), op, *_workspace(ws, dev)))
 
 
 def moe_linear(shape, x, w, w_scales, out, ws, residual=None, stream=None):
@@ -543,7 +561,7 @@ def moe_linear(shape, x, w, w_scales, out, ws, residual=None, stream=None):
     wp, wsp, op = _linear_args(shape, w, w_scales, out, dev)
     _call_on(dev, stream, _fn("moe_linear"), shape,
              (_arg(x, _BF16S, T * shape.K, dev, "x"), wp, wsp, _arg(residual, _BF16S, T * shape.N, dev, "residual"),
-              op, _arg(ws, _U8S, 0, dev, "ws"), ws.numel()))
+              op, *_workspace(ws, dev)))
 
 
 def moe_linear_prenorm(shape, h, gamma, eps, w, w_scales, out, ws, stream=None):
@@ -552,7 +570,7 @@ def moe_linear_prenorm(shape, h, gamma, eps, w, w_scales, out, ws, stream=None):
     wp, wsp, op = _linear_args(shape, w, w_scales, out, dev)
     _call_on(dev, stream, _fn("moe_linear_prenorm"), shape,
              (_arg(h, _BF16S, T * shape.K, dev, "h"), _arg(gamma, _BF16S, shape.K, dev, "gamma"), eps, wp, wsp, op,
-              _arg(ws, _U8S, 0, dev, "ws"), ws.numel()))
+              *_workspace(ws, dev)))
 
 
 def moe_check_status(ws, stream=None) -> int:

@@ -99,10 +99,11 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 // the environment: MOE_FAULT_INJECT=gemm_tx makes the first grouped GEMM of
 // the call arm one pipeline stage for bytes that never arrive, so its
 // consumer's wait runs out and the call reports MOE_ERR_TIMEOUT through the
-// status word (the kernel then drains and exits normally).
-bool inject_gemm_fault() {
+// status word (the kernel then drains and exits normally); few_scored makes
+// moe_forward_few's exact routing wait for one block more than there are.
+bool inject_fault(const char *which) {
     const char *v = getenv("MOE_FAULT_INJECT");
-    return v && strcmp(v, "gemm_tx") == 0;
+    return v && strcmp(v, which) == 0;
 }
 
 int check_device() {
@@ -265,7 +266,7 @@ int grouped(const moe_shape *s, const void *a, const float *a_scales, const void
     g.seg_rows = ps.seg_rows;
     g.tile_start = ps.tile_start;
     g.status = at<int>(ws, L.status);
-    g.inject_fault = inject_gemm_fault() ? 1 : 0;
+    g.inject_fault = inject_fault("gemm_tx") ? 1 : 0;
     g.ue8m0 = is_ue8m0(s);
     g.tile_m = tile_m;
     g.b_rowmajor = s->weight_layout == MOE_LAYOUT_ROWMAJOR;
@@ -1106,6 +1107,7 @@ int few_impl(const moe_shape *s, const uint16_t *x, const uint16_t *gamma, float
     g.list_rows = L.list_rows;
     g.counters = at<FewCounters>(ws, L.counters);
     g.status = at<int>(ws, L.status);
+    g.inject_fault = inject_fault("few_scored") ? 1 : 0;
     LAUNCH(launch_few(g, st, &n), "moe few");
     mark_launch(st, n);
     g_launches = n;

@@ -174,7 +174,7 @@ struct FewCounters {
     int prepared, scored, exited, abort, next;
     int pad[59];
     int h_done[kFewMaxList + 63];  // [list position] gate/up items done
-    int col_done[kFewMaxCols];     // [128-column block] experts' down items done
+    int col_done[kFewMaxCols];     // [128-column block] stages of the experts' down items done
 };
 struct FewArgs {
     const moe_shape *shape;
@@ -196,6 +196,7 @@ struct FewArgs {
     int list_rows;
     FewCounters *counters;
     int *status;
+    int inject_fault;  // test hook: make one bounded wait run out (see api.cu)
 };
 // xn = bf16((h * rstd) * gamma) of T tokens, rstd as launch_rstd's.
 cudaError_t launch_few_prenorm(const uint16_t *h, const uint16_t *gamma, int T, int d, float eps, uint16_t *xn,
