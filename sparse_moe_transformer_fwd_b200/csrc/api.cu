@@ -1191,8 +1191,7 @@ bool linear_quantises(const moe_linear_shape *s) {
 
 // Which kernel a batch takes, and the K ranges of the tiled GEMM: by the time
 // that each would need, in us, from measured parts.
-//   stream (linear_plan): 0.15, 0.2 or 0.38 a K block of a 128-row tile with 16,
-//     32 or 64 token columns; 4.5 to start and end; 3 where tiles are cut
+//   stream: linear_plan's, and 4.5 to start and end
 //   tiled: 0.58 a K block of a 128-token x 256-column tile; 4 to start and end;
 //     where sums are added or stored by a second kernel 5, and their bytes
 //     written and read at 4 TB/s
@@ -1226,12 +1225,7 @@ LinearChoice linear_choice(const moe_linear_shape *s) {
     if (s->T <= kLinearStreamRows) {
         const int columns = s->T <= 32 ? 32 : 64;
         const int rows = (s->N + 127) / 128, all = rows * ((s->T + columns - 1) / columns);
-        const LinearPlan p = linear_plan(s->T, all, KB);
-        const int whole = p.whole / sms + (p.rest && p.parts == 1 ? 1 : 0);
-        const float t = 4.5f + std::max(bytes / 7e6f, (columns == 32 ? 0.2f : 0.38f) *
-                                                   (whole * KB + (p.parts > 1 ? (KB + p.parts - 1) / p.parts : 0))) +
-                        (p.parts > 1 ? 3.0f : 0.0f);
-        c.stream = t <= best;
+        c.stream = 4.5f + std::max(bytes / 7e6f, linear_plan(s->T, all, KB).us) <= best;
     }
     return c;
 }

@@ -207,14 +207,16 @@ cudaError_t launch_few(const FewArgs &g, cudaStream_t st, int *launches);
 // tokens (linear.cu).
 constexpr int kLinearStreamRows = 512;
 constexpr int kLinearMaxCtas = 160;  // CTAs of linear_stream (sizes its partial sums)
-// `whole` tiles (a multiple of the CTAs), then `rest` tiles of `parts` parts each.
+// `whole` tiles (a multiple of the CTAs), then `rest` tiles of `parts` parts
+// each, added by a cluster or by a second kernel; the time that the tiles take.
 struct LinearPlan {
     int grid, whole, rest, parts;
+    bool cluster;
+    float us;
 };
 // Counters of one launch: zero before it, and left zero.
 struct LinearCounters {
     int next, exited;
-    int parts[kLinearMaxCtas];  // [cut tile] parts stored
 };
 LinearPlan linear_plan(int T, int tiles, int KB);
 constexpr int kLinearQuantRows = 16;  // and of bf16 x, quantised in the same kernel

@@ -13,11 +13,11 @@
 // it takes the next free one (HBM serves some SMs faster: of 7168 x 64007 in
 // equal shares the first CTA ended after 58 us, the last after 76).  The tiles
 // past the last whole round (all of them, where there are fewer than SMs) are
-// cut into equal parts of K, as many as pay (linear_plan); each part's CTA
-// stores its binary32 partial sums in the workspace.  They are added in K order,
-// so the result does not depend on timing: for a few tokens by the last of a
-// tile's CTAs, which count themselves in, else by a second kernel, all SMs of it
-// (64 tokens in two parts: 3 us, and 13 by one CTA a tile).
+// cut into equal parts of K, as many as pay (linear_plan).  The parts' binary32
+// sums are added in K order, so the result does not depend on timing: where all
+// tiles are cut, in 3 to 16 parts, a tile's CTAs are one cluster that exchanges
+// them through shared memory (1.5 us); else they go to the workspace and a second
+// kernel adds them (3 us; a tile's last CTA alone took 13 with 64 tokens).
 //   warp 0      TMA producer: a stage is two K blocks (two 16 KB boxes of W, two
 //               boxes of activations)
 //   warp 1      TMEM allocator and MMA issuer: a stage's K blocks go to adjacent
@@ -34,16 +34,16 @@
 // and end take 4.5; 7 tokens, 7168 x 64007 77 us (5.9 TB/s); 64 tokens with a
 // residual, 16384 x 7168 32 us (3.6 TB/s: the reads of scales and operands from
 // shared memory bound 64 columns).
-// Every wait is bounded; on expiry the block records MOE_ERR_TIMEOUT, counts
-// itself in on its tiles without adding, drains its loads and MMAs, frees its
-// TMEM and exits.  The counters return to zero all the same: a cut tile's by its
-// last CTA, and where items are handed on (a block that gave up does not learn
-// of the rest) all of them by the last CTA out.
+// Every wait is bounded; on expiry the block records MOE_ERR_TIMEOUT, drains its
+// loads and MMAs, frees its TMEM and exits; the last CTA out zeroes the item
+// counter.  (A cluster's barrier has no limit of its own: every CTA reaches it,
+// since its other waits end.)
 #include "common.cuh"
 #include "kernels.h"
 #include "quant_math.cuh"
 
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 
 namespace moe {
@@ -53,7 +53,7 @@ constexpr int W_BYTES = 128 * 128;  // one tile of weights
 constexpr int SC_RING = 8;          // scale slots (two K blocks each)
 constexpr int QUEUE = 4;            // work items between the producer and the other roles
 constexpr int XQ_WARPS = 5;         // warps that quantise x
-constexpr int kSumHere = 4;         // tokens up to which a tile's last CTA adds its parts
+constexpr int MAX_CLUSTER = 16;     // parts that a cluster adds
 
 template <int NT>
 struct LinearSmem {
@@ -63,6 +63,12 @@ struct LinearSmem {
     static_assert(STAGES * 2 * NT <= TMEM_COLS, "accumulators of the ring's stages");
     alignas(1024) uint8_t w[STAGES][2][W_BYTES];
     alignas(1024) uint8_t x[STAGES][2][X_BYTES];
+    // the cluster's sums for this CTA's share of the tile, [part][share][4 tokens]
+    // (64 columns: in the ring, once every CTA is through with its own)
+    static constexpr bool SUMS_IN_RING = NT == 64;
+    static constexpr int SUMS = NT * 32 + MAX_CLUSTER;
+    alignas(16) float4 sums[SUMS_IN_RING ? 1 : SUMS];
+    static_assert(SUMS * 16 <= static_cast<int>(sizeof(w)), "the sums in the ring");
     struct alignas(16) Scales {
         float x[2][NT];
         float w[2];
@@ -76,7 +82,6 @@ struct LinearSmem {
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort;
-    int last;
 };
 
 struct LinearParams {
@@ -92,7 +97,8 @@ struct LinearParams {
     int whole;    // tiles worked on whole: the first ones
     int rest;     // tiles after them
     int parts;    // parts of K of each of those
-    int sum_here; // the last of a tile's CTAs adds its parts (else a kernel after this one)
+    int cluster;  // a tile's parts are one cluster, which adds them (else a kernel after this one)
+    uint32_t share, per_share;  // of the tile's (4 tokens, row) pieces each CTA of the cluster adds; ceil(2^32 / share)
     int out_f32;
     int w_rowmajor;
     int ue;       // power-of-two scales (with XQ)
@@ -181,6 +187,16 @@ linear_sum_kernel(const float *__restrict__ partial, int first_tile, int rest, i
                   token, row * 128 + lane * 4);
 }
 
+// The cluster's barrier, per thread, and another CTA's copy of a shared address.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t cta, const float4 &v) {
+    uint32_t remote;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(cta));
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(remote), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+
 template <int NT, bool XQ>
 constexpr int ls_threads() { return (XQ ? 8 + XQ_WARPS : 8) * 32; }
 
@@ -225,10 +241,14 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
     tc_fence_after();
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, s.tmem_base, 0);
     volatile int *abort = &s.abort;
+    float4 *sums = S::SUMS_IN_RING ? reinterpret_cast<float4 *>(s.w) : s.sums;
     // The kernel before this one has finished when this returns; the producer
     // alone may read W ahead of it (early_w).
     if (!(warp == 0 && p.early_w)) pdl_wait();
     pdl_trigger();
+    // Cluster barriers: the first when every CTA may be written to, the second
+    // when the sums have arrived.
+    if (p.cluster && !S::SUMS_IN_RING) cluster_arrive();
 
     const int items = p.whole + p.rest * p.parts;
     auto decode = [&](int id, Segment &g) {
@@ -277,6 +297,7 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
         if (lane == 0) {
             const uint32_t w_base = smem_u32(s.w[0][0]), x_base = smem_u32(s.x[0][0]), f_base = smem_u32(&s.full[0]);
             const uint64_t policy = l2_evict_normal();
+            const int x_bytes = min(p.T, NT) * 128;
             int stage = 0;
             uint32_t phase = 0, armed = 0, armed_phase = 0;
             bool ok = true, waited = !p.early_w;
@@ -320,7 +341,7 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                     }
                     const int n = min(2, left);
                     const uint32_t bar = f_base + stage * 8, w = w_base + stage * 2 * W_BYTES;
-                    mbar_arrive_expect_tx(&s.full[stage], n * (W_BYTES + (XQ ? 0 : S::X_BYTES)));
+                    mbar_arrive_expect_tx(&s.full[stage], n * (W_BYTES + (XQ ? 0 : x_bytes)));
                     tma_load_2d_policy(w, &tmap_w, wx, wy, bar, policy);
                     if (n == 2) tma_load_2d_policy(w + W_BYTES, &tmap_w, wx + dx, wy + dy, bar, policy);
                     if constexpr (!XQ) {
@@ -601,48 +622,69 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                     }
                 }
             } else {
-                // one part of a tile: partial sums to the workspace, [token][128
-                // rows]; the last CTA adds them all, its own among them
-                float *mine = p.partial + static_cast<size_t>(g.part) * NT * 128 + r;
-                if (ok) {
+                // One part of a tile: [token][128 rows] to the workspace, or each
+                // piece to the CTA of the cluster that adds it.
+                if (!p.cluster) {
+                    float *mine = p.partial + static_cast<size_t>(g.part) * NT * 128 + r;
+                    if (ok) {
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        if (t < T) mine[t * 128] = sum(t);
+                        for (int t = 0; t < NT; ++t)
+                            if (t < T) mine[t * 128] = sum(t);
+                    }
+                    continue;
                 }
-                if (!p.sum_here) continue;
-                named_bar_sync(1, 128);
-                const int tile = g.tile - p.whole;
-                if (threadIdx.x == 128) {
-                    __threadfence();  // (covers what the barrier orders before it)
-                    const int last = atomicAdd(p.counters->parts + tile, 1) == p.parts - 1;
-                    if (last) p.counters->parts[tile] = 0;  // everyone has counted: zero for the next launch
-                    __threadfence();
-                    s.last = last;
+                if (S::SUMS_IN_RING) cluster_arrive();
+                cluster_wait();
+                const uint32_t at = smem_u32(sums) + (blockIdx.x % p.parts) * p.share * 16;
+#pragma unroll
+                for (int t = 0; t < NT; t += 4) {
+                    if (t >= T) break;
+                    const uint32_t piece = t / 4 * 128 + r, owner = __umulhi(piece, p.per_share);
+                    st_cluster(at + (piece - owner * p.share) * 16, owner, make_float4(sum(t), sum(t + 1), sum(t + 2), sum(t + 3)));
                 }
-                named_bar_sync(1, 128);
-                if (ok && s.last)
-                    for (int t = q; t < p.T; t += 4)
-                        add_parts<NT>(reinterpret_cast<const float4 *>(p.partial) +
-                                          (static_cast<size_t>(tile) * p.parts * NT + t) * 32 + lane,
-                                      p.parts, out, t, g.n0 + lane * 4);
-                named_bar_sync(1, 128);  // s.last is rewritten by the next part
+                cluster_arrive();
             }
         }
     }
 
+    if (p.cluster) {
+        if (warp < 4 || warp >= 8) {
+            if (S::SUMS_IN_RING) cluster_arrive();
+            cluster_wait();
+            cluster_arrive();
+        }
+        cluster_wait();
+        Segment g;
+        decode(blockIdx.x, g);
+        const int rank = blockIdx.x % p.parts;
+        const LinearOut out{p.residual, p.out, p.T, p.N, p.out_f32};
+        for (uint32_t i = threadIdx.x; i < p.share; i += blockDim.x) {
+            const int piece = rank * p.share + i, n = g.n0 + (piece & 127), t = g.t0 + (piece >> 7) * 4;
+            if (n >= p.N || t >= min(g.t0 + NT, p.T)) continue;
+            const size_t at = static_cast<size_t>(t) * p.N + n;
+            float f[4] = {}, res[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                res[j] = p.residual && t + j < p.T ? bf16_f(p.residual[at + static_cast<size_t>(j) * p.N]) : 0.0f;
+            for (int k = 0; k < p.parts; ++k) {
+                const float4 v = sums[k * p.share + i];
+                f[0] = __fadd_rn(f[0], v.x), f[1] = __fadd_rn(f[1], v.y), f[2] = __fadd_rn(f[2], v.z), f[3] = __fadd_rn(f[3], v.w);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (t + j < p.T) out.store(at + static_cast<size_t>(j) * p.N, f[j], res[j]);
+        }
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, S::TMEM_COLS);
     }
-    // the last CTA out zeroes the counters for the next launch
+    // the last CTA out zeroes the item counter for the next launch
     if (threadIdx.x == 0 && taken) {
         __threadfence();
-        if (atomicAdd(&p.counters->exited, 1) == static_cast<int>(gridDim.x) - 1) {
-            p.counters->next = p.counters->exited = 0;
-            for (int i = 0; i < p.rest; ++i) p.counters->parts[i] = 0;
-        }
+        if (atomicAdd(&p.counters->exited, 1) == static_cast<int>(gridDim.x) - 1) p.counters->next = p.counters->exited = 0;
     }
 }
 
@@ -761,22 +803,66 @@ linear_finish_kernel(const float *__restrict__ partial, int ksplit, int T, int N
     }
 }
 
+template <int NT>
+constexpr size_t stream_smem() {
+    static_assert(sizeof(LinearSmem<NT>) + 1024 <= 227 * 1024, "shared memory budget of one CTA");
+    return sizeof(LinearSmem<NT>) + 1024;
+}
+
+template <int NT, bool XQ>
+cudaError_t configure_stream() {
+    static DeviceConfigured configured{};
+    if (!first_use_on_device(configured)) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(linear_stream_kernel<NT, XQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(stream_smem<NT>()));
+    if (e == cudaSuccess)  // clusters of more than 8
+        e = cudaFuncSetAttribute(linear_stream_kernel<NT, XQ>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) mark_used_on_device(configured);
+    return e;
+}
+
+// Clusters of n CTAs that the device holds at once (one CTA an SM, a cluster
+// within one of the device's groups of SMs: 33 of 4, 22 of 6, 15 of 9, 7 of 16
+// on one B200); asked once for each device.
+int cluster_room(int n) {
+    static std::atomic<int> known[64][MAX_CLUSTER + 1];  // room + 1
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int room = known[dev][n].load(std::memory_order_relaxed);
+    if (room) return room - 1;
+    if (configure_stream<16, false>() != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n);
+    cfg.blockDim = dim3(ls_threads<16, false>());
+    cfg.dynamicSmemBytes = stream_smem<16>();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {static_cast<unsigned>(n), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, linear_stream_kernel<16, false>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        clusters = 0;
+    }
+    known[dev][n].store(clusters + 1, std::memory_order_relaxed);
+    return clusters;
+}
+
 template <int NT, bool XQ>
 cudaError_t launch_stream_t(const LinearStreamArgs &g, cudaStream_t st, int *launches) {
     CUtensorMap mx, mw;
     const int rows = (g.N + 127) / 128, KB = g.K / 128, groups = (g.T + NT - 1) / NT, tiles = rows * groups;
     std::memset(&mx, 0, sizeof mx);
-    if (!XQ && !make_map_2d(&mx, g.a, true, g.K, g.T, NT)) return cudaErrorInvalidValue;
+    // boxes of the tokens there are: rows past the array, which TMA fills with
+    // zeros, cost 0.5 us at one token of 7168 x 7168 (columns past T hold anything)
+    const int box = std::min(g.T, NT);
+    if (!XQ && !make_map_2d(&mx, g.a, true, g.K, g.T, box)) return cudaErrorInvalidValue;
     if (g.w_rowmajor ? !make_map_2d(&mw, g.w, true, g.K, g.N) : !make_map_2d(&mw, g.w, true, 128, rows * KB * 128))
         return cudaErrorInvalidValue;
-    constexpr size_t smem = sizeof(LinearSmem<NT>) + 1024;
-    static_assert(smem <= 227 * 1024, "shared memory budget of one CTA");
-    static DeviceConfigured configured{};
-    if (first_use_on_device(configured)) {
-        const cudaError_t e = cudaFuncSetAttribute(linear_stream_kernel<NT, XQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
+    {
+        const cudaError_t e = configure_stream<NT, XQ>();
         if (e != cudaSuccess) return e;
-        mark_used_on_device(configured);
     }
     LinearParams p{};
     p.x = g.x;
@@ -795,7 +881,9 @@ cudaError_t launch_stream_t(const LinearStreamArgs &g, cudaStream_t st, int *lau
     p.whole = plan.whole;
     p.rest = plan.rest;
     p.parts = plan.parts;
-    p.sum_here = g.T <= kSumHere;
+    p.cluster = plan.cluster;
+    p.share = (static_cast<uint32_t>((std::min(g.T, NT) + 3) / 4) * 128 + plan.parts - 1) / plan.parts;
+    p.per_share = static_cast<uint32_t>(((1ull << 32) + p.share - 1) / p.share);
     p.out_f32 = g.out_f32;
     p.w_rowmajor = g.w_rowmajor;
     p.ue = g.ue8m0;
@@ -803,9 +891,21 @@ cudaError_t launch_stream_t(const LinearStreamArgs &g, cudaStream_t st, int *lau
     mark_launch(st, *launches, "linear_stream");
     const auto kernel = linear_stream_kernel<NT, XQ>;
     constexpr int threads = ls_threads<NT, XQ>();
-    LAUNCH_OR_RETURN(launch_pdl(kernel, dim3(plan.grid), dim3(threads), smem, st, mx, mw, p));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(plan.grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = stream_smem<NT>();
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {static_cast<unsigned>(plan.parts), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = plan.cluster ? 2 : 1;
+    LAUNCH_OR_RETURN(cudaLaunchKernelEx(&cfg, kernel, mx, mw, p));
     ++*launches;
-    if (plan.parts == 1 || p.sum_here) return cudaSuccess;
+    if (plan.parts == 1 || plan.cluster) return cudaSuccess;
     mark_launch(st, *launches, "linear_sum");
     const LinearOut out{g.residual, g.out, g.T, g.N, g.out_f32};
     LAUNCH_OR_RETURN(launch_pdl(linear_sum_kernel<NT>, dim3(plan.rest * NT / 8), dim3(256), 0, st, g.partial, plan.whole,
@@ -817,23 +917,30 @@ cudaError_t launch_stream_t(const LinearStreamArgs &g, cudaStream_t st, int *lau
 }  // namespace
 
 // One CTA a SM.  The rest tiles are cut into the number of parts that ends
-// first, by two measured costs: a CTA alone streams a K block of a tile in 0.15
-// us (0.2 with 32 columns; 0.38 with 64, whose scales every epilogue warp reads
-// from shared memory: with the operands 1300 clk of its bandwidth a stage), and
-// storing and adding parts takes 3 us.  Parts of all tiles together (equal shares of the whole stream, two cut
-// tiles a CTA) took 17.4 us for one token at 1536 x 24576 and 9.6 at 7168 x 2112.
+// first, by measured costs: a CTA alone streams a K block of a tile in 0.15 us
+// (0.2 with 32 columns; 0.38 with 64, whose scales every epilogue warp reads from
+// shared memory: with the operands 1300 clk of its bandwidth a stage); storing
+// and adding parts takes 3 us, and 1.5 in clusters (not of two, which sit on one
+// pair of SMs: 64 tokens, 16384 x 7168 in 112 CTAs 36.7 us so and 32.8 spread
+// out with the second kernel).  Parts of all tiles together
+// (equal shares of the whole stream, two cut tiles a CTA) took 17.4 us for one
+// token at 1536 x 24576 and 9.6 at 7168 x 2112.
 LinearPlan linear_plan(int T, int tiles, int KB) {
     const int most = std::min(num_sms(), kLinearMaxCtas);
     LinearPlan p;
     p.whole = tiles / most * most;
     p.rest = tiles - p.whole;
     p.parts = 1;
+    p.cluster = false;
     const float block = T <= 16 ? 0.15f : (T <= 32 ? 0.2f : 0.38f);
-    float best = block * KB;
+    p.us = block * KB;
     for (int k = 2; p.rest && k <= std::min(most / p.rest, KB); ++k) {
-        const float t = block * ((KB + k - 1) / k) + 3.0f;
-        if (t < best) best = t, p.parts = k;
+        const bool cluster = !p.whole && k > 2 && k <= MAX_CLUSTER && cluster_room(k) >= p.rest;
+        const float t = block * ((KB + k - 1) / k) + (cluster ? 1.5f : 3.0f);
+        if (t < p.us) p.us = t, p.parts = k, p.cluster = cluster;
     }
+    if (!p.rest) p.us = 0.0f;
+    p.us += block * KB * (p.whole / most);
     p.grid = p.whole ? most : p.rest * p.parts;
     return p;
 }
