@@ -504,6 +504,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
         if (lane == 0) {
             const uint32_t w_base = smem_u32(s.w[0][0]), x_base = smem_u32(s.x[0][0]), f_base = smem_u32(&s.full[0]);
             const uint64_t once = l2_evict_first(), keep = l2_evict_normal();  // a weight is read once
+            const int x_bytes = T * 128;  // boxes of the tokens there are (the other columns hold anything)
             int stage = 0;
             uint32_t phase = 0, armed = 0, armed_phase = 0;
             bool ok = true;
@@ -574,7 +575,7 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                     }
                     const bool one = odd && q == last;
                     const uint32_t bar = f_base + stage * 8, w = w_base + stage * 2 * W_BYTES;
-                    mbar_arrive_expect_tx(&s.full[stage], one ? W_BYTES + X_BYTES : 2 * W_BYTES + per * X_BYTES);
+                    mbar_arrive_expect_tx(&s.full[stage], one ? W_BYTES + x_bytes : 2 * W_BYTES + per * x_bytes);
                     tma_load_2d_policy(w, wm, ax, ay, bar, once);
                     if (!one) tma_load_2d_policy(w + W_BYTES, wm, bx, by, bar, once);
                     if (have_x) load_x(stage, xx, it.down && !one);
@@ -1095,8 +1096,8 @@ cudaError_t launch_few(const FewArgs &g, cudaStream_t st, int *launches) {
     if (t13 >= (1LL << 31) || t2 >= (1LL << 31)) return cudaErrorInvalidValue;
     const int per = 128 / es;
     const void *xop = fp8 ? static_cast<const void *>(g.xq) : g.x;
-    if (!make_map_2d(&mx, xop, fp8, s.d_model, s.T, FT) ||
-        !make_map_2d(&mh, g.h, fp8, s.d_expert, g.list_rows * FT, FT) ||
+    if (!make_map_2d(&mx, xop, fp8, s.d_model, s.T, s.T) ||
+        !make_map_2d(&mh, g.h, fp8, s.d_expert, g.list_rows * FT, s.T) ||
         !make_map_2d(&m13, g.w13, fp8, rm ? s.d_model : per, static_cast<int>(t13)) ||
         !make_map_2d(&m2, g.w2, fp8, rm ? s.d_expert : per, static_cast<int>(t2)))
         return cudaErrorInvalidValue;
