@@ -513,7 +513,7 @@ def _arg(t, dtypes, numel, dev, name):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtypes if len(dtypes) > 1 else dtypes[0]}")
-    if t.device != dev:
+    if t.get_device() != dev.index:
         raise ValueError(f"{name}: on {t.device}, the call's other tensors on {dev}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")

@@ -43,8 +43,8 @@
 #include "quant_math.cuh"
 
 #include <algorithm>
-#include <atomic>
 #include <cstring>
+#include <mutex>
 
 namespace moe {
 namespace {
@@ -821,32 +821,36 @@ cudaError_t configure_stream() {
     return e;
 }
 
-// Clusters of n CTAs that the device holds at once (one CTA an SM, a cluster
-// within one of the device's groups of SMs: 33 of 4, 22 of 6, 15 of 9, 7 of 16
-// on one B200); asked once for each device.
-int cluster_room(int n) {
-    static std::atomic<int> known[64][MAX_CLUSTER + 1];  // room + 1
+// [n]: clusters of n CTAs that the current device holds at once (one CTA an SM,
+// a cluster within one of the device's groups of SMs: 33 of 4, 22 of 6, 15 of 9,
+// 7 of 16 on one B200); asked once for each device.
+struct ClusterRoom {
+    int n[MAX_CLUSTER + 1];
+};
+const ClusterRoom &cluster_room() {
+    static const ClusterRoom none{};
+    static ClusterRoom known[64];
+    static std::once_flag asked[64];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    int room = known[dev][n].load(std::memory_order_relaxed);
-    if (room) return room - 1;
-    if (configure_stream<16, false>() != cudaSuccess) return 0;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(n);
-    cfg.blockDim = dim3(ls_threads<16, false>());
-    cfg.dynamicSmemBytes = stream_smem<16>();
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {static_cast<unsigned>(n), 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int clusters = 0;
-    if (cudaOccupancyMaxActiveClusters(&clusters, linear_stream_kernel<16, false>, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        clusters = 0;
-    }
-    known[dev][n].store(clusters + 1, std::memory_order_relaxed);
-    return clusters;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || configure_stream<16, false>() != cudaSuccess) return none;
+    std::call_once(asked[dev], [dev] {
+        for (int n = 2; n <= MAX_CLUSTER; ++n) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(n);
+            cfg.blockDim = dim3(ls_threads<16, false>());
+            cfg.dynamicSmemBytes = stream_smem<16>();
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim = {static_cast<unsigned>(n), 1, 1};
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&known[dev].n[n], linear_stream_kernel<16, false>, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                known[dev].n[n] = 0;
+            }
+        }
+    });
+    return known[dev];
 }
 
 template <int NT, bool XQ>
@@ -934,8 +938,9 @@ LinearPlan linear_plan(int T, int tiles, int KB) {
     p.cluster = false;
     const float block = T <= 16 ? 0.15f : (T <= 32 ? 0.2f : 0.38f);
     p.us = block * KB;
+    const ClusterRoom &room = cluster_room();
     for (int k = 2; p.rest && k <= std::min(most / p.rest, KB); ++k) {
-        const bool cluster = !p.whole && k > 2 && k <= MAX_CLUSTER && cluster_room(k) >= p.rest;
+        const bool cluster = !p.whole && k > 2 && k <= MAX_CLUSTER && room.n[k] >= p.rest;
         const float t = block * ((KB + k - 1) / k) + (cluster ? 1.5f : 3.0f);
         if (t < p.us) p.us = t, p.parts = k, p.cluster = cluster;
     }
