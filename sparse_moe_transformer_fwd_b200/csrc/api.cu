@@ -1196,8 +1196,8 @@ bool linear_quantises(const moe_linear_shape *s) {
 //     where sums are added or stored by a second kernel 5, and their bytes
 //     written and read at 4 TB/s
 //   both at least the weights, at 7 and 5.5 TB/s
-// The tiled GEMM needs enough tiles: 128 tokens, 7168 x 2112 (9 tiles) 23.7 us
-// against 11.4 in the stream kernel; 128 tokens, 16384 x 7168 39.6 against 52.
+// The tiled GEMM needs enough tiles: 128 tokens, 7168 x 2112 (9 tiles) 23.4 us
+// against 10.9 in the stream kernel; 256 tokens, 16384 x 7168 52 against 77.
 struct LinearChoice {
     bool stream;
     int ksplit;

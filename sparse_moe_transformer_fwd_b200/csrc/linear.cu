@@ -16,24 +16,24 @@
 // cut into equal parts of K, as many as pay (linear_plan).  The parts' binary32
 // sums are added in K order, so the result does not depend on timing: where all
 // tiles are cut, in 3 to 16 parts, a tile's CTAs are one cluster that exchanges
-// them through shared memory (1.5 us); else they go to the workspace and a second
-// kernel adds them (3 us; a tile's last CTA alone took 13 with 64 tokens).
+// them through shared memory (1 us); else they go to the workspace and a second
+// kernel adds them (2 us; a tile's last CTA alone took 13 with 64 tokens).
 //   warp 0      TMA producer: a stage is two K blocks (two 16 KB boxes of W, two
 //               boxes of activations)
 //   warp 1      TMEM allocator and MMA issuer: a stage's K blocks go to adjacent
 //               accumulators; a stage is one wait and one commit
 //   warps 2-3   scales of a K block each, copied to a ring in shared memory with
 //               cp.async (rows past T: zeros)
-//   warps 4-7   epilogue: thread = weight row; adds each accumulator, times its
-//               scale product, to the token sums in registers
+//   warps 4-7   epilogue: 32 weight rows a warp; adds each accumulator, times its
+//               scale product, to the sums in registers
 //   warps 8-12  (at most 16 tokens of bf16 input, short shares) quantise the
 //               stage's 1x128 tiles of x straight into the operand's swizzled
 //               rows; every CTA does it for the K blocks it reads, which costs
 //               less than a launch that writes the codes first
-// Measured (one B200, CUDA graph): 1 token, 7168 x 1536 7.6 us, of which start
-// and end take 4.5; 7 tokens, 7168 x 64007 77 us (5.9 TB/s); 64 tokens with a
-// residual, 16384 x 7168 32 us (3.6 TB/s: the reads of scales and operands from
-// shared memory bound 64 columns).
+// Measured (one B200, CUDA graph): 1 token, 7168 x 1536 7.7 us, of which start
+// and end take 4.5; 7 tokens, 7168 x 64007 76 us (6.0 TB/s); 64 tokens with a
+// residual, 16384 x 7168 30 us (3.9 TB/s of weights; half as much again of
+// activations from L2 comes with it).
 // Every wait is bounded; on expiry the block records MOE_ERR_TIMEOUT, drains its
 // loads and MMAs, frees its TMEM and exits; the last CTA out zeroes the item
 // counter.  (A cluster's barrier has no limit of its own: every CTA reaches it,
@@ -63,12 +63,12 @@ struct LinearSmem {
     static_assert(STAGES * 2 * NT <= TMEM_COLS, "accumulators of the ring's stages");
     alignas(1024) uint8_t w[STAGES][2][W_BYTES];
     alignas(1024) uint8_t x[STAGES][2][X_BYTES];
-    // the cluster's sums for this CTA's share of the tile, [part][share][4 tokens]
-    // (64 columns: in the ring, once every CTA is through with its own)
+    // the cluster's sums for this CTA's share of the tile, [part][share] (64
+    // columns: in the ring, once every CTA is through with its own)
     static constexpr bool SUMS_IN_RING = NT == 64;
-    static constexpr int SUMS = NT * 32 + MAX_CLUSTER;
-    alignas(16) float4 sums[SUMS_IN_RING ? 1 : SUMS];
-    static_assert(SUMS * 16 <= static_cast<int>(sizeof(w)), "the sums in the ring");
+    static constexpr int SUMS = NT * 64 + MAX_CLUSTER;
+    alignas(16) float2 sums[SUMS_IN_RING ? 2 : SUMS];
+    static_assert(SUMS * 8 <= static_cast<int>(sizeof(w)), "the sums in the ring");
     struct alignas(16) Scales {
         float x[2][NT];
         float w[2];
@@ -98,7 +98,7 @@ struct LinearParams {
     int rest;     // tiles after them
     int parts;    // parts of K of each of those
     int cluster;  // a tile's parts are one cluster, which adds them (else a kernel after this one)
-    uint32_t share, per_share;  // of the tile's (4 tokens, row) pieces each CTA of the cluster adds; ceil(2^32 / share)
+    uint32_t share, per_share;  // of the tile's (2 tokens, row) pieces each CTA of the cluster adds; ceil(2^32 / share)
     int out_f32;
     int w_rowmajor;
     int ue;       // power-of-two scales (with XQ)
@@ -190,11 +190,41 @@ linear_sum_kernel(const float *__restrict__ partial, int first_tile, int rest, i
 // The cluster's barrier, per thread, and another CTA's copy of a shared address.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t cta, const float4 &v) {
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t cta, const float2 &v) {
     uint32_t remote;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(cta));
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(remote), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-                 : "memory");
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote), "f"(v.x), "f"(v.y) : "memory");
+}
+
+// 8 x GROUPS accumulator columns of 16 rows: value 4 g + 2 i + j of a lane is
+// row lane / 4 + 8 i, column 8 g + 2 (lane % 4) + j.  A lane so holds four rows
+// of a quarter of the tokens, and reads only those tokens' scales: with a row
+// and every token to each lane the reads of 64 tokens' scales took 512 of a
+// stage's 1300 clk of shared memory.
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, float (&v)[32]) {
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+// Four groups, into v[16 HALF] on.
+template <int HALF>
+__device__ __forceinline__ void tmem_ld_rows16_half(uint32_t taddr, float (&v)[32]) {
+    uint32_t *r = reinterpret_cast<uint32_t *>(v) + 16 * HALF;
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
 }
 
 template <int NT, bool XQ>
@@ -241,7 +271,7 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
     tc_fence_after();
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, s.tmem_base, 0);
     volatile int *abort = &s.abort;
-    float4 *sums = S::SUMS_IN_RING ? reinterpret_cast<float4 *>(s.w) : s.sums;
+    float2 *sums = S::SUMS_IN_RING ? reinterpret_cast<float2 *>(s.w) : s.sums;
     // The kernel before this one has finished when this returns; the producer
     // alone may read W ahead of it (early_w).
     if (!(warp == 0 && p.early_w)) pdl_wait();
@@ -531,7 +561,6 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
         }
     } else if (warp >= 4 && warp < 8) {
         const int q = warp & 3;
-        const int r = q * 32 + lane;  // weight row of the tile
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
         int stage = 0, slot = 0;
         uint32_t phase = 0, sphase = 0;
@@ -542,9 +571,11 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
         Taken item;
         Segment g;
         while (next_segment(item, g)) {
-            float2 acc[NT / 2];
+            // [token group][16 rows][8 rows]: tokens 8 group + 2 (lane % 4) and the next
+            float2 acc[NT / 8][2][2];
 #pragma unroll
-            for (int i = 0; i < NT / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
+            for (int i = 0; i < NT / 8; ++i)
+                acc[i][0][0] = acc[i][0][1] = acc[i][1][0] = acc[i][1][1] = make_float2(0.0f, 0.0f);
             for (int i = 0; i < g.nk && ok; i += 2) {
                 const bool both = i + 1 < g.nk;
                 const bool ready = mbar_wait(&s.sfull[slot], sphase, abort, p.status) &&
@@ -556,18 +587,16 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                 tc_fence_after();
                 const auto &sc = s.sc[slot];
                 const uint32_t base = lane_base + 2 * stage * NT;
-                // columns c .. c + 31 of the stage's accumulators (16 tokens: of both)
-                auto add = [&](const float (&v)[32], int c) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const int j = (c + e) / NT, t = (c + e) % NT;
-                        if (j == 0 || both) {
-                            const float4 sx = *reinterpret_cast<const float4 *>(&sc.x[j][t]);
-                            const float2 sw = make_float2(sc.w[j], sc.w[j]);
-                            const float2 s0 = __fmul2_rn(make_float2(sx.x, sx.y), sw), s1 = __fmul2_rn(make_float2(sx.z, sx.w), sw);
-                            acc[t / 2] = __ffma2_rn(make_float2(v[e], v[e + 1]), s0, acc[t / 2]);
-                            acc[t / 2 + 1] = __ffma2_rn(make_float2(v[e + 2], v[e + 3]), s1, acc[t / 2 + 1]);
-                        }
+                // 8 columns from c on of the stage's accumulators, of rows 0-15 and 16-31
+                auto add = [&](int c, const float *lo, const float *hi) {
+                    const int j = c / NT, gr = c % NT / 8;
+                    if (j == 0 || both) {
+                        const float2 sx = *reinterpret_cast<const float2 *>(&sc.x[j][8 * gr + 2 * (lane & 3)]);
+                        const float2 f = __fmul2_rn(sx, make_float2(sc.w[j], sc.w[j]));
+                        acc[gr][0][0] = __ffma2_rn(make_float2(lo[0], lo[1]), f, acc[gr][0][0]);
+                        acc[gr][0][1] = __ffma2_rn(make_float2(lo[2], lo[3]), f, acc[gr][0][1]);
+                        acc[gr][1][0] = __ffma2_rn(make_float2(hi[0], hi[1]), f, acc[gr][1][0]);
+                        acc[gr][1][1] = __ffma2_rn(make_float2(hi[2], hi[3]), f, acc[gr][1][1]);
                     }
                 };
                 auto drained = [&] {
@@ -577,20 +606,22 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                 };
                 if constexpr (NT == 16) {
                     float v[32];
-                    tmem_ld32(base, v);
+                    tmem_ld_rows16_half<0>(base, v);
+                    tmem_ld_rows16_half<1>(base + (16 << 16), v);
                     tmem_wait_ld(v);
                     drained();
-                    add(v, 0);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) add(8 * e, v + 4 * e, v + 16 + 4 * e);
                 } else {
 #pragma unroll
                     for (int c = 0; c < 2 * NT; c += 64) {
                         float v0[32], v1[32];
-                        tmem_ld32(base + c, v0);
-                        tmem_ld32(base + c + 32, v1);
+                        tmem_ld_rows16(base + c, v0);
+                        tmem_ld_rows16(base + c + (16 << 16), v1);
                         tmem_wait_ld(v0, v1);
                         if (c + 64 >= 2 * NT) drained();
-                        add(v0, c);
-                        add(v1, c + 32);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) add(c + 8 * e, v0 + 4 * e, v1 + 4 * e);
                     }
                 }
                 __syncwarp();
@@ -604,22 +635,27 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                     sphase ^= 1;
                 }
             }
-            auto sum = [&](int t) { return t & 1 ? acc[t >> 1].y : acc[t >> 1].x; };
             const int T = p.T - g.t0;  // tokens from the group's first on
+            const int r = q * 32 + (lane >> 2), t2 = 2 * (lane & 3);
             if (g.nk == KB) {
-                const int n = g.n0 + r;
-                if (ok && n < p.N) {
+                if (!ok) continue;
+                constexpr int AHEAD = 2;  // token groups whose residuals are in flight together
 #pragma unroll
-                    for (int t0 = 0; t0 < NT; t0 += 16) {
-                        const size_t at = static_cast<size_t>(g.t0 + t0) * p.N + n;
-                        float res[16];
+                for (int g0 = 0; g0 < NT / 8; g0 += AHEAD) {
+                    if (8 * g0 >= T) break;
+                    float res[AHEAD][8] = {};
+                    auto each = [&](auto &&f) {
 #pragma unroll
-                        for (int t = 0; t < 16; ++t)
-                            res[t] = p.residual && t0 + t < T ? bf16_f(p.residual[at + static_cast<size_t>(t) * p.N]) : 0.0f;
-#pragma unroll
-                        for (int t = 0; t < 16; ++t)
-                            if (t0 + t < T) out.store(at + static_cast<size_t>(t) * p.N, sum(t0 + t), res[t]);
-                    }
+                        for (int e = 0; e < AHEAD * 8; ++e) {
+                            const int gr = g0 + e / 8, t = 8 * gr + t2 + (e & 1), n = g.n0 + r + (e & 6) * 4;
+                            if (t < T && n < p.N) f(e, gr, static_cast<size_t>(g.t0 + t) * p.N + n);
+                        }
+                    };
+                    if (p.residual) each([&](int e, int, size_t at) { res[e / 8][e % 8] = bf16_f(p.residual[at]); });
+                    each([&](int e, int gr, size_t at) {
+                        const float2 v = acc[gr][e >> 2 & 1][e >> 1 & 1];
+                        out.store(at, e & 1 ? v.y : v.x, res[e / 8][e % 8]);
+                    });
                 }
             } else {
                 // One part of a tile: [token][128 rows] to the workspace, or each
@@ -628,19 +664,25 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                     float *mine = p.partial + static_cast<size_t>(g.part) * NT * 128 + r;
                     if (ok) {
 #pragma unroll
-                        for (int t = 0; t < NT; ++t)
-                            if (t < T) mine[t * 128] = sum(t);
+                        for (int e = 0; e < NT; ++e) {
+                            const int t = e / 8 * 8 + t2 + (e & 1);
+                            const float2 v = acc[e / 8][e >> 2 & 1][e >> 1 & 1];
+                            if (t < T) mine[t * 128 + (e & 6) * 4] = e & 1 ? v.y : v.x;
+                        }
                     }
                     continue;
                 }
                 if (S::SUMS_IN_RING) cluster_arrive();
                 cluster_wait();
-                const uint32_t at = smem_u32(sums) + (blockIdx.x % p.parts) * p.share * 16;
+                const uint32_t at = smem_u32(sums) + (blockIdx.x % p.parts) * p.share * 8;
 #pragma unroll
-                for (int t = 0; t < NT; t += 4) {
-                    if (t >= T) break;
-                    const uint32_t piece = t / 4 * 128 + r, owner = __umulhi(piece, p.per_share);
-                    st_cluster(at + (piece - owner * p.share) * 16, owner, make_float4(sum(t), sum(t + 1), sum(t + 2), sum(t + 3)));
+                for (int gr = 0; gr < NT / 8; ++gr) {
+                    if (8 * gr >= T) break;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t piece = ((gr * 4 + q) * 4 + e) * 32 + lane, owner = __umulhi(piece, p.per_share);
+                        st_cluster(at + (piece - owner * p.share) * 8, owner, acc[gr][e >> 1][e & 1]);
+                    }
                 }
                 cluster_arrive();
             }
@@ -659,20 +701,24 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
         const int rank = blockIdx.x % p.parts;
         const LinearOut out{p.residual, p.out, p.T, p.N, p.out_f32};
         for (uint32_t i = threadIdx.x; i < p.share; i += blockDim.x) {
-            const int piece = rank * p.share + i, n = g.n0 + (piece & 127), t = g.t0 + (piece >> 7) * 4;
+            const int piece = rank * p.share + i;  // [token group][warp][8 rows][lane]
+            const int n = g.n0 + (piece >> 5 & 15) * 8 + (piece >> 2 & 7), t = g.t0 + (piece >> 9) * 8 + 2 * (piece & 3);
             if (n >= p.N || t >= min(g.t0 + NT, p.T)) continue;
             const size_t at = static_cast<size_t>(t) * p.N + n;
-            float f[4] = {}, res[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                res[j] = p.residual && t + j < p.T ? bf16_f(p.residual[at + static_cast<size_t>(j) * p.N]) : 0.0f;
-            for (int k = 0; k < p.parts; ++k) {
-                const float4 v = sums[k * p.share + i];
-                f[0] = __fadd_rn(f[0], v.x), f[1] = __fadd_rn(f[1], v.y), f[2] = __fadd_rn(f[2], v.z), f[3] = __fadd_rn(f[3], v.w);
+            const bool two = t + 1 < p.T;
+            float res[2] = {};
+            if (p.residual) {
+                res[0] = bf16_f(p.residual[at]);
+                if (two) res[1] = bf16_f(p.residual[at + p.N]);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (t + j < p.T) out.store(at + static_cast<size_t>(j) * p.N, f[j], res[j]);
+            float2 f = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+            for (int k = 0; k < p.parts; ++k) {
+                const float2 v = sums[k * p.share + i];
+                f.x = __fadd_rn(f.x, v.x), f.y = __fadd_rn(f.y, v.y);
+            }
+            out.store(at, f.x, res[0]);
+            if (two) out.store(at + p.N, f.y, res[1]);
         }
     }
     tc_fence_before();
@@ -886,7 +932,7 @@ cudaError_t launch_stream_t(const LinearStreamArgs &g, cudaStream_t st, int *lau
     p.rest = plan.rest;
     p.parts = plan.parts;
     p.cluster = plan.cluster;
-    p.share = (static_cast<uint32_t>((std::min(g.T, NT) + 3) / 4) * 128 + plan.parts - 1) / plan.parts;
+    p.share = (static_cast<uint32_t>((std::min(g.T, NT) + 7) / 8) * 512 + plan.parts - 1) / plan.parts;
     p.per_share = static_cast<uint32_t>(((1ull << 32) + p.share - 1) / p.share);
     p.out_f32 = g.out_f32;
     p.w_rowmajor = g.w_rowmajor;
@@ -922,13 +968,12 @@ cudaError_t launch_stream_t(const LinearStreamArgs &g, cudaStream_t st, int *lau
 
 // One CTA a SM.  The rest tiles are cut into the number of parts that ends
 // first, by measured costs: a CTA alone streams a K block of a tile in 0.15 us
-// (0.2 with 32 columns; 0.38 with 64, whose scales every epilogue warp reads from
-// shared memory: with the operands 1300 clk of its bandwidth a stage); storing
-// and adding parts takes 3 us, and 1.5 in clusters (not of two, which sit on one
+// (0.2 with 32 columns, 0.34 with 64: 3 and 6 KB more of activations); storing
+// and adding parts takes 2 us, and 1 in clusters (not of two, which sit on one
 // pair of SMs: 64 tokens, 16384 x 7168 in 112 CTAs 36.7 us so and 32.8 spread
-// out with the second kernel).  Parts of all tiles together
-// (equal shares of the whole stream, two cut tiles a CTA) took 17.4 us for one
-// token at 1536 x 24576 and 9.6 at 7168 x 2112.
+// out with the second kernel).  Parts of all tiles together (equal shares of the
+// whole stream, two cut tiles a CTA) took 17.4 us for one token at 1536 x 24576
+// and 9.6 at 7168 x 2112, where this takes 10.5 and 6.8.
 LinearPlan linear_plan(int T, int tiles, int KB) {
     const int most = std::min(num_sms(), kLinearMaxCtas);
     LinearPlan p;
@@ -936,12 +981,12 @@ LinearPlan linear_plan(int T, int tiles, int KB) {
     p.rest = tiles - p.whole;
     p.parts = 1;
     p.cluster = false;
-    const float block = T <= 16 ? 0.15f : (T <= 32 ? 0.2f : 0.38f);
+    const float block = T <= 16 ? 0.15f : (T <= 32 ? 0.2f : 0.34f);
     p.us = block * KB;
     const ClusterRoom &room = cluster_room();
     for (int k = 2; p.rest && k <= std::min(most / p.rest, KB); ++k) {
         const bool cluster = !p.whole && k > 2 && k <= MAX_CLUSTER && room.n[k] >= p.rest;
-        const float t = block * ((KB + k - 1) / k) + (cluster ? 1.5f : 3.0f);
+        const float t = block * ((KB + k - 1) / k) + (cluster ? 1.0f : 2.0f);
         if (t < p.us) p.us = t, p.parts = k, p.cluster = cluster;
     }
     if (!p.rest) p.us = 0.0f;
