@@ -307,15 +307,6 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
             tmem_alloc(&s.tmem_base, TMEM_COLS);
             tmem_relinquish();
         }
-        // The shared expert's weights are needed whatever the routing: into L2
-        // while it is found.
-        if (tid == 96 && p.n_shared) {
-            const size_t es = FP8 ? 1 : 2, b13 = static_cast<size_t>(2) * de * d * es, b2 = static_cast<size_t>(d) * de * es;
-            for (size_t o = static_cast<size_t>(cta) * W_BYTES; o < b13; o += static_cast<size_t>(G) * W_BYTES)
-                l2_prefetch(p.w13 + E * b13 + o, static_cast<uint32_t>(min(b13 - o, static_cast<size_t>(W_BYTES))));
-            for (size_t o = static_cast<size_t>(cta) * W_BYTES; o < b2; o += static_cast<size_t>(G) * W_BYTES)
-                l2_prefetch(p.w2 + E * b2 + o, static_cast<uint32_t>(min(b2 - o, static_cast<size_t>(W_BYTES))));
-        }
         if constexpr (FP8) {
             // half-warps over the (token, 128-column) tiles of all CTAs
             const int half = cta * (MAIN_THREADS / 16) + tid / 16, l16 = tid % 16;
@@ -390,6 +381,15 @@ moe_few_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                 p.rough[static_cast<size_t>(tid >> 1) * E + cta + (e0 + (tid & 1)) * G] = __fdividef(1.0f, 1.0f + __expf(-l));
             }
             if (e0 + 2 < ne) named_bar_sync(3, MAIN_THREADS);
+        }
+        // The shared expert's weights are needed whatever the routing: into L2
+        // while it is found.
+        if (tid == 96 && p.n_shared) {
+            const size_t es = FP8 ? 1 : 2, b13 = static_cast<size_t>(2) * de * d * es, b2 = static_cast<size_t>(d) * de * es;
+            for (size_t o = static_cast<size_t>(cta) * W_BYTES; o < b13; o += static_cast<size_t>(G) * W_BYTES)
+                l2_prefetch(p.w13 + E * b13 + o, static_cast<uint32_t>(min(b13 - o, static_cast<size_t>(W_BYTES))));
+            for (size_t o = static_cast<size_t>(cta) * W_BYTES; o < b2; o += static_cast<size_t>(G) * W_BYTES)
+                l2_prefetch(p.w2 + E * b2 + o, static_cast<uint32_t>(min(b2 - o, static_cast<size_t>(W_BYTES))));
         }
         fence_proxy_async_global();  // the codes of x are read by TMA
         named_bar_sync(3, MAIN_THREADS);
