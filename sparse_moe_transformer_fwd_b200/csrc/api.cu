@@ -1175,10 +1175,6 @@ int check_linear_shape(const moe_linear_shape *s) {
 
 int linear_padded_n(const moe_linear_shape *s) { return (s->N + 255) / 256 * 256; }
 
-// Sums in binary32 and a finishing kernel where the tiled GEMM cannot store
-// the output itself (256 bf16 columns a tile).
-bool linear_direct(const moe_linear_shape *s) { return s->N % 256 == 0 && !s->out_f32; }
-
 // x is quantised in the product's kernel for at most kLinearQuantRows tokens
 // and shares of at most 16 K blocks a CTA: every CTA quantises what it reads,
 // which a long stream waits for (7 tokens, 7168 x 64007: 189 blocks a CTA, 91 us
@@ -1189,39 +1185,46 @@ bool linear_quantises(const moe_linear_shape *s) {
            static_cast<long long>(tiles) * KB <= 16LL * linear_plan(s->T, tiles, KB).grid;
 }
 
-// Which kernel a batch takes, and the K ranges of the tiled GEMM: by the time
-// that each would need, in us, from measured parts.
+// Which kernel a batch takes, and how the tiled GEMM divides its tiles: by the
+// time that each would need, in us, from measured parts.
 //   stream: linear_plan's, and 4.5 to start and end
-//   tiled: 0.58 a K block of a 128-token x 256-column tile; 4 to start and end;
-//     where sums are added or stored by a second kernel 5, and their bytes
-//     written and read at 4 TB/s
+//   tiled: 0.58 a K block of a 128-token x 256-column tile (0.45 by the
+//     block-scaled MMA, which cannot cut K or give binary32 sums); whole rounds of
+//     tiles, then the rest in as many ranges of K as pay; 4 to start and end;
+//     where sums are added by a second kernel 5, and their bytes written and read
+//     at 4 TB/s.  (4096 tokens, 7168 x 4096, 512 tiles: in four rounds 152 us.)
 //   both at least the weights, at 7 and 5.5 TB/s
 // The tiled GEMM needs enough tiles: 128 tokens, 7168 x 2112 (9 tiles) 23.4 us
 // against 10.9 in the stream kernel; 256 tokens, 16384 x 7168 52 against 77.
 struct LinearChoice {
-    bool stream;
-    int ksplit;
+    bool stream, mx;
+    int from, ksplit;  // tiles done whole; ranges of K of the others
 };
 
-int linear_most_splits(const moe_linear_shape *s, int sms) {
-    const int tiles = gemm_output_tiles(s->T, linear_padded_n(s));
-    return std::max(1, std::min({kMaxSplitK, sms / std::max(tiles, 1), s->K / 256}));
-}
+// Sums of every tile in binary32 and a finishing kernel where the GEMM cannot
+// store the output itself (vectors of 8 columns).
+bool linear_sums(const moe_linear_shape *s) { return s->N % 8 != 0; }
+int linear_tiles(const moe_linear_shape *s) { return gemm_output_tiles(s->T, linear_padded_n(s)); }
 
 LinearChoice linear_choice(const moe_linear_shape *s) {
-    LinearChoice c{s->T <= kLinearQuantRows, 1};
+    const int tiles = linear_tiles(s), KB = s->K / 128;
+    LinearChoice c{s->T <= kLinearQuantRows, false, tiles, 1};
     if (c.stream || s->T == 0) return c;
-    const int sms = std::min(num_sms(), kLinearMaxCtas), KB = s->K / 128;
+    const int sms = std::min(num_sms(), kLinearMaxCtas);
     const float bytes = static_cast<float>(s->N) * s->K;
-    const bool direct = linear_direct(s) || s->N % 256 == 0;  // binary32 sums may be the output (no residual)
-    const long long tiles = gemm_output_tiles(s->T, linear_padded_n(s));
-    const float plane = 8.0f * s->T * linear_padded_n(s) / 4e6f;  // binary32 sums written and read
+    const bool sums = linear_sums(s);
+    const float tile_sums = 2.0f * 128 * 256 * 4 / 4e6f;  // binary32, written and read
     float best = 0.0f;
-    for (int k = 1; k <= linear_most_splits(s, sms); ++k) {
-        const long long steps = (tiles * k + sms - 1) / sms * ((KB + k - 1) / k);
-        const float t = 4.0f + std::max(0.58f * steps, bytes / 5.5e6f) + (k > 1 || !direct ? 5.0f + plane * k : 0.0f);
-        if (k == 1 || t < best) best = t, c.ksplit = k;
-    }
+    auto take = [&](float us, bool mx, int from, int ks) {
+        us = 4.0f + std::max(us, bytes / 5.5e6f) + (from < tiles ? 5.0f + tile_sums * (tiles - from) * ks : 0.0f);
+        if (best == 0.0f || us < best) best = us, c.mx = mx, c.from = from, c.ksplit = ks;
+    };
+    const float rounds = static_cast<float>((tiles + sms - 1) / sms);
+    take(0.58f * KB * rounds, false, sums ? 0 : tiles, 1);
+    if (!sums && !s->out_f32 && s->precision == MOE_FP8_UE8M0) take(0.45f * KB * rounds, true, tiles, 1);
+    const int from = sums ? 0 : tiles / sms * sms, rest = tiles - from;
+    for (int ks = 2; rest && rest < sms && ks <= std::min(sms / rest, KB / 4); ++ks)
+        take(0.58f * (KB * (from / sms) + std::min(KB, (KB + ks - 1) / ks + 3)), false, from, ks);
     if (s->T <= kLinearStreamRows) {
         const int columns = s->T <= 32 ? 32 : 64;
         const int rows = (s->N + 127) / 128, all = rows * ((s->T + columns - 1) / columns);
@@ -1250,8 +1253,8 @@ LinearLayout linear_layout(const moe_linear_shape *s) {
     // either kernel's partial sums, for any SM count
     size_t partial = s->T <= kLinearStreamRows ? linear_partial_floats(s->T) : 0;
     if (s->T > kLinearQuantRows) {
-        const int k = linear_most_splits(s, kLinearMaxCtas);
-        if (k > 1 || !linear_direct(s)) partial = std::max(partial, static_cast<size_t>(k) * T * linear_padded_n(s));
+        const size_t tiles = linear_tiles(s), cut = std::min<size_t>(kLinearMaxCtas, tiles * std::max<size_t>(K / 512, 1));
+        partial = std::max(partial, (linear_sums(s) ? std::max(tiles, cut) : cut) * 128 * 256);
     }
     L.partial = take(partial * 4);
     L.total = off;
@@ -1289,10 +1292,7 @@ int linear_product(const moe_linear_shape *s, const uint16_t *x, const void *a, 
         LAUNCH(launch_linear_stream(g, st, n), "linear");
         return MOE_OK;
     }
-    const int ks = choice.ksplit;
-    // binary32 outputs of whole tiles without a residual are the sums themselves
-    const bool in_place = ks == 1 && s->out_f32 && s->N % 256 == 0 && !residual;
-    const bool sums = ks > 1 || !linear_direct(s);
+    const int tiles = linear_tiles(s);
     GemmArgs g{};
     g.fp8 = true;
     g.gate_up = false;
@@ -1308,20 +1308,19 @@ int linear_product(const moe_linear_shape *s, const uint16_t *x, const void *a, 
     g.n_slots = 1;
     g.n_segments = 1;
     g.status = at<int>(ws, L.status);
-    // the block-scaled MMA keeps all of K in one accumulator: no binary32
-    // sums per range, so those take the promotion path (a power-of-two scale
-    // is a binary32 scale)
-    g.ue8m0 = s->precision == MOE_FP8_UE8M0 && !sums;
+    g.ue8m0 = choice.mx;
     g.tile_m = kTileM;
     g.early_b = *n > 0;
-    g.ksplit = ks;
-    g.partial = in_place ? static_cast<float *>(out) : (sums ? partial : nullptr);
-    g.b_rows_valid = g.N_out != s->N ? s->N : 0;
-    g.residual = sums ? nullptr : residual;
+    g.n_valid = s->N;
+    g.out_f32 = s->out_f32 != 0;
+    g.split_from = choice.from;
+    g.ksplit = choice.ksplit;
+    g.partial = choice.from < tiles ? partial : nullptr;
+    g.residual = residual;
     LAUNCH(launch_grouped_gemm(g, st, n), "linear GEMM");
-    if (sums && !in_place)
-        LAUNCH(launch_linear_finish(partial, ks, s->T, s->N, g.N_out, residual, out, s->out_f32, st, n),
-               "linear finish");
+    if (choice.from < tiles)
+        LAUNCH(launch_linear_tiles(partial, choice.from, tiles, choice.ksplit, s->T, s->N, residual, out, s->out_f32, st, n),
+               "linear tiles");
     return MOE_OK;
 }
 

@@ -165,7 +165,12 @@ struct KParams {
     int sc_tma;            // fp32 promotion: the scale groups are loaded by TMA (tmap_sa, tmap_sw)
     int early_b;           // single segment: B may be read ahead of the kernel before this one
     int nb_valid;          // 128-row blocks of B that have scales (a single slot's ragged last tile)
+    // LINEAR: tiles below split_from are done whole and stored to out [rows_total,
+    // n_valid] (out_f32: binary32); of those from it on, each of ksplit items of a
+    // tile stores its sums to partial [tile][item][128][256].
+    int split_from, n_valid, out_f32;
 };
+constexpr int DENSE_FFN = 1, LINEAR = 2;  // kinds of single-segment instances
 
 template <int TM>
 __device__ __forceinline__ void decode_tile(const GemmSmem &s, int n_seg, int tile, int n_tiles_n,
@@ -261,7 +266,7 @@ __device__ __forceinline__ int stored_row_of_lane(int l, int q, int rows_valid) 
 // exponent field 0, matching E8M0 code 0).
 __device__ __forceinline__ uint32_t e8m0(float sc) { return (__float_as_uint(sc) >> 23) & 0xffu; }
 
-template <bool FP8, bool GATE_UP, bool MX, bool M64, bool DENSE>
+template <bool FP8, bool GATE_UP, bool MX, bool M64, int DENSE>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const __grid_constant__ CUtensorMap tmap_b,
@@ -269,9 +274,10 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const __grid_constant__ CUtensorMap tmap_sw, const KParams p) {
     static_assert(FP8 || !MX, "the block-scaled MMA takes e4m3 operands");
     static_assert(!M64 || (FP8 && !MX), "64-row tiles: fp8 with software promotion only");
-    // DENSE: the down GEMM of a dense layer, with split K (software promotion
-    // only) and a residual add (a separate instance, so the expert GEMMs keep
-    // their register budget)
+    // DENSE: the down GEMM of a dense layer (DENSE_FFN), with split K (software
+    // promotion only) and a residual add, or the block-scaled linear (LINEAR), any
+    // number of columns (separate instances, so the expert GEMMs keep their
+    // register budget)
     static_assert(!DENSE || !GATE_UP, "split K and residual: down GEMM only");
     using R = Roles<MX>;
     extern __shared__ uint8_t smem_raw[];
@@ -294,7 +300,23 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     const int n_seg = p.n_segments;
     // work item = (output tile, K range): K blocks [kb0, kb0 + nk)
     const int KS = (DENSE && !MX) ? p.ksplit : 1;  // MX: residual only
+    const int from = DENSE == LINEAR && !MX ? p.split_from : 0;
     auto k_range = [&](int item, int &tile, int &ks, int &kb0, int &nk) {
+        if (DENSE == LINEAR && (MX || item < from)) {
+            tile = item;
+            ks = 0;
+            kb0 = 0;
+            nk = KB;
+            return;
+        }
+        if (DENSE == LINEAR) {  // ranges of whole scale groups (four K blocks)
+            const int j = item - from, t = j / KS;
+            tile = from + t;
+            ks = j - t * KS;
+            kb0 = ks * KB / KS & ~3;
+            nk = (ks + 1 == KS ? KB : (ks + 1) * KB / KS & ~3) - kb0;
+            return;
+        }
         tile = item / KS;
         ks = item - tile * KS;
         kb0 = ks * KB / KS;
@@ -350,7 +372,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     if (warp == 0 && lane == 0) {
         prefetch_tmap(&tmap_a);
         prefetch_tmap(&tmap_b);
-        const int single_items = ((p.rows_total + TM - 1) / TM) * p.n_tiles_n * KS;
+        const int single_items = from + (((p.rows_total + TM - 1) / TM) * p.n_tiles_n - from) * KS;
         if (p.early_b && !p.seg_start && !MX && static_cast<int>(blockIdx.x) < single_items) {
             int tile, ks, kb0, nk;
             k_range(blockIdx.x, tile, ks, kb0, nk);
@@ -389,7 +411,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     tc_fence_after();
     const uint32_t tmem_base = s.tmem_base;
     const int total_tiles = s.tile_start[n_seg] * p.n_tiles_n;
-    const int total_items = total_tiles * KS;
+    const int total_items = from + (total_tiles - from) * KS;
     volatile int *abort = &s.abort;
 
     if (warp < 4) {
@@ -945,8 +967,8 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     }
                 }
             } else {
-                if (DENSE && p.partial) {
-                    // split K (or sums wanted in binary32): store this K range's binary32 partial sums; the
+                if (DENSE == DENSE_FFN && p.partial) {
+                    // split K: store this K range's binary32 partial sums; the
                     // reduce kernel that follows adds the KS ranges in K order
                     ks = item - (item / KS) * KS;  // recomputed: not kept live through the chunk loop
                     if (store_row) {
@@ -962,13 +984,18 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     continue;
                 }
                 if (!warp_active) continue;  // uniform over the warp
-                if (DENSE && p.residual && store_row) {
+                // LINEAR: out has any multiple of 8 columns
+                const int ldo = DENSE == LINEAR ? p.n_valid : p.N_out;
+                auto in_out = [&](int col) { return DENSE != LINEAR || nt * 256 + col < p.n_valid; };
+                const bool part = DENSE == LINEAR && !MX && item >= from;
+                if (DENSE && p.residual && store_row && !part) {
                     // the pre-norm block's residual, added before the one rounding
-                    const uint16_t *rp = p.residual + row * p.N_out + nt * 256;
+                    const uint16_t *rp = p.residual + row * ldo + nt * 256;
+                    const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
                     for (int c = 0; c < 64; c += 8) {
-                        const uint4 a = *reinterpret_cast<const uint4 *>(rp + col_lo + c);
-                        const uint4 b = *reinterpret_cast<const uint4 *>(rp + col_hi + c);
+                        const uint4 a = in_out(col_lo + c) ? *reinterpret_cast<const uint4 *>(rp + col_lo + c) : zero;
+                        const uint4 b = in_out(col_hi + c) ? *reinterpret_cast<const uint4 *>(rp + col_hi + c) : zero;
                         const uint32_t ra[4] = {a.x, a.y, a.z, a.w}, rb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -978,6 +1005,30 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                             acc(64 + c + 2 * i + 1) = __fadd_rn(acc(64 + c + 2 * i + 1), bf16_hi(rb[i]));
                         }
                     }
+                }
+                if (DENSE == LINEAR && (p.out_f32 || part)) {
+                    // binary32 rows: chunks of 4 columns, 32 columns at a time,
+                    // transposed as below (a row to each lane and 16 bytes of it to
+                    // a store, 4096 tokens 2048 x 7168 took 140 us)
+                    float *base = part ? p.partial + static_cast<size_t>(item - from) * (128 * 256)
+                                       : static_cast<float *>(p.out) + static_cast<size_t>(row0) * ldo + nt * 256;
+                    const int ld = part ? 256 : ldo, cols = part ? 256 : p.n_valid - nt * 256, li = lane & 7;
+#pragma unroll
+                    for (int c = 0; c < 128; c += 32) {
+                        uint4 ch[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            ch[j] = make_uint4(__float_as_uint(acc(c + 4 * j)), __float_as_uint(acc(c + 4 * j + 1)),
+                                               __float_as_uint(acc(c + 4 * j + 2)), __float_as_uint(acc(c + 4 * j + 3)));
+                        transpose_chunks<8>(ch, li);
+                        const int col = (c < 64 ? col_lo + c : col_hi + c - 64) + 4 * li;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int o = stored_row_of_lane<M64>((lane & ~7) | j, q, rows_valid);
+                            if (o >= 0 && col < cols) *reinterpret_cast<uint4 *>(base + static_cast<size_t>(o) * ld + col) = ch[j];
+                        }
+                    }
+                    continue;
                 }
                 // Y rows of the tile: one segment, so the base is uniform over
                 // the warp and each lane's row differs by its index
@@ -1009,8 +1060,8 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const int col = (hf ? col_hi : col_lo) + 8 * li;
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        if (yoff[j] >= 0)
-                            *reinterpret_cast<uint4 *>(ybase + (yr0 + yoff[j]) * p.N_out + col) = ch[j];
+                        if (yoff[j] >= 0 && in_out(col))
+                            *reinterpret_cast<uint4 *>(ybase + (yr0 + yoff[j]) * ldo + col) = ch[j];
                 }
             }
         }
@@ -1079,7 +1130,7 @@ bool make_map_scales(CUtensorMap *m, const float *base, int cols, long long rows
                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool FP8, bool GATE_UP, bool MX, bool M64 = false, bool DENSE = false>
+template <bool FP8, bool GATE_UP, bool MX, bool M64 = false, int DENSE = 0>
 cudaError_t launch_t(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &msa,
                      const CUtensorMap &msw, const KParams &kp, int grid, cudaStream_t st) {
     const size_t smem = sizeof(GemmSmem) + 1024;
@@ -1114,10 +1165,10 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launche
     if (!m64 && g.tile_m != 128) return cudaErrorInvalidValue;
     if (!make_map_2d(&ma, g.a, g.fp8, g.K, g.rows_total, m64 ? 64 : 128))
         return cudaErrorInvalidValue;
-    if (g.b_rows_valid && (g.n_slots != 1 || g.gate_up || g.seg_start || !g.partial || g.b_rows_valid > b_rows))
-        return cudaErrorInvalidValue;
-    // rows of B: past them the maps fill with zeros
-    const long long rows = g.b_rows_valid ? g.b_rows_valid : static_cast<long long>(g.n_slots) * b_rows;
+    // rows of B: past them the maps fill with zeros (linear: N_out is padded to whole tiles)
+    const bool linear = g.n_valid > 0;
+    if (linear && (g.n_slots != 1 || g.gate_up || g.seg_start || !g.fp8 || m64 || g.n_valid > b_rows)) return cudaErrorInvalidValue;
+    const long long rows = linear ? g.n_valid : static_cast<long long>(g.n_slots) * b_rows;
     if (g.b_rowmajor) {
         if (rows >= (1LL << 31)) return cudaErrorInvalidValue;
         if (!make_map_2d(&mb, g.b, g.fp8, g.K, static_cast<int>(rows))) return cudaErrorInvalidValue;
@@ -1146,7 +1197,7 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launche
     kp.rows_total = g.rows_total;
     kp.b_rowmajor = g.b_rowmajor ? 1 : 0;
     kp.early_b = g.early_b ? 1 : 0;
-    kp.nb_valid = g.b_rows_valid ? (g.b_rows_valid + 127) / 128 : b_rows / 128;
+    kp.nb_valid = linear ? (g.n_valid + 127) / 128 : b_rows / 128;
     kp.seg_slot = g.seg_slot;
     kp.seg_src = g.seg_src;
     kp.seg_ret = g.seg_ret;
@@ -1159,7 +1210,7 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launche
     std::memset(&msw, 0, sizeof(msw));
     if (g.fp8 && !g.ue8m0) {
         const int kbn = g.K / 128;
-        const int ksp = (g.gate_up || g.ksplit < 1) ? 1 : g.ksplit;
+        const int ksp = (g.gate_up || g.ksplit < 1 || linear) ? 1 : g.ksplit;  // (linear: whole groups)
         bool aligned = true;  // every work item's first K block a multiple of 4 (16-byte x)
         for (int ks = 0; ks < ksp; ++ks) aligned = aligned && (ks * kbn / ksp) % 4 == 0;
         kp.sc_tma = aligned &&
@@ -1175,10 +1226,20 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launche
         return cudaErrorInvalidValue;
     kp.partial = g.partial;
     // with split K the residual is added by the reduce kernel
-    kp.residual = (g.gate_up || g.partial) ? nullptr : g.residual;
+    kp.residual = (g.gate_up || (g.partial && !linear)) ? nullptr : g.residual;
     // upper bound of work items: every segment's tiles, each at most one partial
-    const long long max_mtiles = g.rows_total / g.tile_m + g.n_segments;
-    const long long max_tiles = max_mtiles * kp.n_tiles_n * kp.ksplit;
+    const long long max_mtiles = linear ? (g.rows_total + 127) / 128 : g.rows_total / g.tile_m + g.n_segments;
+    long long max_tiles = max_mtiles * kp.n_tiles_n * kp.ksplit;
+    if (linear) {
+        const long long tiles = max_mtiles * kp.n_tiles_n;
+        if (g.split_from < 0 || g.split_from > tiles || (mx && g.split_from != tiles) || (g.split_from < tiles && !g.partial) ||
+            (g.split_from && g.n_valid % 8) || (kp.ksplit > 1 && g.K / 128 / kp.ksplit < 4))
+            return cudaErrorInvalidValue;
+        kp.split_from = g.split_from;
+        kp.n_valid = g.n_valid;
+        kp.out_f32 = g.out_f32 ? 1 : 0;
+        max_tiles = g.split_from + (tiles - g.split_from) * kp.ksplit;
+    }
     const int grid = static_cast<int>(max_tiles < num_sms() ? max_tiles : num_sms());
     if (grid <= 0) return cudaSuccess;
     cudaError_t e;
@@ -1186,17 +1247,21 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launche
     // the dense layer's down GEMM (split K or a residual) has its own instances
     const bool dense = !g.gate_up && (kp.partial || kp.residual);
     if (mx && kp.partial) return cudaErrorInvalidValue;
-    if (dense && mx)
-        e = launch_t<true, false, true, false, true>(ma, mb, msa, msw, kp, grid, st);
+    if (linear && mx)
+        e = launch_t<true, false, true, false, LINEAR>(ma, mb, msa, msw, kp, grid, st);
+    else if (linear)
+        e = launch_t<true, false, false, false, LINEAR>(ma, mb, msa, msw, kp, grid, st);
+    else if (dense && mx)
+        e = launch_t<true, false, true, false, DENSE_FFN>(ma, mb, msa, msw, kp, grid, st);
     else if (g.fp8 && g.ue8m0)
         e = g.gate_up ? launch_t<true, true, true>(ma, mb, msa, msw, kp, grid, st)
                       : launch_t<true, false, true>(ma, mb, msa, msw, kp, grid, st);
     else if (dense && g.fp8 && m64)
-        e = launch_t<true, false, false, true, true>(ma, mb, msa, msw, kp, grid, st);
+        e = launch_t<true, false, false, true, DENSE_FFN>(ma, mb, msa, msw, kp, grid, st);
     else if (dense && g.fp8)
-        e = launch_t<true, false, false, false, true>(ma, mb, msa, msw, kp, grid, st);
+        e = launch_t<true, false, false, false, DENSE_FFN>(ma, mb, msa, msw, kp, grid, st);
     else if (dense)
-        e = launch_t<false, false, false, false, true>(ma, mb, msa, msw, kp, grid, st);
+        e = launch_t<false, false, false, false, DENSE_FFN>(ma, mb, msa, msw, kp, grid, st);
     else if (g.fp8 && m64)
         e = g.gate_up ? launch_t<true, true, false, true>(ma, mb, msa, msw, kp, grid, st)
                       : launch_t<true, false, false, true>(ma, mb, msa, msw, kp, grid, st);

@@ -141,13 +141,18 @@ struct GemmArgs {
     // sums to partial [ksplit][rows_total][N_out] instead of Y; the caller
     // then runs launch_splitk_reduce.
     int ksplit;
-    float *partial;            // also taken with ksplit 1: binary32 sums instead of Y
+    float *partial;
     // Single segment: an earlier launch of the same call has waited for the
     // stream, so B may be loaded ahead of this launch's own wait.
     bool early_b;
-    // Rows of B that exist, of the N_out read (one slot, no gate/up; 0: all
-    // of them).  Columns past them come out as 0, in partial only.
-    int b_rows_valid;
+    // n_valid > 0: the block-scaled linear (one segment and slot, N_out = n_valid
+    // rounded up to 256).  Output tiles are numbered column by column; those below
+    // split_from are stored to out [rows_total, n_valid] (n_valid a multiple of 8;
+    // out_f32: binary32), residual added; those from it on are cut into ksplit
+    // ranges of K (four K blocks each at least), whose binary32 sums go to partial
+    // [tile][range][128][256] for launch_linear_tiles.
+    int n_valid, split_from;
+    bool out_f32;
     const uint16_t *residual;  // down GEMM without split: bf16 [rows_total, N_out] added before rounding
 };
 // Tensor map of a row-major [rows, K] operand of the tensor cores (e4m3 or
@@ -246,10 +251,11 @@ cudaError_t launch_linear_quant(const uint16_t *x, int rows, int K, bool ue8m0, 
                                 cudaStream_t st, int *launches);
 cudaError_t launch_linear_prenorm_quant(const uint16_t *h, const uint16_t *gamma, int rows, int K, float eps, bool ue8m0,
                                         uint8_t *a, float *a_scales, cudaStream_t st, int *launches);
-// out [T, N] = sum of ksplit planes [T, ldp] in order (+ residual).
-cudaError_t launch_linear_finish(const float *partial, int ksplit, int T, int N, int ldp,
-                                 const uint16_t *residual, void *out, int out_f32, cudaStream_t st,
-                                 int *launches);
+// Output tiles `from` to `tiles` - 1 of a linear: the sums of their ksplit ranges
+// in order (+ residual).
+cudaError_t launch_linear_tiles(const float *partial, int from, int tiles, int ksplit, int T, int N,
+                                const uint16_t *residual, void *out, int out_f32, cudaStream_t st,
+                                int *launches);
 
 int num_sms();
 

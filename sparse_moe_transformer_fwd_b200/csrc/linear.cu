@@ -793,30 +793,35 @@ linear_prenorm_quant_kernel(const uint16_t *__restrict__ h, const uint16_t *__re
         encode(kb, kb < KB ? __ldg(reinterpret_cast<const uint4 *>(gamma + kb * 128 + l16 * 8)) : make_uint4(0, 0, 0, 0));
 }
 
-// out[t, n] = sum of the ksplit binary32 planes [ksplit][T][ldp] in order
-// (+ residual), in bf16 or binary32; one thread per 8 columns, whole 16-byte
-// vectors where N is a multiple of 8.
-__global__ void __launch_bounds__(128)
-linear_finish_kernel(const float *__restrict__ partial, int ksplit, int T, int N, int ldp,
-                     const uint16_t *__restrict__ residual, void *__restrict__ out, int out_f32) {
-    const int t = blockIdx.x;
-    const int n0 = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
+// A tile of the tiled GEMM (tiles numbered column by column): the sums of its
+// ksplit ranges [range][128][256] in order (+ residual); a thread takes 8 columns
+// of a row, whole 16-byte vectors where N is a multiple of 8.
+__global__ void __launch_bounds__(256)
+linear_tiles_kernel(const float *__restrict__ partial, int from, int ksplit, int T, int N,
+                    const uint16_t *__restrict__ residual, void *__restrict__ out, int out_f32) {
+    const int tile = from + blockIdx.x, m_tiles = (T + 127) / 128, nt = tile / m_tiles;
+    const int row = blockIdx.y * 8 + threadIdx.x / 32, c = threadIdx.x % 32 * 8;
+    const int t = (tile - nt * m_tiles) * 128 + row, n0 = nt * 256 + c;
     pdl_wait_and_trigger();
-    if (n0 >= N) return;
-    const size_t plane = static_cast<size_t>(T) * ldp;
-    const float *src = partial + static_cast<size_t>(t) * ldp + n0;
-    float f[8];
-    {
-        const float4 a = __ldcg(reinterpret_cast<const float4 *>(src));
-        const float4 b = __ldcg(reinterpret_cast<const float4 *>(src + 4));
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-    }
-    for (int k = 1; k < ksplit; ++k) {
-        const float4 a = __ldcg(reinterpret_cast<const float4 *>(src + k * plane));
-        const float4 b = __ldcg(reinterpret_cast<const float4 *>(src + k * plane + 4));
-        const float g[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (t >= T || n0 >= N) return;
+    const float4 *src = reinterpret_cast<const float4 *>(partial + ((static_cast<size_t>(blockIdx.x) * ksplit * 128 + row) * 256 + c));
+    constexpr int PLANE = 128 * 256 / 4, AHEAD = 4;
+    float f[8] = {};
+    for (int k0 = 0; k0 < ksplit; k0 += AHEAD) {
+        float4 a[AHEAD], b[AHEAD];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = __fadd_rn(f[i], g[i]);
+        for (int k = 0; k < AHEAD; ++k) {
+            if (k0 + k >= ksplit) break;
+            a[k] = __ldcg(src + static_cast<size_t>(k0 + k) * PLANE);
+            b[k] = __ldcg(src + static_cast<size_t>(k0 + k) * PLANE + 1);
+        }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            if (k0 + k >= ksplit) break;
+            const float g[8] = {a[k].x, a[k].y, a[k].z, a[k].w, b[k].x, b[k].y, b[k].z, b[k].w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = __fadd_rn(f[i], g[i]);
+        }
     }
     const size_t at = static_cast<size_t>(t) * N + n0;
     if (N % 8 == 0) {
@@ -843,7 +848,7 @@ linear_finish_kernel(const float *__restrict__ partial, int ksplit, int T, int N
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         if (n0 + i >= N) break;
-        if (residual) f[i] = __fadd_rn(f[i], __uint_as_float(static_cast<uint32_t>(residual[at + i]) << 16));
+        if (residual) f[i] = __fadd_rn(f[i], bf16_f(residual[at + i]));
         if (out_f32) static_cast<float *>(out)[at + i] = f[i];
         else static_cast<__nv_bfloat16 *>(out)[at + i] = __float2bfloat16_rn(f[i]);
     }
@@ -1025,13 +1030,12 @@ cudaError_t launch_linear_prenorm_quant(const uint16_t *h, const uint16_t *gamma
     return cudaGetLastError();
 }
 
-cudaError_t launch_linear_finish(const float *partial, int ksplit, int T, int N, int ldp,
-                                 const uint16_t *residual, void *out, int out_f32, cudaStream_t st,
-                                 int *launches) {
-    if (ksplit < 1 || ldp % 8 || ldp < N) return cudaErrorInvalidValue;
-    mark_launch(st, *launches, "linear_finish");
-    const dim3 grid(T, (N + 1023) / 1024);
-    LAUNCH_OR_RETURN(launch_pdl(linear_finish_kernel, grid, dim3(128), 0, st, partial, ksplit, T, N, ldp,
+cudaError_t launch_linear_tiles(const float *partial, int from, int tiles, int ksplit, int T, int N,
+                                const uint16_t *residual, void *out, int out_f32, cudaStream_t st,
+                                int *launches) {
+    if (ksplit < 1 || from >= tiles) return cudaErrorInvalidValue;
+    mark_launch(st, *launches, "linear_tiles");
+    LAUNCH_OR_RETURN(launch_pdl(linear_tiles_kernel, dim3(tiles - from, 16), dim3(256), 0, st, partial, from, ksplit, T, N,
                                 residual, out, out_f32));
     ++*launches;
     return cudaGetLastError();
