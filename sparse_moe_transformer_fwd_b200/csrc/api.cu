@@ -1188,11 +1188,12 @@ bool linear_quantises(const moe_linear_shape *s) {
 // Which kernel a batch takes, and how the tiled GEMM divides its tiles: by the
 // time that each would need, in us, from measured parts.
 //   stream: linear_plan's, and 4.5 to start and end
-//   tiled: 0.58 a K block of a 128-token x 256-column tile (0.45 by the
-//     block-scaled MMA, which cannot cut K or give binary32 sums); whole rounds of
-//     tiles, then the rest in as many ranges of K as pay; 4 to start and end;
-//     where sums are added by a second kernel 5, and their bytes written and read
-//     at 4 TB/s.  (4096 tokens, 7168 x 4096, 512 tiles: in four rounds 152 us.)
+//   tiled: 0.54 a K block of a 128-token x 256-column tile and 2.3 a tile (0.48 and
+//     3 by the block-scaled MMA, which cannot cut K and sums all of K less exactly
+//     than binary32 outputs want); whole rounds of tiles, then the rest in as many
+//     ranges of K as pay, whose sums a second kernel adds: 3, and their bytes from
+//     L2 and back at 8 TB/s; 4 to start and end.  (4096 tokens, 7168 x 4096, 512
+//     tiles: in four rounds 132 us, with the last one cut in two 126.)
 //   both at least the weights, at 7 and 5.5 TB/s
 // The tiled GEMM needs enough tiles: 128 tokens, 7168 x 2112 (9 tiles) 23.4 us
 // against 10.9 in the stream kernel; 256 tokens, 16384 x 7168 52 against 77.
@@ -1201,9 +1202,6 @@ struct LinearChoice {
     int from, ksplit;  // tiles done whole; ranges of K of the others
 };
 
-// Sums of every tile in binary32 and a finishing kernel where the GEMM cannot
-// store the output itself (vectors of 8 columns).
-bool linear_sums(const moe_linear_shape *s) { return s->N % 8 != 0; }
 int linear_tiles(const moe_linear_shape *s) { return gemm_output_tiles(s->T, linear_padded_n(s)); }
 
 LinearChoice linear_choice(const moe_linear_shape *s) {
@@ -1211,20 +1209,19 @@ LinearChoice linear_choice(const moe_linear_shape *s) {
     LinearChoice c{s->T <= kLinearQuantRows, false, tiles, 1};
     if (c.stream || s->T == 0) return c;
     const int sms = std::min(num_sms(), kLinearMaxCtas);
-    const float bytes = static_cast<float>(s->N) * s->K;
-    const bool sums = linear_sums(s);
-    const float tile_sums = 2.0f * 128 * 256 * 4 / 4e6f;  // binary32, written and read
-    float best = 0.0f;
-    auto take = [&](float us, bool mx, int from, int ks) {
-        us = 4.0f + std::max(us, bytes / 5.5e6f) + (from < tiles ? 5.0f + tile_sums * (tiles - from) * ks : 0.0f);
-        if (best == 0.0f || us < best) best = us, c.mx = mx, c.from = from, c.ksplit = ks;
-    };
+    const float bytes = static_cast<float>(s->N) * s->K, stream_w = bytes / 5.5e6f;
     const float rounds = static_cast<float>((tiles + sms - 1) / sms);
-    take(0.58f * KB * rounds, false, sums ? 0 : tiles, 1);
-    if (!sums && !s->out_f32 && s->precision == MOE_FP8_UE8M0) take(0.45f * KB * rounds, true, tiles, 1);
-    const int from = sums ? 0 : tiles / sms * sms, rest = tiles - from;
-    for (int ks = 2; rest && rest < sms && ks <= std::min(sms / rest, KB / 4); ++ks)
-        take(0.58f * (KB * (from / sms) + std::min(KB, (KB + ks - 1) / ks + 3)), false, from, ks);
+    float best = 4.0f + std::max(stream_w, rounds * (0.54f * KB + 2.3f));
+    auto take = [&](float us, bool mx, int from, int ks) {
+        if (us < best) best = us, c.mx = mx, c.from = from, c.ksplit = ks;
+    };
+    if (s->precision == MOE_FP8_UE8M0 && !s->out_f32)
+        take(4.0f + std::max(stream_w, rounds * (0.48f * KB + 3.0f)), true, tiles, 1);
+    const int whole = tiles / sms, from = whole * sms, rest = tiles - from;
+    for (int ks = 2; rest && ks <= std::min(sms / rest, KB / 4); ++ks) {
+        const float us = whole * (0.54f * KB + 2.3f) + 0.54f * std::min(KB, (KB + ks - 1) / ks + 3) + 2.3f;
+        take(7.0f + std::max(stream_w, us) + 2.0f * 128 * 256 * 4 / 8e6f * rest * ks, false, from, ks);
+    }
     if (s->T <= kLinearStreamRows) {
         const int columns = s->T <= 32 ? 32 : 64;
         const int rows = (s->N + 127) / 128, all = rows * ((s->T + columns - 1) / columns);
@@ -1253,8 +1250,8 @@ LinearLayout linear_layout(const moe_linear_shape *s) {
     // either kernel's partial sums, for any SM count
     size_t partial = s->T <= kLinearStreamRows ? linear_partial_floats(s->T) : 0;
     if (s->T > kLinearQuantRows) {
-        const size_t tiles = linear_tiles(s), cut = std::min<size_t>(kLinearMaxCtas, tiles * std::max<size_t>(K / 512, 1));
-        partial = std::max(partial, (linear_sums(s) ? std::max(tiles, cut) : cut) * 128 * 256);
+        const size_t cut = std::min<size_t>(kLinearMaxCtas, linear_tiles(s) * (K / 512));  // ranges of the cut tiles
+        partial = std::max(partial, cut * 128 * 256);
     }
     L.partial = take(partial * 4);
     L.total = off;

@@ -170,7 +170,7 @@ struct KParams {
     // tile stores its sums to partial [tile][item][128][256].
     int split_from, n_valid, out_f32;
 };
-constexpr int DENSE_FFN = 1, LINEAR = 2;  // kinds of single-segment instances
+constexpr int DENSE_FFN = 1, LINEAR = 2, LINEAR_RAGGED = 3;  // kinds of single-segment instances
 
 template <int TM>
 __device__ __forceinline__ void decode_tile(const GemmSmem &s, int n_seg, int tile, int n_tiles_n,
@@ -275,9 +275,11 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     static_assert(FP8 || !MX, "the block-scaled MMA takes e4m3 operands");
     static_assert(!M64 || (FP8 && !MX), "64-row tiles: fp8 with software promotion only");
     // DENSE: the down GEMM of a dense layer (DENSE_FFN), with split K (software
-    // promotion only) and a residual add, or the block-scaled linear (LINEAR), any
-    // number of columns (separate instances, so the expert GEMMs keep their
-    // register budget)
+    // promotion only) and a residual add, or the block-scaled linear (LINEAR:
+    // columns a multiple of 8, LINEAR_RAGGED: any number); separate instances, so
+    // the expert GEMMs keep their register budget (as LINEAR keeps its own: with
+    // the ragged stores in it 4096 tokens of 7168 x 4096 take 152 us, not 145)
+    constexpr bool LIN = DENSE >= LINEAR;
     static_assert(!DENSE || !GATE_UP, "split K and residual: down GEMM only");
     using R = Roles<MX>;
     extern __shared__ uint8_t smem_raw[];
@@ -300,16 +302,16 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     const int n_seg = p.n_segments;
     // work item = (output tile, K range): K blocks [kb0, kb0 + nk)
     const int KS = (DENSE && !MX) ? p.ksplit : 1;  // MX: residual only
-    const int from = DENSE == LINEAR && !MX ? p.split_from : 0;
+    const int from = LIN && !MX ? p.split_from : 0;
     auto k_range = [&](int item, int &tile, int &ks, int &kb0, int &nk) {
-        if (DENSE == LINEAR && (MX || item < from)) {
+        if (LIN && (MX || item < from)) {
             tile = item;
             ks = 0;
             kb0 = 0;
             nk = KB;
             return;
         }
-        if (DENSE == LINEAR) {  // ranges of whole scale groups (four K blocks)
+        if (LIN) {  // ranges of whole scale groups (four K blocks)
             const int j = item - from, t = j / KS;
             tile = from + t;
             ks = j - t * KS;
@@ -984,11 +986,13 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     continue;
                 }
                 if (!warp_active) continue;  // uniform over the warp
-                // LINEAR: out has any multiple of 8 columns
-                const int ldo = DENSE == LINEAR ? p.n_valid : p.N_out;
-                auto in_out = [&](int col) { return DENSE != LINEAR || nt * 256 + col < p.n_valid; };
-                const bool part = DENSE == LINEAR && !MX && item >= from;
-                if (DENSE && p.residual && store_row && !part) {
+                // LINEAR: out has any number of columns; `ragged` rows are not whole
+                // 16-byte vectors
+                const int ldo = LIN ? p.n_valid : p.N_out;
+                auto in_out = [&](int col) { return !LIN || nt * 256 + col < p.n_valid; };
+                const bool part = LIN && !MX && item >= from;
+                constexpr bool ragged = DENSE == LINEAR_RAGGED;
+                if (DENSE && p.residual && store_row && !part && !ragged) {
                     // the pre-norm block's residual, added before the one rounding
                     const uint16_t *rp = p.residual + row * ldo + nt * 256;
                     const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -1006,10 +1010,12 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                         }
                     }
                 }
-                if (DENSE == LINEAR && (p.out_f32 || part)) {
-                    // binary32 rows: chunks of 4 columns, 32 columns at a time,
-                    // transposed as below (a row to each lane and 16 bytes of it to
-                    // a store, 4096 tokens 2048 x 7168 took 140 us)
+                if (LIN && (p.out_f32 || part || ragged)) {
+                    // binary32 or ragged rows: chunks of 4 columns, 32 columns at a
+                    // time, transposed as below (a row to each lane and 16 bytes of
+                    // it to a store, 4096 tokens 2048 x 7168 took 140 us, now 91;
+                    // odd widths by a second kernel from binary32 sums, 4096 x 7001
+                    // took 251)
                     float *base = part ? p.partial + static_cast<size_t>(item - from) * (128 * 256)
                                        : static_cast<float *>(p.out) + static_cast<size_t>(row0) * ldo + nt * 256;
                     const int ld = part ? 256 : ldo, cols = part ? 256 : p.n_valid - nt * 256, li = lane & 7;
@@ -1025,7 +1031,40 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const int o = stored_row_of_lane<M64>((lane & ~7) | j, q, rows_valid);
-                            if (o >= 0 && col < cols) *reinterpret_cast<uint4 *>(base + static_cast<size_t>(o) * ld + col) = ch[j];
+                            if (o < 0 || col >= cols) continue;
+                            if (part || !ragged) {
+                                *reinterpret_cast<uint4 *>(base + static_cast<size_t>(o) * ld + col) = ch[j];
+                                continue;
+                            }
+                            const size_t at = static_cast<size_t>(row0 + o) * ldo + nt * 256 + col;
+                            float f[4] = {__uint_as_float(ch[j].x), __uint_as_float(ch[j].y), __uint_as_float(ch[j].z),
+                                          __uint_as_float(ch[j].w)};
+                            if (p.residual) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (col + i < cols) f[i] = __fadd_rn(f[i], __uint_as_float(static_cast<uint32_t>(p.residual[at + i]) << 16));
+                            }
+                            if (p.out_f32) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (col + i < cols) static_cast<float *>(p.out)[at + i] = f[i];
+                                continue;
+                            }
+                            uint16_t *op = static_cast<uint16_t *>(p.out) + at;
+                            const uint32_t lo = pack_bf16x2(f[0], f[1]), hi = pack_bf16x2(f[2], f[3]);
+                            if (col + 4 <= cols && at % 2 == 0) {
+                                reinterpret_cast<uint32_t *>(op)[0] = lo;
+                                reinterpret_cast<uint32_t *>(op)[1] = hi;
+                            } else {
+                                op[0] = static_cast<uint16_t>(lo);
+                                if (col + 4 <= cols) {
+                                    *reinterpret_cast<uint32_t *>(op + 1) = lo >> 16 | hi << 16;
+                                } else {
+                                    if (col + 1 < cols) op[1] = static_cast<uint16_t>(lo >> 16);
+                                    if (col + 2 < cols) op[2] = static_cast<uint16_t>(hi);
+                                }
+                                if (col + 3 < cols) op[3] = static_cast<uint16_t>(hi >> 16);
+                            }
                         }
                     }
                     continue;
@@ -1233,7 +1272,7 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launche
     if (linear) {
         const long long tiles = max_mtiles * kp.n_tiles_n;
         if (g.split_from < 0 || g.split_from > tiles || (mx && g.split_from != tiles) || (g.split_from < tiles && !g.partial) ||
-            (g.split_from && g.n_valid % 8) || (kp.ksplit > 1 && g.K / 128 / kp.ksplit < 4))
+            (kp.ksplit > 1 && g.K / 128 / kp.ksplit < 4))
             return cudaErrorInvalidValue;
         kp.split_from = g.split_from;
         kp.n_valid = g.n_valid;
@@ -1247,10 +1286,12 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launche
     // the dense layer's down GEMM (split K or a residual) has its own instances
     const bool dense = !g.gate_up && (kp.partial || kp.residual);
     if (mx && kp.partial) return cudaErrorInvalidValue;
-    if (linear && mx)
-        e = launch_t<true, false, true, false, LINEAR>(ma, mb, msa, msw, kp, grid, st);
+    if (linear && g.n_valid % 8)
+        e = mx ? launch_t<true, false, true, false, LINEAR_RAGGED>(ma, mb, msa, msw, kp, grid, st)
+               : launch_t<true, false, false, false, LINEAR_RAGGED>(ma, mb, msa, msw, kp, grid, st);
     else if (linear)
-        e = launch_t<true, false, false, false, LINEAR>(ma, mb, msa, msw, kp, grid, st);
+        e = mx ? launch_t<true, false, true, false, LINEAR>(ma, mb, msa, msw, kp, grid, st)
+               : launch_t<true, false, false, false, LINEAR>(ma, mb, msa, msw, kp, grid, st);
     else if (dense && mx)
         e = launch_t<true, false, true, false, DENSE_FFN>(ma, mb, msa, msw, kp, grid, st);
     else if (g.fp8 && g.ue8m0)

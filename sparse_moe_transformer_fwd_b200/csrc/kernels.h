@@ -147,9 +147,9 @@ struct GemmArgs {
     bool early_b;
     // n_valid > 0: the block-scaled linear (one segment and slot, N_out = n_valid
     // rounded up to 256).  Output tiles are numbered column by column; those below
-    // split_from are stored to out [rows_total, n_valid] (n_valid a multiple of 8;
-    // out_f32: binary32), residual added; those from it on are cut into ksplit
-    // ranges of K (four K blocks each at least), whose binary32 sums go to partial
+    // split_from are stored to out [rows_total, n_valid] (out_f32: binary32),
+    // residual added; those from it on are cut into ksplit ranges of K (four K
+    // blocks each at least), whose binary32 sums go to partial
     // [tile][range][128][256] for launch_linear_tiles.
     int n_valid, split_from;
     bool out_f32;
