@@ -565,7 +565,6 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
         int stage = 0, slot = 0;
         uint32_t phase = 0, sphase = 0;
         bool ok = true;
-        const LinearOut out{p.residual, p.out, p.T, p.N, p.out_f32};
         if (lane < STAGES) mbar_arrive(&s.full[lane]);  // the accumulators are free
         __syncwarp();
         Taken item;
@@ -637,26 +636,45 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
             }
             const int T = p.T - g.t0;  // tokens from the group's first on
             const int r = q * 32 + (lane >> 2), t2 = 2 * (lane & 3);
-            if (g.nk == KB) {
+            if (__builtin_expect(g.nk == KB, 0)) {
                 if (!ok) continue;
-                constexpr int AHEAD = 2;  // token groups whose residuals are in flight together
+                // (addresses advance by constants: worked out for each of 64 values
+                // they took 2.7 us a tile)
+                const size_t first = static_cast<size_t>(g.t0 + t2) * p.N + g.n0 + r;
+                const int rows = p.N - g.n0 - r;  // e (8 rows on) is a row if 8 e < rows
+                auto store = [&](auto *dst, auto &&convert) {
+                    constexpr int AHEAD = 2;  // token groups whose residuals are in flight together
+                    const size_t group = static_cast<size_t>(8) * p.N;
 #pragma unroll
-                for (int g0 = 0; g0 < NT / 8; g0 += AHEAD) {
-                    if (8 * g0 >= T) break;
-                    float res[AHEAD][8] = {};
-                    auto each = [&](auto &&f) {
+                    for (int g0 = 0; g0 < NT / 8; g0 += AHEAD) {
+                        if (8 * g0 >= T) break;
+                        float res[AHEAD][2][4] = {};
+                        if (p.residual) {
 #pragma unroll
-                        for (int e = 0; e < AHEAD * 8; ++e) {
-                            const int gr = g0 + e / 8, t = 8 * gr + t2 + (e & 1), n = g.n0 + r + (e & 6) * 4;
-                            if (t < T && n < p.N) f(e, gr, static_cast<size_t>(g.t0 + t) * p.N + n);
+                            for (int i = 0; i < 2 * AHEAD; ++i) {
+                                const uint16_t *src = p.residual + first + (g0 + i / 2) * group + (i & 1) * p.N;
+                                if (8 * (g0 + i / 2) + t2 + (i & 1) < T)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        if (8 * e < rows) res[i / 2][i & 1][e] = bf16_f(src[8 * e]);
+                            }
                         }
-                    };
-                    if (p.residual) each([&](int e, int, size_t at) { res[e / 8][e % 8] = bf16_f(p.residual[at]); });
-                    each([&](int e, int gr, size_t at) {
-                        const float2 v = acc[gr][e >> 2 & 1][e >> 1 & 1];
-                        out.store(at, e & 1 ? v.y : v.x, res[e / 8][e % 8]);
-                    });
-                }
+#pragma unroll
+                        for (int i = 0; i < 2 * AHEAD; ++i) {
+                            auto *to = dst + first + (g0 + i / 2) * group + (i & 1) * p.N;
+                            if (8 * (g0 + i / 2) + t2 + (i & 1) < T)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float2 a = acc[g0 + i / 2][e >> 1][e & 1];
+                                    float v = i & 1 ? a.y : a.x;
+                                    if (p.residual) v = __fadd_rn(v, res[i / 2][i & 1][e]);
+                                    if (8 * e < rows) to[8 * e] = convert(v);
+                                }
+                        }
+                    }
+                };
+                if (p.out_f32) store(static_cast<float *>(p.out), [](float v) { return v; });
+                else store(static_cast<__nv_bfloat16 *>(p.out), [](float v) { return __float2bfloat16_rn(v); });
             } else {
                 // One part of a tile: [token][128 rows] to the workspace, or each
                 // piece to the CTA of the cluster that adds it.
@@ -973,8 +991,8 @@ cudaError_t launch_stream_t(const LinearStreamArgs &g, cudaStream_t st, int *lau
 
 // One CTA a SM.  The rest tiles are cut into the number of parts that ends
 // first, by measured costs: a CTA alone streams a K block of a tile in 0.15 us
-// (0.2 with 32 columns, 0.34 with 64: 3 and 6 KB more of activations); storing
-// and adding parts takes 2 us, and 1 in clusters (not of two, which sit on one
+// (0.2 with 32 columns, 0.34 with 64: 3 and 6 KB more of activations) and stores
+// a whole one in 0.2 (0.3, 1); storing and adding parts takes 2 us, and 1 in clusters (not of two, which sit on one
 // pair of SMs: 64 tokens, 16384 x 7168 in 112 CTAs 36.7 us so and 32.8 spread
 // out with the second kernel).  Parts of all tiles together (equal shares of the
 // whole stream, two cut tiles a CTA) took 17.4 us for one token at 1536 x 24576
@@ -987,7 +1005,8 @@ LinearPlan linear_plan(int T, int tiles, int KB) {
     p.parts = 1;
     p.cluster = false;
     const float block = T <= 16 ? 0.15f : (T <= 32 ? 0.2f : 0.34f);
-    p.us = block * KB;
+    const float store = T <= 16 ? 0.2f : (T <= 32 ? 0.3f : 1.0f);
+    p.us = block * KB + store;
     const ClusterRoom &room = cluster_room();
     for (int k = 2; p.rest && k <= std::min(most / p.rest, KB); ++k) {
         const bool cluster = !p.whole && k > 2 && k <= MAX_CLUSTER && room.n[k] >= p.rest;
@@ -995,7 +1014,7 @@ LinearPlan linear_plan(int T, int tiles, int KB) {
         if (t < p.us) p.us = t, p.parts = k, p.cluster = cluster;
     }
     if (!p.rest) p.us = 0.0f;
-    p.us += block * KB * (p.whole / most);
+    p.us += (block * KB + store) * (p.whole / most);
     p.grid = p.whole ? most : p.rest * p.parts;
     return p;
 }
