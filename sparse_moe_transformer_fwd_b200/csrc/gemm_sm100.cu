@@ -54,6 +54,7 @@
 #include "common.cuh"
 #include "kernels.h"
 
+#include <algorithm>
 #include <cstddef>
 #include <cstdio>
 #include <cstring>
@@ -169,6 +170,7 @@ struct KParams {
     // n_valid] (out_f32: binary32); of those from it on, each of ksplit items of a
     // tile stores its sums to partial [tile][item][128][256].
     int split_from, n_valid, out_f32;
+    int a_bytes;  // of a K block's A box: of the rows there are, where they are fewer than a tile
 };
 constexpr int DENSE_FFN = 1, LINEAR = 2, LINEAR_RAGGED = 3;  // kinds of single-segment instances
 
@@ -382,7 +384,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
             b_blocks(0, tile / ((p.rows_total + TM - 1) / TM), t_lo, t_hi);  // column-tile major
             pre = min(STAGES, nk);
             for (int st = 0; st < pre; ++st) {
-                mbar_arrive_expect_tx(&s.full[st], TM * 128 + B_BYTES);
+                mbar_arrive_expect_tx(&s.full[st], (LIN ? p.a_bytes : TM * 128) + B_BYTES);
                 load_b(s.b[st], t_lo, kb0 + st, &s.full[st]);
                 load_b(s.b[st] + B_BYTES / 2, t_hi, kb0 + st, &s.full[st]);
             }
@@ -447,7 +449,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     } else {
                         const bool inject = p.inject_fault && blockIdx.x == 0 && armed == 0;
                         mbar_arrive_expect_tx(&s.full[stage],
-                                              TM * 128 + B_BYTES + (inject ? 16 : 0));
+                                              (LIN ? p.a_bytes : TM * 128) + B_BYTES + (inject ? 16 : 0));
                         tma_load_2d(s.a[stage], &tmap_a, kc, row0, &s.full[stage]);
                         load_b(s.b[stage], t_lo, kb, &s.full[stage]);
                         load_b(s.b[stage] + B_BYTES / 2, t_hi, kb, &s.full[stage]);
@@ -1202,10 +1204,11 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launche
     const bool m64 = g.tile_m == 64;
     if (m64 && (!g.fp8 || g.ue8m0)) return cudaErrorInvalidValue;
     if (!m64 && g.tile_m != 128) return cudaErrorInvalidValue;
-    if (!make_map_2d(&ma, g.a, g.fp8, g.K, g.rows_total, m64 ? 64 : 128))
-        return cudaErrorInvalidValue;
-    // rows of B: past them the maps fill with zeros (linear: N_out is padded to whole tiles)
     const bool linear = g.n_valid > 0;
+    // (linear: rows past the array, which TMA fills with zeros, cost time)
+    const int a_rows = m64 ? 64 : (linear ? std::min(g.rows_total, 128) : 128);
+    if (!make_map_2d(&ma, g.a, g.fp8, g.K, g.rows_total, a_rows)) return cudaErrorInvalidValue;
+    // rows of B: past them the maps fill with zeros (linear: N_out is padded to whole tiles)
     if (linear && (g.n_slots != 1 || g.gate_up || g.seg_start || !g.fp8 || m64 || g.n_valid > b_rows)) return cudaErrorInvalidValue;
     const long long rows = linear ? g.n_valid : static_cast<long long>(g.n_slots) * b_rows;
     if (g.b_rowmajor) {
@@ -1276,6 +1279,7 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launche
             return cudaErrorInvalidValue;
         kp.split_from = g.split_from;
         kp.n_valid = g.n_valid;
+        kp.a_bytes = a_rows * 128;
         kp.out_f32 = g.out_f32 ? 1 : 0;
         max_tiles = g.split_from + (tiles - g.split_from) * kp.ksplit;
     }
