@@ -38,10 +38,9 @@
 //   warps 8-11  exact routing: 8-10 copy the operands, 11 runs the chains; then
 //               warp 9 watches for complete experts' H
 // Measured (one B200, 7168 / 2048, 256 experts of which 8 and a shared one, CUDA
-// graph): e4m3, 1 token 73 us (6.0 TB/s of weights), 3 tokens 169 us, 16 tokens
-// 610 us (7.4 TB/s); bf16, 2048 / 1024, 5 tokens 69 us; one token of 1024 / 512
-// with 16 experts 16.6 us, where the chain of steps bounds it: start and x 4 us,
-// routing 5, two products and their hand-over 6.
+// graph): e4m3, 1 token 71 us (HBM from 11 us on), 3 tokens 168 us, 16 tokens 605
+// us (7.5 TB/s); bf16, 2048 / 1408, 64 experts of which 6, 5 tokens 67 to 74 us; two
+// tokens of bf16 512 / 256, 16 experts, 16.7 us, where the chain of steps bounds it.
 // The kernel is launched cooperatively (all CTAs resident), since CTAs wait for
 // one another.  Every wait is bounded: on expiry the CTA records
 // MOE_ERR_TIMEOUT, sets an abort word that ends the others' waits, drains what

@@ -30,7 +30,7 @@
 //               stage's 1x128 tiles of x straight into the operand's swizzled
 //               rows; every CTA does it for the K blocks it reads, which costs
 //               less than a launch that writes the codes first
-// Measured (one B200, CUDA graph): 1 token, 7168 x 1536 7.7 us, of which start
+// Measured (one B200, CUDA graph): 1 token, 7168 x 2112 7.7 us, of which start
 // and end take 4.5; 7 tokens, 7168 x 64007 76 us (6.0 TB/s); 64 tokens with a
 // residual, 16384 x 7168 30 us (3.9 TB/s of weights; half as much again of
 // activations from L2 comes with it).
