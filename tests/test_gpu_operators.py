@@ -2,6 +2,10 @@
 borders between the kernels and their column groups, outputs and weights beyond
 2^31 elements, padded outputs, overlapping calls, shared workspaces, a wait that
 runs out.  Tolerances are those of the operators' own tests."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -33,6 +37,25 @@ def test_borders_with_residual(T, K, N, out_dtype):
     _check(lin(xd), a, w)
     for _ in range(3):  # counters are back at zero
         assert torch.equal(lin(xd, residual=res), out)
+    assert lin.check_status(T) == 0
+
+
+# the tiled GEMM: padded and odd widths, one round of tiles and more (the rest
+# cut in ranges of K), the block-scaled MMA where it applies
+@pytest.mark.parametrize("T,K,N", [(700, 512, 640), (700, 1152, 999), (2048, 2048, 2560), (2300, 1152, 2531), (1000, 128, 72),
+                                   (600, 7168, 136)])
+@pytest.mark.parametrize("precision", ["fp8", "fp8_ue8m0"])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_tiled(T, K, N, precision, out_dtype):
+    x, lin, w, g = _inputs(T, K, N, precision, "rowmajor", seed=T + N)
+    lin.out_dtype = out_dtype
+    res = torch.randn(T, N, generator=g).bfloat16().to(DEV)
+    a = _quant(x, precision)[2]
+    xd = x.to(DEV)
+    _check(lin(xd), a, w)
+    out = lin(xd, residual=res)
+    _check(out, a, w, residual=res)
+    assert torch.equal(lin(xd, residual=res), out)
     assert lin.check_status(T) == 0
 
 
@@ -215,3 +238,31 @@ def test_few_wait_that_runs_out(monkeypatch):
     out = L.lib.forward_few(x.to(DEV))
     assert L.lib.check_status(3) == 0
     _check_few(out, *L.reference(x)[1:])
+
+
+def test_first_calls_of_a_process_captured():
+    """Nothing that the first call sets up stands in the way of a capture."""
+    code = """
+import torch, sparse_moe_transformer_fwd_b200 as moe
+d, E, de, T = 256, 8, 128, 3
+g = torch.Generator("cuda").manual_seed(0)
+r = lambda *s: torch.randn(*s, device="cuda", generator=g).bfloat16()
+L = moe.MoELayer(r(E, d), torch.zeros(E, device="cuda"), r(E + 1, 2 * de, d), r(E + 1, d, de), top_k=2)
+lin = moe.Fp8Linear(r(640, 7168))
+x, y = r(T, d), r(T, 7168)
+out, lout = torch.empty(T, d, device="cuda").bfloat16(), torch.empty(T, 640, device="cuda").bfloat16()
+L.few_workspace(T), lin.workspace(T)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    L.forward_few(x, out=out)
+    lin(y, out=lout)
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(out, L.forward_few(x)) and torch.equal(lout, lin(y))
+assert L.check_status(T) == 0 and lin.check_status(T) == 0
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0 and "captured" in p.stdout, p.stderr[-2000:]
