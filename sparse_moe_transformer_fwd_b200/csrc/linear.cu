@@ -17,7 +17,8 @@
 // sums are added in K order, so the result does not depend on timing: where all
 // tiles are cut, in 3 to 16 parts, a tile's CTAs are one cluster that exchanges
 // them through shared memory (1 us); else they go to the workspace and a second
-// kernel adds them (2 us; a tile's last CTA alone took 13 with 64 tokens).
+// kernel adds them (2 us; a tile's last CTA alone took 13 with 64 tokens, and 10
+// with its own part kept in registers).
 //   warp 0      TMA producer: a stage is two K blocks (two 16 KB boxes of W, two
 //               boxes of activations)
 //   warp 1      TMEM allocator and MMA issuer: a stage's K blocks go to adjacent
@@ -636,60 +637,7 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
             }
             const int T = p.T - g.t0;  // tokens from the group's first on
             const int r = q * 32 + (lane >> 2), t2 = 2 * (lane & 3);
-            if (__builtin_expect(g.nk == KB, 0)) {
-                if (!ok) continue;
-                // (addresses advance by constants: worked out for each of 64 values
-                // they took 2.7 us a tile)
-                const size_t first = static_cast<size_t>(g.t0 + t2) * p.N + g.n0 + r;
-                const int rows = p.N - g.n0 - r;  // e (8 rows on) is a row if 8 e < rows
-                auto store = [&](auto *dst, auto &&convert) {
-                    constexpr int AHEAD = 2;  // token groups whose residuals are in flight together
-                    const size_t group = static_cast<size_t>(8) * p.N;
-#pragma unroll
-                    for (int g0 = 0; g0 < NT / 8; g0 += AHEAD) {
-                        if (8 * g0 >= T) break;
-                        float res[AHEAD][2][4] = {};
-                        if (p.residual) {
-#pragma unroll
-                            for (int i = 0; i < 2 * AHEAD; ++i) {
-                                const uint16_t *src = p.residual + first + (g0 + i / 2) * group + (i & 1) * p.N;
-                                if (8 * (g0 + i / 2) + t2 + (i & 1) < T)
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        if (8 * e < rows) res[i / 2][i & 1][e] = bf16_f(src[8 * e]);
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < 2 * AHEAD; ++i) {
-                            auto *to = dst + first + (g0 + i / 2) * group + (i & 1) * p.N;
-                            if (8 * (g0 + i / 2) + t2 + (i & 1) < T)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const float2 a = acc[g0 + i / 2][e >> 1][e & 1];
-                                    float v = i & 1 ? a.y : a.x;
-                                    if (p.residual) v = __fadd_rn(v, res[i / 2][i & 1][e]);
-                                    if (8 * e < rows) to[8 * e] = convert(v);
-                                }
-                        }
-                    }
-                };
-                if (p.out_f32) store(static_cast<float *>(p.out), [](float v) { return v; });
-                else store(static_cast<__nv_bfloat16 *>(p.out), [](float v) { return __float2bfloat16_rn(v); });
-            } else {
-                // One part of a tile: [token][128 rows] to the workspace, or each
-                // piece to the CTA of the cluster that adds it.
-                if (!p.cluster) {
-                    float *mine = p.partial + static_cast<size_t>(g.part) * NT * 128 + r;
-                    if (ok) {
-#pragma unroll
-                        for (int e = 0; e < NT; ++e) {
-                            const int t = e / 8 * 8 + t2 + (e & 1);
-                            const float2 v = acc[e / 8][e >> 2 & 1][e >> 1 & 1];
-                            if (t < T) mine[t * 128 + (e & 6) * 4] = e & 1 ? v.y : v.x;
-                        }
-                    }
-                    continue;
-                }
+            if (p.cluster) {  // each piece to the CTA of the cluster that adds it
                 if (S::SUMS_IN_RING) cluster_arrive();
                 cluster_wait();
                 const uint32_t at = smem_u32(sums) + (blockIdx.x % p.parts) * p.share * 8;
@@ -703,7 +651,58 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
                     }
                 }
                 cluster_arrive();
+                continue;
             }
+            if (g.nk != KB) {  // one part of a tile: [token][128 rows] to the workspace
+                float *mine = p.partial + static_cast<size_t>(g.part) * NT * 128 + r;
+                if (ok) {
+#pragma unroll
+                    for (int e = 0; e < NT; ++e) {
+                        const int t = e / 8 * 8 + t2 + (e & 1);
+                        const float2 v = acc[e / 8][e >> 2 & 1][e >> 1 & 1];
+                        if (t < T) mine[t * 128 + (e & 6) * 4] = e & 1 ? v.y : v.x;
+                    }
+                }
+                continue;
+            }
+            if (!ok) continue;
+            // (addresses advance by constants: worked out for each of 64 values
+            // they took 2.7 us a tile)
+            const size_t first = static_cast<size_t>(g.t0 + t2) * p.N + g.n0 + r;
+            const int rows = p.N - g.n0 - r;  // e (8 rows on) is a row if 8 e < rows
+            auto store = [&](auto *dst, auto &&convert) {
+                constexpr int AHEAD = 2;  // token groups whose residuals are in flight together
+                const size_t group = static_cast<size_t>(8) * p.N;
+#pragma unroll
+                for (int g0 = 0; g0 < NT / 8; g0 += AHEAD) {
+                    if (8 * g0 >= T) break;
+                    float res[AHEAD][2][4] = {};
+                    if (p.residual) {
+#pragma unroll
+                        for (int i = 0; i < 2 * AHEAD; ++i) {
+                            const uint16_t *src = p.residual + first + (g0 + i / 2) * group + (i & 1) * p.N;
+                            if (8 * (g0 + i / 2) + t2 + (i & 1) < T)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (8 * e < rows) res[i / 2][i & 1][e] = bf16_f(src[8 * e]);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2 * AHEAD; ++i) {
+                        auto *to = dst + first + (g0 + i / 2) * group + (i & 1) * p.N;
+                        if (8 * (g0 + i / 2) + t2 + (i & 1) < T)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float2 a = acc[g0 + i / 2][e >> 1][e & 1];
+                                float v = i & 1 ? a.y : a.x;
+                                if (p.residual) v = __fadd_rn(v, res[i / 2][i & 1][e]);
+                                if (8 * e < rows) to[8 * e] = convert(v);
+                            }
+                    }
+                }
+            };
+            if (p.out_f32) store(static_cast<float *>(p.out), [](float v) { return v; });
+            else store(static_cast<__nv_bfloat16 *>(p.out), [](float v) { return __float2bfloat16_rn(v); });
         }
     }
 
