@@ -270,6 +270,11 @@ __device__ __forceinline__ void l2_prefetch(const void *p, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
+// Brings the line at `p` (an address that may be read) into L2: a hint.
+__device__ __forceinline__ void l2_prefetch_line(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
+}
+
 // Makes this thread's generic-proxy shared-memory writes visible to the
 // async proxy (tcgen05.cp, TMA) once a barrier orders them.
 __device__ __forceinline__ void fence_proxy_async_smem() {

@@ -571,6 +571,9 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
         Taken item;
         Segment g;
         while (next_segment(item, g)) {
+            // the residual's rows into L2 while the tile streams (two lines a token)
+            if (const int i = threadIdx.x & 127; p.residual && i < 2 * NT && g.t0 + i / 2 < p.T && g.n0 + (i & 1) * 64 < p.N)
+                l2_prefetch_line(p.residual + static_cast<size_t>(g.t0 + i / 2) * p.N + g.n0 + (i & 1) * 64);
             // [token group][16 rows][8 rows]: tokens 8 group + 2 (lane % 4) and the next
             float2 acc[NT / 8][2][2];
 #pragma unroll
@@ -717,27 +720,39 @@ linear_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
         decode(blockIdx.x, g);
         const int rank = blockIdx.x % p.parts;
         const LinearOut out{p.residual, p.out, p.T, p.N, p.out_f32};
-        for (uint32_t i = threadIdx.x; i < p.share; i += blockDim.x) {
-            const int piece = rank * p.share + i;  // [token group][warp][8 rows][lane]
-            const int n = g.n0 + (piece >> 5 & 15) * 8 + (piece >> 2 & 7), t = g.t0 + (piece >> 9) * 8 + 2 * (piece & 3);
-            if (n >= p.N || t >= min(g.t0 + NT, p.T)) continue;
-            const size_t at = static_cast<size_t>(t) * p.N + n;
-            const bool two = t + 1 < p.T;
-            float res[2] = {};
-            if (p.residual) {
-                res[0] = bf16_f(p.residual[at]);
-                if (two) res[1] = bf16_f(p.residual[at + p.N]);
+        // a piece: [token group][warp][8 rows][lane]; residuals of BATCH pieces in
+        // flight together (one at a time, 64 tokens' took 7 us; few tokens have
+        // one, and less code to fetch)
+        constexpr int BATCH = NT == 64 ? 4 : 1;
+        for (uint32_t i0 = threadIdx.x; i0 < p.share; i0 += BATCH * blockDim.x) {
+            float res[BATCH][2] = {};
+            size_t at[BATCH];
+            int have[BATCH];  // tokens of the piece that are stored
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                const uint32_t i = i0 + b * blockDim.x;
+                const int piece = rank * p.share + i;
+                const int n = g.n0 + (piece >> 5 & 15) * 8 + (piece >> 2 & 7), t = g.t0 + (piece >> 9) * 8 + 2 * (piece & 3);
+                have[b] = i < p.share && n < p.N ? min(2, min(g.t0 + NT, p.T) - t) : 0;
+                at[b] = static_cast<size_t>(t) * p.N + n;
+                if (p.residual && have[b] > 0) res[b][0] = bf16_f(p.residual[at[b]]);
+                if (p.residual && have[b] > 1) res[b][1] = bf16_f(p.residual[at[b] + p.N]);
             }
-            float2 f = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                if (have[b] <= 0) continue;
+                float2 f = make_float2(0.0f, 0.0f);
 #pragma unroll 4
-            for (int k = 0; k < p.parts; ++k) {
-                const float2 v = sums[k * p.share + i];
-                f.x = __fadd_rn(f.x, v.x), f.y = __fadd_rn(f.y, v.y);
+                for (int k = 0; k < p.parts; ++k) {
+                    const float2 v = sums[k * p.share + i0 + b * blockDim.x];
+                    f.x = __fadd_rn(f.x, v.x), f.y = __fadd_rn(f.y, v.y);
+                }
+                out.store(at[b], f.x, res[b][0]);
+                if (have[b] > 1) out.store(at[b] + p.N, f.y, res[b][1]);
             }
-            out.store(at, f.x, res[0]);
-            if (two) out.store(at + p.N, f.y, res[1]);
         }
     }
+
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
