@@ -792,6 +792,11 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
             const int nch = (nk + SPC - 1) / SPC;  // K chunks of the item (last may be short)
             int seg, row0, rows_valid, nt;
             decode_tile<TM>(s, n_seg, tile, p.n_tiles_n, seg, row0, rows_valid, nt);
+            if (LIN && p.residual) {  // its rows into L2 while the tile is worked on
+                for (int i = threadIdx.x - 128; i < 512; i += EPI_THREADS)
+                    if (i / 4 < rows_valid && nt * 256 + i % 4 * 64 < p.n_valid)
+                        l2_prefetch_line(p.residual + static_cast<size_t>(row0 + i / 4) * p.n_valid + nt * 256 + i % 4 * 64);
+            }
             const bool warp_active = q * (M64 ? 16 : 32) < rows_valid;
             const bool valid = r_in < rows_valid;
             const bool store_row = valid && hh == 0;  // M64: one lane of the pair stores
