@@ -113,6 +113,16 @@ def test_weights_beyond_32_bits(T, layout):
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("T,K,N", [(3, 1 << 20, 130), (40, 1 << 17, 40), (1, 128, 1 << 20), (20, 256, (1 << 19) + 5), (600, 1 << 16, 24)])
+def test_longest_sizes(T, K, N):
+    """The limits of K and N: many parts of one tile, many rounds of short ones."""
+    x, lin, w, _ = _inputs(T, K, N, "fp8", "rowmajor", seed=7)
+    out = lin(x.to(DEV))
+    assert lin.check_status(T) == 0
+    _check(out, _quant(x, "fp8")[2], w)
+    assert torch.equal(lin(x.to(DEV)), out)
+
+
 def test_graphs_that_share_a_workspace():
     """Captured calls of different shapes on one workspace, replayed in turn."""
     shapes = [(2, 7168, 640), (40, 512, 999), (3, 256, 40064), (300, 1536, 256)]
