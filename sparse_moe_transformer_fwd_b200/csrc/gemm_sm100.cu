@@ -792,11 +792,6 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
             const int nch = (nk + SPC - 1) / SPC;  // K chunks of the item (last may be short)
             int seg, row0, rows_valid, nt;
             decode_tile<TM>(s, n_seg, tile, p.n_tiles_n, seg, row0, rows_valid, nt);
-            if (LIN && p.residual) {  // its rows into L2 while the tile is worked on
-                for (int i = threadIdx.x - 128; i < 512; i += EPI_THREADS)
-                    if (i / 4 < rows_valid && nt * 256 + i % 4 * 64 < p.n_valid)
-                        l2_prefetch_line(p.residual + static_cast<size_t>(row0 + i / 4) * p.n_valid + nt * 256 + i % 4 * 64);
-            }
             const bool warp_active = q * (M64 ? 16 : 32) < rows_valid;
             const bool valid = r_in < rows_valid;
             const bool store_row = valid && hh == 0;  // M64: one lane of the pair stores
@@ -805,6 +800,48 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
             float2 acc2[64];  // columns (2j, 2j+1) of the thread's 128
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc2[i] = make_float2(0.0f, 0.0f);
+            const bool part = LIN && !MX && item >= from;
+            constexpr bool ragged = DENSE == LINEAR_RAGGED;  // rows that are not whole 16-byte vectors
+            if (LIN && p.residual && !part) {
+                // The sums start from the residual: read in row segments (a lane 8
+                // or 4 columns of each of 8 rows) and transposed to a row a lane.
+                // (Added at the tile's end, 16 bytes of 32 rows to a load, it took
+                // 4 us a tile; read there in segments, it spilled registers.)
+                constexpr int CW = ragged ? 4 : 8;  // columns of a chunk
+                const int li = lane & 7;
+#pragma unroll
+                for (int c = 0; c < 128; c += 8 * CW) {
+                    const int col = (c < 64 ? col_lo + c : col_hi + c - 64) + CW * li, cols = p.n_valid - nt * 256;
+                    uint4 ch[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int o = stored_row_of_lane<M64>((lane & ~7) | j, q, rows_valid);
+                        const uint16_t *rp = p.residual + static_cast<size_t>(row0 + o) * p.n_valid + nt * 256 + col;
+                        ch[j] = make_uint4(0, 0, 0, 0);
+                        if constexpr (ragged) {
+                            if (o >= 0 && col < cols) ch[j].x = static_cast<uint32_t>(rp[0]) << 16;
+                            if (o >= 0 && col + 1 < cols) ch[j].y = static_cast<uint32_t>(rp[1]) << 16;
+                            if (o >= 0 && col + 2 < cols) ch[j].z = static_cast<uint32_t>(rp[2]) << 16;
+                            if (o >= 0 && col + 3 < cols) ch[j].w = static_cast<uint32_t>(rp[3]) << 16;
+                        } else {
+                            if (o >= 0 && col < cols) ch[j] = *reinterpret_cast<const uint4 *>(rp);
+                        }
+                    }
+                    transpose_chunks<8>(ch, li);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t w[4] = {ch[j].x, ch[j].y, ch[j].z, ch[j].w};
+                        const int at = (c + CW * j) / 2;
+                        if constexpr (ragged) {
+                            acc2[at] = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+                            acc2[at + 1] = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc2[at + i] = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
+                        }
+                    }
+                }
+            }
             // K block (counted from kb0) whose partial this thread promotes in chunk c
             auto kb_of = [&](int c) { return M64 ? 2 * c + hh : c; };
             // chunks per scale group of four K blocks (M64: K steps 2c and
@@ -993,20 +1030,16 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     continue;
                 }
                 if (!warp_active) continue;  // uniform over the warp
-                // LINEAR: out has any number of columns; `ragged` rows are not whole
-                // 16-byte vectors
+                // LINEAR: out has any number of columns
                 const int ldo = LIN ? p.n_valid : p.N_out;
                 auto in_out = [&](int col) { return !LIN || nt * 256 + col < p.n_valid; };
-                const bool part = LIN && !MX && item >= from;
-                constexpr bool ragged = DENSE == LINEAR_RAGGED;
-                if (DENSE && p.residual && store_row && !part && !ragged) {
+                if (DENSE == DENSE_FFN && p.residual && store_row) {
                     // the pre-norm block's residual, added before the one rounding
-                    const uint16_t *rp = p.residual + row * ldo + nt * 256;
-                    const uint4 zero = make_uint4(0, 0, 0, 0);
+                    const uint16_t *rp = p.residual + row * p.N_out + nt * 256;
 #pragma unroll
                     for (int c = 0; c < 64; c += 8) {
-                        const uint4 a = in_out(col_lo + c) ? *reinterpret_cast<const uint4 *>(rp + col_lo + c) : zero;
-                        const uint4 b = in_out(col_hi + c) ? *reinterpret_cast<const uint4 *>(rp + col_hi + c) : zero;
+                        const uint4 a = *reinterpret_cast<const uint4 *>(rp + col_lo + c);
+                        const uint4 b = *reinterpret_cast<const uint4 *>(rp + col_hi + c);
                         const uint32_t ra[4] = {a.x, a.y, a.z, a.w}, rb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -1044,13 +1077,8 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                                 continue;
                             }
                             const size_t at = static_cast<size_t>(row0 + o) * ldo + nt * 256 + col;
-                            float f[4] = {__uint_as_float(ch[j].x), __uint_as_float(ch[j].y), __uint_as_float(ch[j].z),
+                            const float f[4] = {__uint_as_float(ch[j].x), __uint_as_float(ch[j].y), __uint_as_float(ch[j].z),
                                           __uint_as_float(ch[j].w)};
-                            if (p.residual) {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    if (col + i < cols) f[i] = __fadd_rn(f[i], __uint_as_float(static_cast<uint32_t>(p.residual[at + i]) << 16));
-                            }
                             if (p.out_f32) {
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
