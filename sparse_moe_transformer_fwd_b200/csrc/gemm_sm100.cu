@@ -842,6 +842,14 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     }
                 }
             }
+            if (DENSE == LINEAR && p.residual && item + static_cast<int>(gridDim.x) < (MX ? total_items : from)) {
+                // the next whole tile's residual into L2 while this one is worked on
+                int nseg, nrow0, nrows, nnt;
+                decode_tile<TM>(s, n_seg, item + gridDim.x, p.n_tiles_n, nseg, nrow0, nrows, nnt);
+                for (int i = threadIdx.x - 128; i < 512; i += EPI_THREADS)
+                    if (i / 4 < nrows && nnt * 256 + i % 4 * 64 < p.n_valid)
+                        l2_prefetch_line(p.residual + static_cast<size_t>(nrow0 + i / 4) * p.n_valid + nnt * 256 + i % 4 * 64);
+            }
             // K block (counted from kb0) whose partial this thread promotes in chunk c
             auto kb_of = [&](int c) { return M64 ? 2 * c + hh : c; };
             // chunks per scale group of four K blocks (M64: K steps 2c and
