@@ -476,7 +476,7 @@ typedef struct {
 } moe_linear_shape;
 
 /* Bytes of workspace the three calls below need (0 on an invalid shape): the
- * status word first (moe_check_status), then tile counters, which every call
+ * status word first (moe_check_status), then counters, which every call
  * leaves zero, the quantised x and partial sums.  Zero-fill it once before
  * first use; one workspace then serves linear calls of any shapes that it is
  * large enough for, one after the other on a stream (calls that overlap need

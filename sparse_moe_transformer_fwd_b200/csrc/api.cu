@@ -1147,9 +1147,9 @@ int moe_forward_few_prenorm(const moe_shape *s, const uint16_t *h, const uint16_
 namespace moe {
 namespace {
 
-// Tile counters of linear_stream sit in a region of fixed size, so that one
-// zero-filled workspace serves linears of any shapes: each launch leaves the
-// counters zero, and no other region of another shape reaches them.
+// The stream kernel's counters sit in a region of fixed size, so that one
+// zero-filled workspace serves linears of any shapes: each launch leaves them
+// zero, and no other region of another shape reaches them.
 constexpr int kLinearMaxN = 1 << 20;
 
 int check_linear_shape(const moe_linear_shape *s) {
@@ -1165,7 +1165,7 @@ int check_linear_shape(const moe_linear_shape *s) {
     if (s->weight_layout == MOE_LAYOUT_TILED && s->N % 128)
         return fail(MOE_ERR_INVALID_ARG, "tiled weights need N %% 128 == 0");
     if (s->out_f32 != 0 && s->out_f32 != 1) return fail(MOE_ERR_INVALID_ARG, "out_f32 must be 0 or 1");
-    // tensor-map coordinates are 32-bit, and the padded partial sums of a batch stay addressable
+    // tensor-map coordinates are 32-bit
     if (static_cast<long long>(s->N + 255) / 256 * 2 * s->K >= (1LL << 31))
         return fail(MOE_ERR_INVALID_ARG, "N * K too large");
     if (static_cast<long long>(s->T) * std::max(s->K, s->N) > (1LL << 36) || s->T > (1 << 30))
@@ -1178,7 +1178,7 @@ int linear_padded_n(const moe_linear_shape *s) { return (s->N + 255) / 256 * 256
 // x is quantised in the product's kernel for at most kLinearQuantRows tokens
 // and shares of at most 16 K blocks a CTA: every CTA quantises what it reads,
 // which a long stream waits for (7 tokens, 7168 x 64007: 189 blocks a CTA, 91 us
-// so against 81) and a short one hides (one launch less).
+// so against 81 at the time) and a short one hides (one launch less).
 bool linear_quantises(const moe_linear_shape *s) {
     const int tiles = (s->N + 127) / 128, KB = s->K / 128;
     return s->T <= kLinearQuantRows &&

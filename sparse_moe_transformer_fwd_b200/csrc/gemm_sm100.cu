@@ -165,7 +165,7 @@ struct KParams {
     uint16_t *const *ret_y;  // device array [world]
     int sc_tma;            // fp32 promotion: the scale groups are loaded by TMA (tmap_sa, tmap_sw)
     int early_b;           // single segment: B may be read ahead of the kernel before this one
-    int nb_valid;          // 128-row blocks of B that have scales (a single slot's ragged last tile)
+    int nb_valid;          // LINEAR: 128-row blocks of B that have scales (the last tile may have one)
     // LINEAR: tiles below split_from are done whole and stored to out [rows_total,
     // n_valid] (out_f32: binary32); of those from it on, each of ksplit items of a
     // tile stores its sums to partial [tile][item][128][256].
@@ -356,9 +356,9 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     }
     // One segment (a dense layer): the block's first work item and the weights
     // it streams depend on no earlier kernel of the call (early_b: nor on one
-    // before the call, which an earlier launch of the call has waited for), so thread 0 (which initialised
-    // the barriers) starts the B loads of its first `pre` stages before the
-    // wait below; the producer adds their A loads after it.
+    // before the call, which an earlier launch of the call has waited for), so
+    // thread 0 (which initialised the barriers) starts the B loads of its first
+    // `pre` stages before the wait below; the producer adds their A loads after it.
     int pre = 0;
     const int NBq = p.b_rows / 128;
     auto b_blocks = [&](int slot, int nt, long long &t_lo, long long &t_hi) {
@@ -625,7 +625,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                             const int which = lane / SF_GROUP, j = lane % SF_GROUP;
                             const int nb = which == 0 ? (GATE_UP ? nt : 2 * nt)
                                                       : (GATE_UP ? p.N_out / 128 + nt : 2 * nt + 1);
-                            const bool in = kb0 + j < KB && nb < p.nb_valid;
+                            const bool in = kb0 + j < KB && (!LIN || nb < p.nb_valid);
                             const int slot_w = p.seg_slot ? __ldg(p.seg_slot + seg) : seg;
                             cp_async4(&s.sf_b[slot][which][j],
                                       p.b_scales + (in ? (static_cast<size_t>(slot_w) * NB + nb) * KB + kb0 + j : 0),
@@ -737,7 +737,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                         a0[j] = (in && r0 < rows_valid) ? __ldg(p.a_scales + (static_cast<size_t>(row0) + r0) * KB + kb) : 0.0f;
                         a1[j] = (in && r1 < rows_valid) ? __ldg(p.a_scales + (static_cast<size_t>(row0) + r1) * KB + kb) : 0.0f;
                     }
-                    if (lane < 8 && kbg + wj < kb0 + nk && (wh ? nb_hi : nb_lo) < p.nb_valid)
+                    if (lane < 8 && kbg + wj < kb0 + nk && (!LIN || (wh ? nb_hi : nb_lo) < p.nb_valid))
                         wv = __ldg(p.b_scales + (static_cast<size_t>(slot_w) * NB + (wh ? nb_hi : nb_lo)) * KB + kbg + wj);
                     int go = 1;
                     if (lane == 0) go = mbar_wait(&s.sc_empty[slot], par, abort, p.status) ? 1 : 0;
@@ -1021,7 +1021,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     }
                 }
             } else {
-                if (DENSE == DENSE_FFN && p.partial) {
+                if (DENSE == DENSE_FFN && KS > 1) {
                     // split K: store this K range's binary32 partial sums; the
                     // reduce kernel that follows adds the KS ranges in K order
                     ks = item - (item / KS) * KS;  // recomputed: not kept live through the chunk loop
@@ -1085,8 +1085,8 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                                 continue;
                             }
                             const size_t at = static_cast<size_t>(row0 + o) * ldo + nt * 256 + col;
-                            const float f[4] = {__uint_as_float(ch[j].x), __uint_as_float(ch[j].y), __uint_as_float(ch[j].z),
-                                          __uint_as_float(ch[j].w)};
+                            const float f[4] = {__uint_as_float(ch[j].x), __uint_as_float(ch[j].y),
+                                                __uint_as_float(ch[j].z), __uint_as_float(ch[j].w)};
                             if (p.out_f32) {
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
@@ -1309,7 +1309,7 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launche
         return cudaErrorInvalidValue;
     kp.partial = g.partial;
     // with split K the residual is added by the reduce kernel
-    kp.residual = (g.gate_up || (g.partial && !linear)) ? nullptr : g.residual;
+    kp.residual = (g.gate_up || (kp.ksplit > 1 && !linear)) ? nullptr : g.residual;
     // upper bound of work items: every segment's tiles, each at most one partial
     const long long max_mtiles = linear ? (g.rows_total + 127) / 128 : g.rows_total / g.tile_m + g.n_segments;
     long long max_tiles = max_mtiles * kp.n_tiles_n * kp.ksplit;
@@ -1329,8 +1329,7 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launche
     cudaError_t e;
     mark_launch(st, *launches, g.gate_up ? "grouped_gemm_gate_up" : "grouped_gemm_down");
     // the dense layer's down GEMM (split K or a residual) has its own instances
-    const bool dense = !g.gate_up && (kp.partial || kp.residual);
-    if (mx && kp.partial) return cudaErrorInvalidValue;
+    const bool dense = !g.gate_up && (kp.ksplit > 1 || kp.residual);
     if (linear && g.n_valid % 8)
         e = mx ? launch_t<true, false, true, false, LINEAR_RAGGED>(ma, mb, msa, msw, kp, grid, st)
                : launch_t<true, false, false, false, LINEAR_RAGGED>(ma, mb, msa, msw, kp, grid, st);
