@@ -79,6 +79,16 @@ class MoeError(RuntimeError):
 
 
 _LIB = None
+_FAST = {}  # binding.c's functions
+
+
+def _fast(name):
+    """binding.c's function: it checks the arguments and makes the call in half
+    the host time that Python and ctypes take, or returns None where an argument
+    is not what the call needs; the path below then says what is wrong."""
+    if not _FAST:
+        lib()
+    return _FAST[name]
 
 
 def lib() -> ctypes.CDLL:
@@ -144,6 +154,17 @@ def lib() -> ctypes.CDLL:
                      "fp8_block_gemm", "moe_linear", "moe_linear_prenorm", "moe_forward_few",
                      "moe_forward_few_prenorm"):
             getattr(L, name).restype = ci
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise ImportError("_binding not built: run sparse_moe_transformer_fwd_b200/build.py "
+                              "(or __graft_entry__.build())") from e
+        _binding.setup(torch.Tensor, (torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn),
+                       torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream,
+                       tuple(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in
+                             ("fp8_block_gemm", "moe_linear", "moe_linear_prenorm", "moe_forward_few",
+                              "moe_forward_few_prenorm")))
+        _FAST.update(linear=_binding.linear, few=_binding.few)
         _LIB = L
     return _LIB
 
@@ -448,6 +469,10 @@ def _few_call(fn, shape, x, gamma, eps, w_router, bias, w13, w13_scales, w2, w2_
 def moe_forward_few(shape, x, w_router, bias, w13, w13_scales, w2, w2_scales, out, ws,
                     topk_idx_out=None, stream=None):
     """The whole layer for at most MOE_FEW_MAX_TOKENS tokens, in one launch."""
+    rc = _fast("few")(False, shape, x, None, 0.0, w_router, bias, w13, w13_scales, w2, w2_scales, out, ws,
+                      topk_idx_out, stream)
+    if rc is not None:
+        return _check(rc)
     _few_call(_fn("moe_forward_few"), shape, x, None, 0.0, w_router, bias, w13, w13_scales, w2, w2_scales, out,
               ws, topk_idx_out, stream)
 
@@ -455,6 +480,10 @@ def moe_forward_few(shape, x, w_router, bias, w13, w13_scales, w2, w2_scales, ou
 def moe_forward_few_prenorm(shape, h, gamma, eps, w_router, bias, w13, w13_scales, w2, w2_scales, out,
                             ws, topk_idx_out=None, stream=None):
     """out = h + MoE(bf16(RMSNorm(h) * gamma)) for at most MOE_FEW_MAX_TOKENS tokens."""
+    rc = _fast("few")(True, shape, h, gamma, eps, w_router, bias, w13, w13_scales, w2, w2_scales, out, ws,
+                      topk_idx_out, stream)
+    if rc is not None:
+        return _check(rc)
     _few_call(_fn("moe_forward_few_prenorm"), shape, h, gamma, eps, w_router, bias, w13, w13_scales, w2,
               w2_scales, out, ws, topk_idx_out, stream)
 
@@ -487,9 +516,7 @@ _FNS = {}
 
 
 def _fn(name):
-    """The library's function, looked up once: these calls are made for a few
-    microseconds of GPU work, so their own cost is kept low (pointers as plain
-    integers, no context manager on the current device)."""
+    """The library's function, looked up once."""
     f = _FNS.get(name)
     if f is None:
         f = _FNS[name] = getattr(lib(), name)
@@ -548,6 +575,9 @@ def _linear_args(shape, w, w_scales, out, dev):
 
 def fp8_block_gemm(shape, a, a_scales, w, w_scales, out, ws, residual=None, stream=None):
     """out = a W^T (+ residual) of e4m3 codes in 1x128 tiles (a) and 128x128 blocks (w)."""
+    rc = _fast("linear")(0, shape, a, a_scales, 0.0, w, w_scales, residual, out, ws, stream)
+    if rc is not None:
+        return _check(rc)
     T, K, dev = shape.T, shape.K, _device(a, "a")
     wp, wsp, op = _linear_args(shape, w, w_scales, out, dev)
     _call_on(dev, stream, _fn("fp8_block_gemm"), shape,
@@ -557,6 +587,9 @@ def fp8_block_gemm(shape, a, a_scales, w, w_scales, out, ws, residual=None, stre
 
 def moe_linear(shape, x, w, w_scales, out, ws, residual=None, stream=None):
     """out = x W^T (+ residual) of a bf16 x, quantised 1x128 on the way."""
+    rc = _fast("linear")(1, shape, x, None, 0.0, w, w_scales, residual, out, ws, stream)
+    if rc is not None:
+        return _check(rc)
     T, dev = shape.T, _device(x, "x")
     wp, wsp, op = _linear_args(shape, w, w_scales, out, dev)
     _call_on(dev, stream, _fn("moe_linear"), shape,
@@ -566,6 +599,9 @@ def moe_linear(shape, x, w, w_scales, out, ws, residual=None, stream=None):
 
 def moe_linear_prenorm(shape, h, gamma, eps, w, w_scales, out, ws, stream=None):
     """out = bf16(RMSNorm(h) * gamma) W^T."""
+    rc = _fast("linear")(2, shape, h, gamma, eps, w, w_scales, None, out, ws, stream)
+    if rc is not None:
+        return _check(rc)
     T, dev = shape.T, _device(h, "h")
     wp, wsp, op = _linear_args(shape, w, w_scales, out, dev)
     _call_on(dev, stream, _fn("moe_linear_prenorm"), shape,

@@ -1,4 +1,5 @@
-"""Build the CUDA library libmoe_fwd.so in-tree for sm_100a with nvcc.
+"""Build the CUDA library libmoe_fwd.so in-tree for sm_100a with nvcc, and the
+binding's C module (csrc/binding.c) beside it.
 
 The library is the product: every step of the layer runs in its kernels.
 cudart is linked statically and the driver entry point for tensor-map
@@ -10,6 +11,7 @@ import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -17,6 +19,7 @@ OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_fwd.so")
 SOURCES = ["api.cu", "router.cu", "permute.cu", "quant.cu", "combine.cu", "gemm_sm100.cu",
            "route_noalloc.cu", "ep.cu", "linear.cu", "few.cu"]
+BINDING = os.path.join(HERE, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
@@ -29,7 +32,7 @@ def _deps_mtime() -> float:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, BINDING)):
         return LIB
     os.makedirs(OUT, exist_ok=True)
 
@@ -51,6 +54,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
            *[o for o, _ in results], "-o", tmp]
     subprocess.check_call(cmd)
     os.replace(tmp, LIB)
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    subprocess.check_call(["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I" + sysconfig.get_paths()["include"],
+                           os.path.join(CSRC, "binding.c"), "-o", tmp])
+    os.replace(tmp, BINDING)
     return LIB
 
 

@@ -276,3 +276,46 @@ print("captured")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     p = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert p.returncode == 0 and "captured" in p.stdout, p.stderr[-2000:]
+
+
+def test_checked_calls_from_c():
+    """The binding's C functions make a good call, decline (None) whatever the
+    call does not take, and hold on to nothing."""
+    lin = moe.Fp8Linear((torch.randn(256, 512) / 20).bfloat16().to(DEV))
+    x, out, ws, sh = _x(4, 512, 1).to(DEV), torch.empty(4, 256, dtype=torch.bfloat16, device=DEV), lin.workspace(4), lin.shape(4)
+    fast = moe._native._fast("linear")
+    good = dict(kind=1, shape=sh, x=x, second=None, eps=0.0, w=lin.w, w_scales=lin.w_scales, residual=None, out=out, ws=ws,
+                stream=None)
+    call = lambda **o: fast(*{**good, **o}.values())
+    assert call() == 0 and torch.equal(out, lin(x))
+    assert call(stream=torch.cuda.Stream()) == 0
+    held = (x, out, ws, lin.w, lin.w_scales, sh)
+    before = [sys.getrefcount(t) for t in held]
+    bad = dict(x=[x.cpu(), x.float(), x[:, ::2], x[:3], None, 3], w=[lin.w[:100], lin.w.cpu(), lin.w.int()],
+               w_scales=[lin.w_scales.double()], residual=[out.float(), out[:3]], out=[out[:3], out.float(), out.t()],
+               ws=[None, ws.float()], shape=[L_shape(), 5, None], eps=["a"], kind=[None], stream=[7])
+    for name, values in bad.items():
+        for v in values:
+            assert call(**{name: v}) is None, (name, v)
+    for _ in range(100):
+        call()
+    del v, values
+    bad.clear()
+    assert [sys.getrefcount(t) for t in held] == before
+    few = moe._native._fast("few")
+    L = Layer(256, 8, 2, 128, 1, "fp8", "tiled", seed=1).lib
+    x = _x(4, 256, 1).to(DEV)
+    out = torch.empty_like(x)
+    good = dict(prenorm=False, shape=L.shape(4), x=x, gamma=None, eps=0.0, w_router=L.w_router, bias=L.bias, w13=L.w13, s13=L.w13s,
+                w2=L.w2, s2=L.w2s, out=out, ws=L.few_workspace(4), idx=None, stream=None)
+    call = lambda **o: few(*{**good, **o}.values())
+    assert call() == 0 and torch.equal(out, L.forward_few(x))
+    for name in ("x", "w_router", "bias", "w13", "s13", "w2", "s2", "out", "ws"):
+        assert call(**{name: good[name].cpu()}) is None, name
+        assert call(**{name: good[name].reshape(-1)[:-1] if name != "ws" else good[name].float()}) is None, name
+    assert call(idx=torch.empty(8, dtype=torch.int64, device=DEV)) is None
+    assert few(1, 2, 3) is None and fast() is None
+
+
+def L_shape():
+    return moe.make_shape(4, 256, 8, 2, 128)
