@@ -1188,17 +1188,22 @@ bool linear_quantises(const moe_linear_shape *s) {
 // Which kernel a batch takes, and how the tiled GEMM divides its tiles: by the
 // time that each would need, in us, from measured parts.
 //   stream: linear_plan's, and 4.5 to start and end
-//   tiled: 0.54 a K block of a 128-token x 256-column tile and 2.3 a tile (0.48 and
-//     3 by the block-scaled MMA, which cannot cut K and sums all of K less exactly
-//     than binary32 outputs want); whole rounds of tiles, then the rest in as many
-//     ranges of K as pay, whose sums a second kernel adds: 3, and their bytes from
-//     L2 and back at 8 TB/s; 4 to start and end.  (4096 tokens, 7168 x 4096, 512
-//     tiles: in four rounds 132 us, with the last one cut in two 126.)
+//   tiled: 0.54 a K block of a 128-token x 256-column tile and 2.3 a tile; whole
+//     rounds of tiles, then the rest in as many ranges of K as pay, whose sums a
+//     second kernel adds: 3, and their bytes from L2 and back at 8 TB/s; 4 to start
+//     and end.  (4096 tokens, 7168 x 4096, 512 tiles: in four rounds 132 us, with
+//     the last one cut in two 126.)
 //   both at least the weights, at 7 and 5.5 TB/s
 // The tiled GEMM needs enough tiles: 128 tokens, 7168 x 2112 (9 tiles) 23.4 us
 // against 10.9 in the stream kernel; 256 tokens, 16384 x 7168 52 against 77.
+// Power-of-two scales take the same promotion as the others: the block-scaled MMA
+// adds all of K in the tensor core, whose sum drops the low bits of small terms
+// (K = 7168, positive terms: up to 8e-6 of their sum, all one way, and 7e-5 at
+// 65536, against 5e-7 and 2e-6 in binary32).  That costs where K is short: 4096
+// tokens 2048 x 7168 86 us against 78, 4096 x 7001 183 against 162; none at 7168
+// x 4096.
 struct LinearChoice {
-    bool stream, mx;
+    bool stream;
     int from, ksplit;  // tiles done whole; ranges of K of the others
 };
 
@@ -1206,21 +1211,17 @@ int linear_tiles(const moe_linear_shape *s) { return gemm_output_tiles(s->T, lin
 
 LinearChoice linear_choice(const moe_linear_shape *s) {
     const int tiles = linear_tiles(s), KB = s->K / 128;
-    LinearChoice c{s->T <= kLinearQuantRows, false, tiles, 1};
+    LinearChoice c{s->T <= kLinearQuantRows, tiles, 1};
     if (c.stream || s->T == 0) return c;
     const int sms = std::min(num_sms(), kLinearMaxCtas);
     const float bytes = static_cast<float>(s->N) * s->K, stream_w = bytes / 5.5e6f;
     const float rounds = static_cast<float>((tiles + sms - 1) / sms);
     float best = 4.0f + std::max(stream_w, rounds * (0.54f * KB + 2.3f));
-    auto take = [&](float us, bool mx, int from, int ks) {
-        if (us < best) best = us, c.mx = mx, c.from = from, c.ksplit = ks;
-    };
-    if (s->precision == MOE_FP8_UE8M0 && !s->out_f32)
-        take(4.0f + std::max(stream_w, rounds * (0.48f * KB + 3.0f)), true, tiles, 1);
     const int whole = tiles / sms, from = whole * sms, rest = tiles - from;
     for (int ks = 2; rest && ks <= std::min(sms / rest, KB / 4); ++ks) {
-        const float us = whole * (0.54f * KB + 2.3f) + 0.54f * std::min(KB, (KB + ks - 1) / ks + 3) + 2.3f;
-        take(7.0f + std::max(stream_w, us) + 2.0f * 128 * 256 * 4 / 8e6f * rest * ks, false, from, ks);
+        const float work = whole * (0.54f * KB + 2.3f) + 0.54f * std::min(KB, (KB + ks - 1) / ks + 3) + 2.3f;
+        const float us = 7.0f + std::max(stream_w, work) + 2.0f * 128 * 256 * 4 / 8e6f * rest * ks;
+        if (us < best) best = us, c.from = from, c.ksplit = ks;
     }
     if (s->T <= kLinearStreamRows) {
         const int columns = s->T <= 32 ? 32 : 64;
@@ -1305,7 +1306,6 @@ int linear_product(const moe_linear_shape *s, const uint16_t *x, const void *a, 
     g.n_slots = 1;
     g.n_segments = 1;
     g.status = at<int>(ws, L.status);
-    g.ue8m0 = choice.mx;
     g.tile_m = kTileM;
     g.early_b = *n > 0;
     g.n_valid = s->N;

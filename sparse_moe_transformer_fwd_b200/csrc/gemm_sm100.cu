@@ -283,6 +283,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     // the ragged stores in it 4096 tokens of 7168 x 4096 take 152 us, not 145)
     constexpr bool LIN = DENSE >= LINEAR;
     static_assert(!DENSE || !GATE_UP, "split K and residual: down GEMM only");
+    static_assert(!LIN || (FP8 && !MX && !M64), "linear: software promotion, 128-row tiles");
     using R = Roles<MX>;
     extern __shared__ uint8_t smem_raw[];
     GemmSmem &s = *reinterpret_cast<GemmSmem *>(
@@ -304,9 +305,9 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     const int n_seg = p.n_segments;
     // work item = (output tile, K range): K blocks [kb0, kb0 + nk)
     const int KS = (DENSE && !MX) ? p.ksplit : 1;  // MX: residual only
-    const int from = LIN && !MX ? p.split_from : 0;
+    const int from = LIN ? p.split_from : 0;
     auto k_range = [&](int item, int &tile, int &ks, int &kb0, int &nk) {
-        if (LIN && (MX || item < from)) {
+        if (LIN && item < from) {
             tile = item;
             ks = 0;
             kb0 = 0;
@@ -625,7 +626,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                             const int which = lane / SF_GROUP, j = lane % SF_GROUP;
                             const int nb = which == 0 ? (GATE_UP ? nt : 2 * nt)
                                                       : (GATE_UP ? p.N_out / 128 + nt : 2 * nt + 1);
-                            const bool in = kb0 + j < KB && (!LIN || nb < p.nb_valid);
+                            const bool in = kb0 + j < KB;
                             const int slot_w = p.seg_slot ? __ldg(p.seg_slot + seg) : seg;
                             cp_async4(&s.sf_b[slot][which][j],
                                       p.b_scales + (in ? (static_cast<size_t>(slot_w) * NB + nb) * KB + kb0 + j : 0),
@@ -800,7 +801,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
             float2 acc2[64];  // columns (2j, 2j+1) of the thread's 128
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc2[i] = make_float2(0.0f, 0.0f);
-            const bool part = LIN && !MX && item >= from;
+            const bool part = LIN && item >= from;
             constexpr bool ragged = DENSE == LINEAR_RAGGED;  // rows that are not whole 16-byte vectors
             if (LIN && p.residual && !part) {
                 // The sums start from the residual: read in row segments (a lane 8
@@ -842,7 +843,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     }
                 }
             }
-            if (DENSE == LINEAR && p.residual && item + static_cast<int>(gridDim.x) < (MX ? total_items : from)) {
+            if (DENSE == LINEAR && p.residual && item + static_cast<int>(gridDim.x) < from) {
                 // the next whole tile's residual into L2 while this one is worked on
                 int nseg, nrow0, nrows, nnt;
                 decode_tile<TM>(s, n_seg, item + gridDim.x, p.n_tiles_n, nseg, nrow0, nrows, nnt);
@@ -1250,7 +1251,7 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launche
     const int a_rows = m64 ? 64 : (linear ? std::min(g.rows_total, 128) : 128);
     if (!make_map_2d(&ma, g.a, g.fp8, g.K, g.rows_total, a_rows)) return cudaErrorInvalidValue;
     // rows of B: past them the maps fill with zeros (linear: N_out is padded to whole tiles)
-    if (linear && (g.n_slots != 1 || g.gate_up || g.seg_start || !g.fp8 || m64 || g.n_valid > b_rows)) return cudaErrorInvalidValue;
+    if (linear && (g.n_slots != 1 || g.gate_up || g.seg_start || !g.fp8 || g.ue8m0 || m64 || g.n_valid > b_rows)) return cudaErrorInvalidValue;
     const long long rows = linear ? g.n_valid : static_cast<long long>(g.n_slots) * b_rows;
     if (g.b_rowmajor) {
         if (rows >= (1LL << 31)) return cudaErrorInvalidValue;
@@ -1315,7 +1316,7 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launche
     long long max_tiles = max_mtiles * kp.n_tiles_n * kp.ksplit;
     if (linear) {
         const long long tiles = max_mtiles * kp.n_tiles_n;
-        if (g.split_from < 0 || g.split_from > tiles || (mx && g.split_from != tiles) || (g.split_from < tiles && !g.partial) ||
+        if (g.split_from < 0 || g.split_from > tiles || (g.split_from < tiles && !g.partial) ||
             (kp.ksplit > 1 && g.K / 128 / kp.ksplit < 4))
             return cudaErrorInvalidValue;
         kp.split_from = g.split_from;
@@ -1331,11 +1332,9 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launche
     // the dense layer's down GEMM (split K or a residual) has its own instances
     const bool dense = !g.gate_up && (kp.ksplit > 1 || kp.residual);
     if (linear && g.n_valid % 8)
-        e = mx ? launch_t<true, false, true, false, LINEAR_RAGGED>(ma, mb, msa, msw, kp, grid, st)
-               : launch_t<true, false, false, false, LINEAR_RAGGED>(ma, mb, msa, msw, kp, grid, st);
+        e = launch_t<true, false, false, false, LINEAR_RAGGED>(ma, mb, msa, msw, kp, grid, st);
     else if (linear)
-        e = mx ? launch_t<true, false, true, false, LINEAR>(ma, mb, msa, msw, kp, grid, st)
-               : launch_t<true, false, false, false, LINEAR>(ma, mb, msa, msw, kp, grid, st);
+        e = launch_t<true, false, false, false, LINEAR>(ma, mb, msa, msw, kp, grid, st);
     else if (dense && mx)
         e = launch_t<true, false, true, false, DENSE_FFN>(ma, mb, msa, msw, kp, grid, st);
     else if (g.fp8 && g.ue8m0)
