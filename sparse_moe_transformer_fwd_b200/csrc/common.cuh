@@ -243,6 +243,11 @@ __device__ __forceinline__ void cp_async16(void *smem_dst, const void *src, bool
                  "l"(src), "r"(valid ? 16 : 0)
                  : "memory");
 }
+// The first `bytes` (0 to 16) of a 16-byte piece, and zeros.
+__device__ __forceinline__ void cp_async16_part(void *smem_dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(src), "r"(bytes)
+                 : "memory");
+}
 __device__ __forceinline__ void cp_async4(void *smem_dst, const void *src, bool valid) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(smem_dst)),
                  "l"(src), "r"(valid ? 4 : 0)

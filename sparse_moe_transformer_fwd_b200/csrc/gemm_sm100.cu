@@ -65,7 +65,6 @@ namespace {
 
 constexpr int BM = 128;                  // tile rows
 constexpr int BN = 256;                  // tile columns (TMEM columns per buffer)
-constexpr int STAGES = 4;
 constexpr int A_BYTES = BM * 128;        // 16 KB per stage
 constexpr int B_BYTES = BN * 128;        // 32 KB per stage
 constexpr int NUM_THREADS = 384;  // 3 warpgroups
@@ -107,10 +106,23 @@ struct Roles {
                   "register split must fit in the block's launch allocation");
 };
 
+// kinds of single-segment instances; a linear's may be RAGGED (columns not a
+// multiple of 8) and add a RESIDUAL
+constexpr int DENSE_FFN = 1, LINEAR = 2, RAGGED = 4, RESIDUAL = 8;
+
+// RESIDUAL: one stage less, and the tile's residual, staged by each epilogue
+// warp for its own 32 rows of two 64-column halves: 16-byte chunks, or 9 of them
+// a row and half where rows start anywhere.
+template <int DENSE>
 struct __align__(1024) GemmSmem {
+    static constexpr bool RES = DENSE & RESIDUAL;
+    static constexpr int STAGES = RES ? 3 : 4;
+    static constexpr int SEGS = RES ? 1 : MAX_SEG;
+    static constexpr int RES_CHUNKS = DENSE & RAGGED ? 9 : 8;  // of a row's half
+    static constexpr int RES_WARP = 32 * 2 * RES_CHUNKS * 16;  // bytes of a warp
     uint8_t a[STAGES][A_BYTES];
     uint8_t b[STAGES][B_BYTES];
-    uint8_t sf[SF_BUFS][SF_BYTES];  // MX: UE8M0 scale blocks in the tcgen05.cp source layout
+    uint8_t sf[RES ? 1 : SF_BUFS][SF_BYTES];  // MX: UE8M0 scale blocks in the tcgen05.cp source layout
     union {
         float sf_a[SF_STAGING][SF_GROUP][BM];  // MX: fp32 scales staged by warp 3 for warp 2
         ScaleGroup scg[SC_GROUPS];             // fp32 promotion: ring of scale groups
@@ -130,17 +142,23 @@ struct __align__(1024) GemmSmem {
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort;
-    float amax_x[2][2][BM];  // [iteration parity][column half][row]
-    int32_t seg_start[MAX_SEG];
-    int32_t seg_rows[MAX_SEG];
-    int32_t tile_start[MAX_SEG + 1];
+    float amax_x[2][2][RES ? 1 : BM];  // (gate/up) [iteration parity][column half][row]
+    int32_t seg_start[SEGS];
+    int32_t seg_rows[SEGS];
+    int32_t tile_start[SEGS + 1];
+    alignas(16) uint8_t res[RES ? EPI_THREADS / 32 * RES_WARP : 16];
 };
 
-static_assert(sizeof(GemmSmem) + 1024 <= 227 * 1024, "shared memory budget of one CTA");
-// TMA destinations of the scale ring: 128-byte boundaries
-static_assert(offsetof(GemmSmem, scg) % 128 == 0 && sizeof(ScaleGroup) % 128 == 0 &&
-                  offsetof(ScaleGroup, w) % 128 == 0 && sizeof(ScaleGroup::w[0]) == 128,
-              "scale-group TMA destinations must start on 128-byte boundaries");
+template <int DENSE>
+constexpr size_t gemm_smem() {
+    using S = GemmSmem<DENSE>;
+    static_assert(sizeof(S) + 1024 <= 227 * 1024, "shared memory budget of one CTA");
+    // TMA destinations of the scale ring: 128-byte boundaries
+    static_assert(offsetof(S, scg) % 128 == 0 && sizeof(ScaleGroup) % 128 == 0 &&
+                      offsetof(ScaleGroup, w) % 128 == 0 && sizeof(ScaleGroup::w[0]) == 128,
+                  "scale-group TMA destinations must start on 128-byte boundaries");
+    return sizeof(S) + 1024;
+}
 
 struct KParams {
     const float *a_scales;
@@ -172,10 +190,9 @@ struct KParams {
     int split_from, n_valid, out_f32;
     int a_bytes;  // of a K block's A box: of the rows there are, where they are fewer than a tile
 };
-constexpr int DENSE_FFN = 1, LINEAR = 2, LINEAR_RAGGED = 3;  // kinds of single-segment instances
 
-template <int TM>
-__device__ __forceinline__ void decode_tile(const GemmSmem &s, int n_seg, int tile, int n_tiles_n,
+template <int TM, class S>
+__device__ __forceinline__ void decode_tile(const S &s, int n_seg, int tile, int n_tiles_n,
                                             int &seg, int &row0, int &rows_valid, int &nt) {
     if (n_seg == 1) {
         // one segment (a dense layer, or one expert): column-tile major, so the blocks that
@@ -278,15 +295,18 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     static_assert(!M64 || (FP8 && !MX), "64-row tiles: fp8 with software promotion only");
     // DENSE: the down GEMM of a dense layer (DENSE_FFN), with split K (software
     // promotion only) and a residual add, or the block-scaled linear (LINEAR:
-    // columns a multiple of 8, LINEAR_RAGGED: any number); separate instances, so
-    // the expert GEMMs keep their register budget (as LINEAR keeps its own: with
-    // the ragged stores in it 4096 tokens of 7168 x 4096 take 152 us, not 145)
-    constexpr bool LIN = DENSE >= LINEAR;
+    // columns a multiple of 8, | RAGGED: any number; | RESIDUAL); separate
+    // instances, so the expert GEMMs keep their register budget (as LINEAR keeps
+    // its own: with the ragged stores in it 4096 tokens of 7168 x 4096 take 152 us,
+    // not 145)
+    constexpr bool LIN = DENSE >= LINEAR, ragged = DENSE & RAGGED, with_residual = DENSE & RESIDUAL;
     static_assert(!DENSE || !GATE_UP, "split K and residual: down GEMM only");
     static_assert(!LIN || (FP8 && !MX && !M64), "linear: software promotion, 128-row tiles");
     using R = Roles<MX>;
     extern __shared__ uint8_t smem_raw[];
-    GemmSmem &s = *reinterpret_cast<GemmSmem *>(
+    using S = GemmSmem<DENSE>;
+    constexpr int STAGES = S::STAGES;
+    S &s = *reinterpret_cast<S *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int KB = FP8 ? p.K / 128 : p.K / 64;  // stages per tile (128 bytes of K each)
@@ -428,7 +448,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
             int stage = 0;
             uint32_t phase = 0;
             int armed = 0;  // bit s: stage s has been armed at least once
-            uint32_t armed_phase[STAGES] = {0, 0, 0, 0};
+            uint32_t armed_phase[STAGES] = {};
             bool ok = true;
             for (int item = blockIdx.x; item < total_items && ok; item += gridDim.x) {
                 int tile, ks, kb0, nk;
@@ -802,54 +822,34 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc2[i] = make_float2(0.0f, 0.0f);
             const bool part = LIN && item >= from;
-            constexpr bool ragged = DENSE == LINEAR_RAGGED;  // rows that are not whole 16-byte vectors
-            if (LIN && p.residual && !part) {
-                // The sums start from the residual: read in row segments (a lane 8
-                // or 4 columns of each of 8 rows) and transposed to a row a lane.
-                // (Added at the tile's end, 16 bytes of 32 rows to a load, it took
-                // 4 us a tile; read there in segments, it spilled registers.)
-                constexpr int CW = ragged ? 4 : 8;  // columns of a chunk
-                const int li = lane & 7;
-#pragma unroll
-                for (int c = 0; c < 128; c += 8 * CW) {
-                    const int col = (c < 64 ? col_lo + c : col_hi + c - 64) + CW * li, cols = p.n_valid - nt * 256;
-                    uint4 ch[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int o = stored_row_of_lane<M64>((lane & ~7) | j, q, rows_valid);
-                        const uint16_t *rp = p.residual + static_cast<size_t>(row0 + o) * p.n_valid + nt * 256 + col;
-                        ch[j] = make_uint4(0, 0, 0, 0);
-                        if constexpr (ragged) {
-                            if (o >= 0 && col < cols) ch[j].x = static_cast<uint32_t>(rp[0]) << 16;
-                            if (o >= 0 && col + 1 < cols) ch[j].y = static_cast<uint32_t>(rp[1]) << 16;
-                            if (o >= 0 && col + 2 < cols) ch[j].z = static_cast<uint32_t>(rp[2]) << 16;
-                            if (o >= 0 && col + 3 < cols) ch[j].w = static_cast<uint32_t>(rp[3]) << 16;
-                        } else {
-                            if (o >= 0 && col < cols) ch[j] = *reinterpret_cast<const uint4 *>(rp);
-                        }
-                    }
-                    transpose_chunks<8>(ch, li);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t w[4] = {ch[j].x, ch[j].y, ch[j].z, ch[j].w};
-                        const int at = (c + CW * j) / 2;
-                        if constexpr (ragged) {
-                            acc2[at] = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
-                            acc2[at + 1] = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) acc2[at + i] = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
-                        }
-                    }
+            // Where a row's half of the residual starts, and the bytes by which that
+            // is off a 16-byte boundary (ragged rows).
+            auto res_start = [&](int r, int hf, int &off) {
+                const uint16_t *rp = p.residual + static_cast<size_t>(row0 + r) * p.n_valid + nt * 256 + (hf ? col_hi : col_lo);
+                off = ragged ? static_cast<int>(reinterpret_cast<uintptr_t>(rp) & 15) : 0;
+                return reinterpret_cast<const uint8_t *>(rp) - off;
+            };
+            uint8_t *res = s.res + (warp - 4) * S::RES_WARP;
+            if (with_residual && !part) {
+                // The tile's residual, this warp's rows and columns, into shared memory
+                // while the tile is worked on; three stages of operands are enough beside
+                // it.  4096 tokens 2048 x 7168 100 us (85 without), 2048 x 7001 143.  Read
+                // at the tile's end it costs the L2 round trip and registers: 139 us, and
+                // 175 with all loads in flight, from spills, for which L1 has no room here;
+                // as the sums' start 103, each addition then rounded at its exponent.
+                constexpr int CH = S::RES_CHUNKS;
+                const uint8_t *end = reinterpret_cast<const uint8_t *>(p.residual + static_cast<size_t>(p.rows_total) * p.n_valid);
+                __syncwarp();  // the tile before has been read
+#pragma unroll 4
+                for (int i = lane; i < 32 * 2 * CH; i += 32) {
+                    const int r = i / (2 * CH), hf = i / CH & 1, k = i % CH, rt = q * 32 + r;
+                    const int cols = min(64, p.n_valid - nt * 256 - (hf ? col_hi : col_lo));
+                    int off;
+                    const uint8_t *src = res_start(rt, hf, off) + 16 * k;
+                    if (rt < rows_valid && 16 * k < off + 2 * cols)  // (a chunk's last bytes may lie behind the array)
+                        cp_async16_part(res + ((r * 2 + hf) * CH + (ragged ? k : k ^ (r & 7))) * 16, src,
+                                        static_cast<int>(min(end - src, static_cast<ptrdiff_t>(16))));
                 }
-            }
-            if (DENSE == LINEAR && p.residual && item + static_cast<int>(gridDim.x) < from) {
-                // the next whole tile's residual into L2 while this one is worked on
-                int nseg, nrow0, nrows, nnt;
-                decode_tile<TM>(s, n_seg, item + gridDim.x, p.n_tiles_n, nseg, nrow0, nrows, nnt);
-                for (int i = threadIdx.x - 128; i < 512; i += EPI_THREADS)
-                    if (i / 4 < nrows && nnt * 256 + i % 4 * 64 < p.n_valid)
-                        l2_prefetch_line(p.residual + static_cast<size_t>(nrow0 + i / 4) * p.n_valid + nnt * 256 + i % 4 * 64);
             }
             // K block (counted from kb0) whose partial this thread promotes in chunk c
             auto kb_of = [&](int c) { return M64 ? 2 * c + hh : c; };
@@ -1042,6 +1042,40 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 // LINEAR: out has any number of columns
                 const int ldo = LIN ? p.n_valid : p.N_out;
                 auto in_out = [&](int col) { return !LIN || nt * 256 + col < p.n_valid; };
+                if (with_residual && !part) {
+                    // added to the finished sums, a row to each lane
+                    cp_async_wait_all();
+                    __syncwarp();
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        if constexpr (ragged) {
+                            int off;
+                            res_start(r_in, hf, off);
+                            const uint32_t *w = reinterpret_cast<const uint32_t *>(res + (lane * 2 + hf) * S::RES_CHUNKS * 16) + off / 4;
+                            const uint32_t pick = off & 2 ? 0x5432 : 0x3210;
+                            uint32_t cur = w[0];
+#pragma unroll
+                            for (int c = 0; c < 64; c += 2) {
+                                const uint32_t next = w[c / 2 + 1], v = __byte_perm(cur, next, pick);
+                                acc(64 * hf + c) = __fadd_rn(acc(64 * hf + c), bf16_lo(v));
+                                acc(64 * hf + c + 1) = __fadd_rn(acc(64 * hf + c + 1), bf16_hi(v));
+                                cur = next;
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const uint4 v = *reinterpret_cast<const uint4 *>(res + ((lane * 2 + hf) * 8 + (k ^ (lane & 7))) * 16);
+                                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const int c = 64 * hf + 8 * k + 2 * i;
+                                    acc(c) = __fadd_rn(acc(c), bf16_lo(w[i]));
+                                    acc(c + 1) = __fadd_rn(acc(c + 1), bf16_hi(w[i]));
+                                }
+                            }
+                        }
+                    }
+                }
                 if (DENSE == DENSE_FFN && p.residual && store_row) {
                     // the pre-norm block's residual, added before the one rounding
                     const uint16_t *rp = p.residual + row * p.N_out + nt * 256;
@@ -1148,6 +1182,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 }
             }
         }
+        if constexpr (with_residual) cp_async_wait_all();  // given up: no copy outlives the block
     }
 
     // ------------------------------------------------------------- teardown
@@ -1216,7 +1251,7 @@ bool make_map_scales(CUtensorMap *m, const float *base, int cols, long long rows
 template <bool FP8, bool GATE_UP, bool MX, bool M64 = false, int DENSE = 0>
 cudaError_t launch_t(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &msa,
                      const CUtensorMap &msw, const KParams &kp, int grid, cudaStream_t st) {
-    const size_t smem = sizeof(GemmSmem) + 1024;
+    constexpr size_t smem = gemm_smem<DENSE>();
     static DeviceConfigured configured{};  // per template instance
     if (first_use_on_device(configured)) {
         // setmaxnreg redistributes exactly NUM_THREADS * LAUNCH_REGS registers:
@@ -1331,10 +1366,12 @@ cudaError_t launch_grouped_gemm(const GemmArgs &g, cudaStream_t st, int *launche
     mark_launch(st, *launches, g.gate_up ? "grouped_gemm_gate_up" : "grouped_gemm_down");
     // the dense layer's down GEMM (split K or a residual) has its own instances
     const bool dense = !g.gate_up && (kp.ksplit > 1 || kp.residual);
-    if (linear && g.n_valid % 8)
-        e = launch_t<true, false, false, false, LINEAR_RAGGED>(ma, mb, msa, msw, kp, grid, st);
+    if (linear && kp.residual)
+        e = g.n_valid % 8 ? launch_t<true, false, false, false, LINEAR | RAGGED | RESIDUAL>(ma, mb, msa, msw, kp, grid, st)
+                          : launch_t<true, false, false, false, LINEAR | RESIDUAL>(ma, mb, msa, msw, kp, grid, st);
     else if (linear)
-        e = launch_t<true, false, false, false, LINEAR>(ma, mb, msa, msw, kp, grid, st);
+        e = g.n_valid % 8 ? launch_t<true, false, false, false, LINEAR | RAGGED>(ma, mb, msa, msw, kp, grid, st)
+                          : launch_t<true, false, false, false, LINEAR>(ma, mb, msa, msw, kp, grid, st);
     else if (dense && mx)
         e = launch_t<true, false, true, false, DENSE_FFN>(ma, mb, msa, msw, kp, grid, st);
     else if (g.fp8 && g.ue8m0)

@@ -1,7 +1,7 @@
 """Which sums a linear's output is made of, bit for bit.  Whatever kernel takes a
 batch and however its tiles are cut, a bf16 output is the binary32 sum rounded
-once.  So the output in binary32 says what the others are; there is no
-tolerance."""
+once, and a residual is added once, to the finished binary32 sum.  So the output
+in binary32 without a residual says what the others are; there is no tolerance."""
 import pytest
 import torch
 
@@ -64,3 +64,18 @@ def test_long_sums_of_positive_terms(T, K, N):
     want = a @ (e4m3(lin.w[:n]) * lin.w_scales.double().repeat_interleave(128, 1).repeat_interleave(128, 0)[:n]).T
     mean = ((off[:, :n] - want) / want).mean().item()
     assert abs(mean) <= 2.0 ** -17 + (K // 128) * 2.0 ** -28, mean
+
+
+@pytest.mark.parametrize("precision", ["fp8", "fp8_ue8m0"])
+@pytest.mark.parametrize("T,K,N", CASES)
+def test_residual_is_added_to_the_finished_sum(T, K, N, precision):
+    """A residual a thousand times the product: were it in the sum from the start,
+    each of the K/128 additions would round at its exponent."""
+    x, lin, g = _linear(T, K, N, precision, T + K + N)
+    res = (torch.randn(T, N, generator=g, device=DEV) * 1024).bfloat16()
+    want = _call(lin, x, torch.float32) + res.float()
+    assert torch.equal(_call(lin, x, torch.float32, res), want)
+    assert torch.equal(_call(lin, x, torch.bfloat16, res), want.bfloat16())
+    buf = res.clone()  # in place
+    lin(x, out=buf, residual=buf)
+    assert torch.equal(buf, want.bfloat16())
