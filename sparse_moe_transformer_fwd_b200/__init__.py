@@ -25,7 +25,7 @@ from ._native import (EXPORTS, MOE_BF16, MOE_FP8_BLOCK, MOE_FP8_UE8M0, MOE_LAYOU
                       moe_ep_grouped_swiglu, MOE_EP_MAX_RANKS, MoeLinearShape, make_linear_shape,
                       moe_linear_workspace_size, alloc_linear_workspace, fp8_block_gemm, moe_linear,
                       moe_linear_prenorm, MOE_FEW_MAX_TOKENS, moe_few_workspace_size,
-                      alloc_few_workspace, moe_forward_few, moe_forward_few_prenorm)
+                      alloc_few_workspace, moe_forward_few, moe_forward_few_prenorm, Workspaces)
 
 __all__ = [
     "MoELayer", "MoeError", "MoeShape", "make_shape", "alloc_workspace", "lib", "EXPORTS",
@@ -104,7 +104,7 @@ class MoELayer:
             self.w13s = self.w2s = None
         else:
             raise ValueError(precision)
-        self._ws, self._few_ws = {}, {}
+        self._ws, self._few_ws, self._few_bytes = {}, Workspaces(self.w13.device), {}
 
     def shape(self, T: int) -> MoeShape:
         return make_shape(T, self.d, self.E, self.top_k, self.de, self.n_shared,
@@ -138,22 +138,26 @@ class MoELayer:
                             topk_idx_out=topk_idx_out, stream=stream)
         return out
 
-    def few_workspace(self, T: int) -> torch.Tensor:
-        ws = self._few_ws.get(T)
-        if ws is None:
-            ws = alloc_few_workspace(self.shape(T), self.w13.device)
-            self._few_ws[T] = ws
-        return ws
+    def few_workspace(self, T: int, stream=None) -> torch.Tensor:
+        """The workspace that forward_few's calls of at most T tokens on `stream`
+        take: streams have one each, captures theirs apart from eager calls'."""
+        nbytes = self._few_bytes.get(T)
+        if nbytes is None:
+            nbytes = self._few_bytes[T] = moe_few_workspace_size(self.shape(T))
+        return self._few_ws.get(nbytes, stream)
 
     def forward_few(self, x: torch.Tensor, out: torch.Tensor | None = None,
                     topk_idx_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """The layer for at most MOE_FEW_MAX_TOKENS tokens, in one launch;
-        routing as in __call__, out equal up to roundings."""
+        routing as in __call__, out equal up to roundings.  Calls on several
+        streams or from several threads may overlap; so may a graph's replay and
+        eager calls, but not two graphs captured on one stream."""
         T = x.shape[0]
         if out is None:
             out = torch.empty(T, self.d, dtype=torch.bfloat16, device=x.device)
-        moe_forward_few(self.shape(T), x, self.w_router, self.bias, self.w13, self.w13s, self.w2,
-                        self.w2s, out, self.few_workspace(T), topk_idx_out=topk_idx_out, stream=stream)
+        with self._few_ws.lock:
+            moe_forward_few(self.shape(T), x, self.w_router, self.bias, self.w13, self.w13s, self.w2,
+                            self.w2s, out, self.few_workspace(T, stream), topk_idx_out=topk_idx_out, stream=stream)
         return out
 
     def forward_few_prenorm(self, h: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6,
@@ -163,15 +167,16 @@ class MoELayer:
         T = h.shape[0]
         if out is None:
             out = torch.empty(T, self.d, dtype=torch.bfloat16, device=h.device)
-        moe_forward_few_prenorm(self.shape(T), h, gamma, eps, self.w_router, self.bias, self.w13,
-                                self.w13s, self.w2, self.w2s, out, self.few_workspace(T),
-                                topk_idx_out=topk_idx_out, stream=stream)
+        with self._few_ws.lock:
+            moe_forward_few_prenorm(self.shape(T), h, gamma, eps, self.w_router, self.bias, self.w13,
+                                    self.w13s, self.w2, self.w2s, out, self.few_workspace(T, stream),
+                                    topk_idx_out=topk_idx_out, stream=stream)
         return out
 
     def check_status(self, T: int) -> int:
-        """Status of the calls with T tokens so far: the first error that
-        either workspace recorded."""
-        few = moe_check_status(self._few_ws[T]) if T in self._few_ws else 0
+        """Status of __call__'s calls with T tokens and of all calls for few
+        tokens so far: the first error that a workspace recorded."""
+        few = self._few_ws.status()
         return moe_check_status(self.workspace(T)) or few
 
 
@@ -240,7 +245,11 @@ class Fp8Linear:
     128x128 blocks; precision "fp8" (fp32 block scales) or "fp8_ue8m0"
     (power-of-two block scales).  weight_layout "tiled" (default where N is a
     multiple of 128) or "rowmajor" (any N).  x bf16 [T, K] is quantised 1x128
-    on the way; out is bf16, or fp32 with out_dtype=torch.float32."""
+    on the way; out is bf16, or fp32 with out_dtype=torch.float32.
+
+    Calls on several streams or from several threads may overlap (every stream
+    has a workspace, of its largest call); so may a graph's replay and eager
+    calls, but not two graphs captured on one stream, which share a workspace."""
 
     def __init__(self, w, *, precision: str = "fp8", weight_layout: str | None = None,
                  out_dtype: torch.dtype = torch.bfloat16):
@@ -261,19 +270,18 @@ class Fp8Linear:
             fp8_block_quant(w.contiguous(), 128, self.w, self.w_scales,
                             layout=MOE_LAYOUT_TILED if weight_layout == "tiled" else MOE_LAYOUT_ROWMAJOR,
                             ue8m0=precision == "fp8_ue8m0")
-        self._ws = {}
+        self._ws = Workspaces(w.device)
+
+    def _sized(self, T: int):
+        s = make_linear_shape(T, self.K, self.N, self.precision, self.weight_layout, self.out_dtype)
+        return s, moe_linear_workspace_size(s)
 
     def shape(self, T: int) -> MoeLinearShape:
-        s = make_linear_shape(T, self.K, self.N, self.precision, self.weight_layout, self.out_dtype)
-        moe_linear_workspace_size(s)
-        return s
+        return self._sized(T)[0]
 
-    def workspace(self, T: int) -> torch.Tensor:
-        ws = self._ws.get(T)
-        if ws is None:
-            ws = alloc_linear_workspace(self.shape(T), self.w.device)
-            self._ws[T] = ws
-        return ws
+    def workspace(self, T: int, stream=None) -> torch.Tensor:
+        """The workspace that calls of T tokens on `stream` take."""
+        return self._ws.get(self._sized(T)[1], stream)
 
     def _out(self, T, out):
         return torch.empty(T, self.N, dtype=self.out_dtype, device=self.w.device) if out is None else out
@@ -283,8 +291,10 @@ class Fp8Linear:
         """x W^T, plus the residual before the one rounding of a bf16 output."""
         T = x.shape[0]
         out = self._out(T, out)
-        moe_linear(self.shape(T), x, self.w, self.w_scales, out, self.workspace(T),
-                   residual=residual, stream=stream)
+        shape, nbytes = self._sized(T)
+        with self._ws.lock:
+            moe_linear(shape, x, self.w, self.w_scales, out, self._ws.get(nbytes, stream), residual=residual,
+                       stream=stream)
         return out
 
     def quantized(self, a: torch.Tensor, a_scales: torch.Tensor, out: torch.Tensor | None = None,
@@ -293,8 +303,10 @@ class Fp8Linear:
         block_rows 1): several projections of one x quantise it once."""
         T = a.shape[0]
         out = self._out(T, out)
-        fp8_block_gemm(self.shape(T), a, a_scales, self.w, self.w_scales, out, self.workspace(T),
-                       residual=residual, stream=stream)
+        shape, nbytes = self._sized(T)
+        with self._ws.lock:
+            fp8_block_gemm(shape, a, a_scales, self.w, self.w_scales, out, self._ws.get(nbytes, stream),
+                           residual=residual, stream=stream)
         return out
 
     def forward_prenorm(self, h: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6,
@@ -302,9 +314,12 @@ class Fp8Linear:
         """bf16(RMSNorm(h) * gamma) W^T (pre-norm fused)."""
         T = h.shape[0]
         out = self._out(T, out)
-        moe_linear_prenorm(self.shape(T), h, gamma, eps, self.w, self.w_scales, out,
-                           self.workspace(T), stream=stream)
+        shape, nbytes = self._sized(T)
+        with self._ws.lock:
+            moe_linear_prenorm(shape, h, gamma, eps, self.w, self.w_scales, out, self._ws.get(nbytes, stream),
+                               stream=stream)
         return out
 
-    def check_status(self, T: int) -> int:
-        return moe_check_status(self.workspace(T))
+    def check_status(self, T: int = 0) -> int:
+        """Status of all calls so far: the first error that a workspace recorded."""
+        return self._ws.status()

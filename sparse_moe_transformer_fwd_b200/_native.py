@@ -6,6 +6,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 import torch
 
@@ -442,6 +443,76 @@ def _zeroed(nbytes, device):
     if cuda:
         torch.cuda.current_stream(ws.device).synchronize()
     return ws
+
+
+def _on(stream, device):
+    """The context in which torch's current stream is the one that a call with
+    `stream` takes (None: the current one of `device`)."""
+    if stream is None:
+        return torch.cuda.device(device)
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(stream.cuda_stream, device))
+
+
+class Workspaces:
+    """The workspaces of one object's calls.  Calls that can overlap need one
+    each, so every stream has its own, which grows to the largest call (what it
+    held is then freed in the stream's order).  Captured calls have theirs apart
+    from eager ones: a capture takes over a workspace that an eager call has
+    made, and later captures on the same stream share it, since graphs are
+    replayed where nothing is known of them.  Hold `lock` from get() until the
+    call is enqueued: a call of several launches must not be cut in two by
+    another thread's on the same workspace."""
+
+    def __init__(self, device):
+        self.lock = threading.RLock()
+        self._device = torch.device(device)
+        self.clear()
+
+    def clear(self) -> None:
+        self._streams, self._captured, self._largest = {}, {}, 0  # by raw stream; those: lists
+
+    def get(self, nbytes: int, stream=None) -> torch.Tensor:
+        index = self._device.index
+        if stream is None and torch._C._cuda_getDevice() == index and not torch.cuda.is_current_stream_capturing():
+            ws = self._streams.get(torch._C._cuda_getCurrentRawStream(index))
+            if ws is not None and ws.numel() >= nbytes:
+                return ws
+        with self.lock, _on(stream, self._device):
+            raw = torch._C._cuda_getCurrentRawStream(index)
+            if not torch.cuda.is_current_stream_capturing():
+                ws = self._streams.get(raw)
+                if ws is None or ws.numel() < nbytes:
+                    ws = self._streams[raw] = _zeroed(nbytes, self._device)
+                    self._largest = max(self._largest, nbytes)
+                return ws
+            held = self._captured.setdefault(raw, [])
+            for ws in held:
+                if ws.numel() >= nbytes:
+                    return ws
+            fit = [(ws.numel(), r) for r, ws in self._streams.items() if ws.numel() >= nbytes]
+            if fit:
+                held.append(self._streams.pop(min(fit)[1]))
+                return held[-1]
+            if nbytes > self._largest:
+                raise RuntimeError("allocate the workspace (or make one call of this size) before the capture")
+            # taken over by other streams' captures: this call's own, out of the
+            # graph's memory, which each replay fills with zeros
+            return torch.zeros(nbytes, dtype=torch.uint8, device=self._device)
+
+    def status(self) -> int:
+        """The first error that any of them recorded; clears them."""
+        first = MOE_OK
+        with self.lock:
+            every = [*self._streams.values(), *(w for held in self._captured.values() for w in held)]
+            if not every:
+                return first
+            torch.cuda.synchronize(self._device)  # whatever streams they are used on
+        with torch.cuda.device(self._device):
+            for ws in every:
+                rc = moe_check_status(ws)
+                first = first or rc
+        return first
 
 
 def alloc_few_workspace(shape: MoeShape, device="cuda") -> torch.Tensor:
