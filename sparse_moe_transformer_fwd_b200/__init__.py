@@ -25,7 +25,7 @@ from ._native import (EXPORTS, MOE_BF16, MOE_FP8_BLOCK, MOE_FP8_UE8M0, MOE_LAYOU
                       moe_ep_grouped_swiglu, MOE_EP_MAX_RANKS, MoeLinearShape, make_linear_shape,
                       moe_linear_workspace_size, alloc_linear_workspace, fp8_block_gemm, moe_linear,
                       moe_linear_prenorm, MOE_FEW_MAX_TOKENS, moe_few_workspace_size,
-                      alloc_few_workspace, moe_forward_few, moe_forward_few_prenorm, Workspaces)
+                      alloc_few_workspace, moe_forward_few, moe_forward_few_prenorm, Workspaces, new_output)
 
 __all__ = [
     "MoELayer", "MoeError", "MoeShape", "make_shape", "alloc_workspace", "lib", "EXPORTS",
@@ -121,7 +121,7 @@ class MoELayer:
                  topk_idx_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         T = x.shape[0]
         if out is None:
-            out = torch.empty(T, self.d, dtype=torch.bfloat16, device=x.device)
+            out = new_output(T, self.d, torch.bfloat16, x.device, stream)
         moe_forward(self.shape(T), x, self.w_router, self.bias, self.w13, self.w13s, self.w2,
                     self.w2s, out, self.workspace(T), topk_idx_out=topk_idx_out, stream=stream)
         return out
@@ -132,7 +132,7 @@ class MoELayer:
         """The FFN block: out = h + MoE(RMSNorm(h) * gamma) (pre-norm fused)."""
         T = h.shape[0]
         if out is None:
-            out = torch.empty(T, self.d, dtype=torch.bfloat16, device=h.device)
+            out = new_output(T, self.d, torch.bfloat16, h.device, stream)
         moe_forward_prenorm(self.shape(T), h, gamma, eps, self.w_router, self.bias, self.w13,
                             self.w13s, self.w2, self.w2s, out, self.workspace(T),
                             topk_idx_out=topk_idx_out, stream=stream)
@@ -154,7 +154,7 @@ class MoELayer:
         eager calls, but not two graphs captured on one stream."""
         T = x.shape[0]
         if out is None:
-            out = torch.empty(T, self.d, dtype=torch.bfloat16, device=x.device)
+            out = new_output(T, self.d, torch.bfloat16, x.device, stream)
         with self._few_ws.lock:
             moe_forward_few(self.shape(T), x, self.w_router, self.bias, self.w13, self.w13s, self.w2,
                             self.w2s, out, self.few_workspace(T, stream), topk_idx_out=topk_idx_out, stream=stream)
@@ -166,7 +166,7 @@ class MoELayer:
         """forward_prenorm for at most MOE_FEW_MAX_TOKENS tokens."""
         T = h.shape[0]
         if out is None:
-            out = torch.empty(T, self.d, dtype=torch.bfloat16, device=h.device)
+            out = new_output(T, self.d, torch.bfloat16, h.device, stream)
         with self._few_ws.lock:
             moe_forward_few_prenorm(self.shape(T), h, gamma, eps, self.w_router, self.bias, self.w13,
                                     self.w13s, self.w2, self.w2s, out, self.few_workspace(T, stream),
@@ -219,7 +219,7 @@ class DenseFFN:
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None):
         T = x.shape[0]
         if out is None:
-            out = torch.empty(T, self.d, dtype=torch.bfloat16, device=x.device)
+            out = new_output(T, self.d, torch.bfloat16, x.device, stream)
         moe_dense_ffn(self.shape(T), x, self.w13, self.w13s, self.w2, self.w2s, out,
                       self.workspace(T), stream=stream)
         return out
@@ -229,7 +229,7 @@ class DenseFFN:
         """The FFN block: out = h + FFN(RMSNorm(h) * gamma)."""
         T = h.shape[0]
         if out is None:
-            out = torch.empty(T, self.d, dtype=torch.bfloat16, device=h.device)
+            out = new_output(T, self.d, torch.bfloat16, h.device, stream)
         moe_dense_ffn_prenorm(self.shape(T), h, gamma, eps, self.w13, self.w13s, self.w2,
                               self.w2s, out, self.workspace(T), stream=stream)
         return out
@@ -283,14 +283,12 @@ class Fp8Linear:
         """The workspace that calls of T tokens on `stream` take."""
         return self._ws.get(self._sized(T)[1], stream)
 
-    def _out(self, T, out):
-        return torch.empty(T, self.N, dtype=self.out_dtype, device=self.w.device) if out is None else out
-
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None,
                  residual: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """x W^T, plus the residual before the one rounding of a bf16 output."""
         T = x.shape[0]
-        out = self._out(T, out)
+        if out is None:
+            out = new_output(T, self.N, self.out_dtype, self.w.device, stream)
         shape, nbytes = self._sized(T)
         with self._ws.lock:
             moe_linear(shape, x, self.w, self.w_scales, out, self._ws.get(nbytes, stream), residual=residual,
@@ -302,7 +300,8 @@ class Fp8Linear:
         """The product of codes that are quantised already (fp8_block_quant,
         block_rows 1): several projections of one x quantise it once."""
         T = a.shape[0]
-        out = self._out(T, out)
+        if out is None:
+            out = new_output(T, self.N, self.out_dtype, self.w.device, stream)
         shape, nbytes = self._sized(T)
         with self._ws.lock:
             fp8_block_gemm(shape, a, a_scales, self.w, self.w_scales, out, self._ws.get(nbytes, stream),
@@ -313,7 +312,8 @@ class Fp8Linear:
                         out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """bf16(RMSNorm(h) * gamma) W^T (pre-norm fused)."""
         T = h.shape[0]
-        out = self._out(T, out)
+        if out is None:
+            out = new_output(T, self.N, self.out_dtype, self.w.device, stream)
         shape, nbytes = self._sized(T)
         with self._ws.lock:
             moe_linear_prenorm(shape, h, gamma, eps, self.w, self.w_scales, out, self._ws.get(nbytes, stream),

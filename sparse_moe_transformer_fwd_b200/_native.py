@@ -454,6 +454,15 @@ def _on(stream, device):
                              else torch.cuda.ExternalStream(stream.cuda_stream, device))
 
 
+def new_output(rows, cols, dtype, device, stream=None) -> torch.Tensor:
+    """An output of a call on `stream`, out of that stream's memory: a block that
+    another stream has freed may still be in use there."""
+    if stream is None:
+        return torch.empty(rows, cols, dtype=dtype, device=device)
+    with _on(stream, device):
+        return torch.empty(rows, cols, dtype=dtype, device=device)
+
+
 class Workspaces:
     """The workspaces of one object's calls.  Calls that can overlap need one
     each, so every stream has its own, which grows to the largest call (what it

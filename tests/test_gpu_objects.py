@@ -190,3 +190,34 @@ def test_a_growing_workspace_under_load():
     for T in sizes:
         assert all(torch.equal(o, want[T]) for o in outs[T]), T
     assert fresh.check_status(1500) == 0
+
+
+def test_outputs_are_the_calls_streams_memory():
+    """An output that a call makes on stream= comes out of that stream's memory: a
+    block that the current stream frees later and takes again is not one that the
+    call still writes, and the other way round."""
+    lin, layer = _linear(), _layer()
+    dense = moe.DenseFFN(_x(512, 1024, 1), _x(1024, 256, 2))
+    x, y, gamma = _x(40, 2048, 1), _x(9, 1024, 2), _x(1, 1024, 3).reshape(-1)
+    calls = [lambda **kw: lin(x, **kw), lambda **kw: lin.forward_prenorm(x, x[0].contiguous(), **kw),
+             lambda **kw: layer.forward_few(y, **kw), lambda **kw: layer.forward_few_prenorm(y, gamma, **kw),
+             lambda **kw: layer(y, **kw), lambda **kw: layer.forward_prenorm(y, gamma, **kw),
+             lambda **kw: dense(y, **kw), lambda **kw: dense.forward_prenorm(y, gamma, **kw)]
+    side = torch.cuda.Stream()
+
+    class Handle:  # what else has a stream's handle
+        cuda_stream = side.cuda_stream
+
+    for call in calls:
+        want = call()
+        for stream in (side, Handle()):
+            torch.cuda.synchronize()
+            out = call(stream=stream)
+            side.synchronize()
+            assert torch.equal(out, want)
+            at, shape = out.data_ptr(), out.shape
+            del out
+            again = [torch.empty(shape, dtype=torch.bfloat16, device=DEV) for _ in range(4)]
+            assert at not in [t.data_ptr() for t in again]
+            with torch.cuda.stream(side):
+                assert torch.empty(shape, dtype=torch.bfloat16, device=DEV).data_ptr() == at
