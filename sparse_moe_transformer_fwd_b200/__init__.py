@@ -68,6 +68,23 @@ def pack_weights(w13: torch.Tensor, w2: torch.Tensor, stream=None):
     return a, b
 
 
+def _tokens(t, cols: int, name: str) -> int:
+    """T of an input [T, cols].  (The calls below take tensors that are longer
+    than their shape; what an object is given says the shape itself.)"""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dim() == 0 or t.numel() != t.shape[0] * cols:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [T, {cols}]")
+    return t.shape[0]
+
+
+def _columns(T: int, cols: int, **tensors) -> None:
+    """Refuses tensors (None passes) of other rows than [T, cols]; more rows may follow."""
+    for name, t in tensors.items():
+        if isinstance(t, torch.Tensor) and t.numel() != T * cols and (t.dim() < 2 or t.shape[-1] != cols):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{T}, {cols}]")
+
+
 class MoELayer:
     """One MoE FFN layer with resident weights.
 
@@ -152,7 +169,9 @@ class MoELayer:
         routing as in __call__, out equal up to roundings.  Calls on several
         streams or from several threads may overlap; so may a graph's replay and
         eager calls, but not two graphs captured on one stream."""
-        T = x.shape[0]
+        T = _tokens(x, self.d, "x")
+        _columns(T, self.d, out=out)
+        _columns(T, self.top_k, topk_idx_out=topk_idx_out)
         if out is None:
             out = new_output(T, self.d, torch.bfloat16, x.device, stream)
         with self._few_ws.lock:
@@ -164,7 +183,10 @@ class MoELayer:
                             out: torch.Tensor | None = None,
                             topk_idx_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """forward_prenorm for at most MOE_FEW_MAX_TOKENS tokens."""
-        T = h.shape[0]
+        T = _tokens(h, self.d, "h")
+        _columns(1, self.d, gamma=gamma)
+        _columns(T, self.d, out=out)
+        _columns(T, self.top_k, topk_idx_out=topk_idx_out)
         if out is None:
             out = new_output(T, self.d, torch.bfloat16, h.device, stream)
         with self._few_ws.lock:
@@ -286,7 +308,8 @@ class Fp8Linear:
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None,
                  residual: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """x W^T, plus the residual before the one rounding of a bf16 output."""
-        T = x.shape[0]
+        T = _tokens(x, self.K, "x")
+        _columns(T, self.N, out=out, residual=residual)
         if out is None:
             out = new_output(T, self.N, self.out_dtype, self.w.device, stream)
         shape, nbytes = self._sized(T)
@@ -299,7 +322,9 @@ class Fp8Linear:
                   residual: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """The product of codes that are quantised already (fp8_block_quant,
         block_rows 1): several projections of one x quantise it once."""
-        T = a.shape[0]
+        T = _tokens(a, self.K, "a")
+        _columns(T, self.K // 128, a_scales=a_scales)
+        _columns(T, self.N, out=out, residual=residual)
         if out is None:
             out = new_output(T, self.N, self.out_dtype, self.w.device, stream)
         shape, nbytes = self._sized(T)
@@ -311,7 +336,9 @@ class Fp8Linear:
     def forward_prenorm(self, h: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6,
                         out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """bf16(RMSNorm(h) * gamma) W^T (pre-norm fused)."""
-        T = h.shape[0]
+        T = _tokens(h, self.K, "h")
+        _columns(1, self.K, gamma=gamma)
+        _columns(T, self.N, out=out)
         if out is None:
             out = new_output(T, self.N, self.out_dtype, self.w.device, stream)
         shape, nbytes = self._sized(T)

@@ -221,3 +221,46 @@ def test_outputs_are_the_calls_streams_memory():
             assert at not in [t.data_ptr() for t in again]
             with torch.cuda.stream(side):
                 assert torch.empty(shape, dtype=torch.bfloat16, device=DEV).data_ptr() == at
+
+
+def test_shapes_that_objects_refuse():
+    """Tensors with enough elements in other rows: a batch in more dimensions than
+    two, longer rows, columns of another width."""
+    lin, layer = _linear(K=512, N=640), _layer(d=512)
+    x, gamma = _x(4, 512, 1), _x(1, 512, 3).reshape(-1)
+    q, s = torch.empty(4, 512, dtype=torch.uint8, device=DEV), torch.empty(4, 4, device=DEV)
+    moe.fp8_block_quant(x, 1, q, s)
+    wide = torch.zeros(4, 1024, dtype=torch.bfloat16, device=DEV)
+    cube = _x(8, 512, 2).reshape(2, 4, 512)
+    for bad in (wide, cube, wide.reshape(2, -1)):
+        for call in (lin, layer.forward_few, lambda t: lin.forward_prenorm(t, gamma),
+                     lambda t: layer.forward_few_prenorm(t, gamma)):
+            with pytest.raises(ValueError, match="expected \\[T, 512\\]"):
+                call(bad)
+    with pytest.raises(ValueError, match="a_scales"):
+        lin.quantized(q, torch.zeros(4, 8, device=DEV))
+    with pytest.raises(ValueError, match="a: shape"):
+        lin.quantized(torch.zeros(4, 1024, dtype=torch.uint8, device=DEV), s)
+    for name in ("out", "residual"):
+        with pytest.raises(ValueError, match=name):
+            lin(x, **{name: wide})
+    with pytest.raises(ValueError, match="gamma"):
+        lin.forward_prenorm(x, wide[0])
+    with pytest.raises(ValueError, match="gamma"):
+        layer.forward_few_prenorm(x, wide[0])
+    with pytest.raises(ValueError, match="out"):
+        layer.forward_few(x, out=wide)
+    with pytest.raises(ValueError, match="topk_idx_out"):
+        layer.forward_few(x, topk_idx_out=torch.zeros(4, 16, dtype=torch.int32, device=DEV))
+    with pytest.raises(TypeError):
+        lin(None)
+    # what says the same rows in another way, and longer outputs, are taken
+    want = lin(x)
+    assert torch.equal(lin(x.reshape(4, 1, 512)), want)
+    out = torch.full((6, 640), 3.0, dtype=torch.bfloat16, device=DEV)
+    lin(x, out=out, residual=torch.zeros_like(out))
+    assert torch.equal(out[:4], want) and torch.all(out[4:] == 3.0)
+    flat = torch.empty(4 * 640, dtype=torch.bfloat16, device=DEV)
+    lin(x, out=flat)
+    assert torch.equal(flat.reshape(4, 640), want)
+    assert torch.equal(lin.forward_prenorm(x, gamma.reshape(1, 512)), lin.forward_prenorm(x, gamma))
