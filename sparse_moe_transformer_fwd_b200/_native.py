@@ -86,7 +86,8 @@ _FAST = {}  # binding.c's functions
 def _fast(name):
     """binding.c's function: it checks the arguments and makes the call in half
     the host time that Python and ctypes take, or returns None where an argument
-    is not what the call needs; the path below then says what is wrong."""
+    is not what the call needs; the path below then makes the call or says what
+    is wrong."""
     if not _FAST:
         lib()
     return _FAST[name]
@@ -155,19 +156,25 @@ def lib() -> ctypes.CDLL:
                      "fp8_block_gemm", "moe_linear", "moe_linear_prenorm", "moe_forward_few",
                      "moe_forward_few_prenorm"):
             getattr(L, name).restype = ci
-        try:
-            from . import _binding
-        except ImportError as e:
-            raise ImportError("_binding not built: run sparse_moe_transformer_fwd_b200/build.py "
-                              "(or __graft_entry__.build())") from e
-        _binding.setup(torch.Tensor, (torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn),
-                       torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream,
-                       tuple(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in
-                             ("fp8_block_gemm", "moe_linear", "moe_linear_prenorm", "moe_forward_few",
-                              "moe_forward_few_prenorm")))
-        _FAST.update(linear=_binding.linear, few=_binding.few)
+        _FAST.update(_c_binding(L))
         _LIB = L
     return _LIB
+
+
+def _c_binding(L) -> dict:
+    """binding.c's functions.  Without the module (built for another Python, or
+    not at all) every call takes the path through ctypes: the same checks and the
+    same kernels, in twice the host time."""
+    try:
+        from . import _binding
+    except ImportError:
+        return dict.fromkeys(("linear", "few"), lambda *args: None)
+    _binding.setup(torch.Tensor, (torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn),
+                   torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream,
+                   tuple(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in
+                         ("fp8_block_gemm", "moe_linear", "moe_linear_prenorm", "moe_forward_few",
+                          "moe_forward_few_prenorm")))
+    return {"linear": _binding.linear, "few": _binding.few}
 
 
 def _check(rc: int) -> None:

@@ -1,5 +1,5 @@
-"""Build the CUDA library libmoe_fwd.so in-tree for sm_100a with nvcc, and the
-binding's C module (csrc/binding.c) beside it.
+"""Build the CUDA library libmoe_fwd.so in-tree for sm_100a with nvcc, and, where
+this Python's headers are, the binding's C module (csrc/binding.c) beside it.
 
 The library is the product: every step of the layer runs in its kernels.
 cudart is linked statically and the driver entry point for tensor-map
@@ -20,6 +20,7 @@ LIB = os.path.join(HERE, "libmoe_fwd.so")
 SOURCES = ["api.cu", "router.cu", "permute.cu", "quant.cu", "combine.cu", "gemm_sm100.cu",
            "route_noalloc.cu", "ep.cu", "linear.cu", "few.cu"]
 BINDING = os.path.join(HERE, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
+INCLUDE = sysconfig.get_paths()["include"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
@@ -32,7 +33,9 @@ def _deps_mtime() -> float:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, BINDING)):
+    with_binding = os.path.exists(os.path.join(INCLUDE, "Python.h"))
+    made = (LIB, BINDING) if with_binding else (LIB,)
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in made):
         return LIB
     os.makedirs(OUT, exist_ok=True)
 
@@ -54,9 +57,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
            *[o for o, _ in results], "-o", tmp]
     subprocess.check_call(cmd)
     os.replace(tmp, LIB)
+    if not with_binding:  # the package does without; an old one may be of other structures
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
+        return LIB
     tmp = BINDING + ".tmp%d" % os.getpid()
-    subprocess.check_call(["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I" + sysconfig.get_paths()["include"],
-                           os.path.join(CSRC, "binding.c"), "-o", tmp])
+    subprocess.check_call(["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I" + INCLUDE, os.path.join(CSRC, "binding.c"), "-o", tmp])
     os.replace(tmp, BINDING)
     return LIB
 
