@@ -425,8 +425,9 @@ int moe_ep_grouped_swiglu(const moe_shape *shape, int rows, const void *a, const
  * block per SM, so that expert weights stream from HBM all the while.
  * Arguments, weights and layouts as for moe_forward; T at most
  * MOE_FEW_MAX_TOKENS (larger: MOE_ERR_INVALID_ARG).
- * Routing (topk_idx_out and the gates) is moe_forward's bit for bit.  The
- * numerics differ from moe_forward's in roundings only: x and H are quantised
+ * Routing (topk_idx_out and the gates) is moe_forward's bit for bit, for any x
+ * and any bias without NaN (with one: top_k different experts, but which is not
+ * specified, neither here nor there).  The numerics differ from moe_forward's in roundings only: x and H are quantised
  * as by moe_linear, and the experts' rows are kept in binary32 up to the one
  * rounding of out.
  * The launch needs every SM of the device for its blocks to wait for one

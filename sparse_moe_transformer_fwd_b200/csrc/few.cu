@@ -189,6 +189,10 @@ struct Item {
     int used, part;  // down: index of the expert among those selected, part of the product
 };
 
+// warp_topk's choice, by integers of the same order as the selection values (two
+// warp reductions a round, not five shuffles of three values).  A NaN, which only
+// the bias can bring in, is ordered by its bits there and not at all in warp_topk;
+// here each round still takes another expert.
 template <int PER_LANE>
 __device__ __forceinline__ void topk_keys(const float *row, const float *bias, int E, int k, int lane, int &my_e,
                                           float &my_s) {
