@@ -430,6 +430,7 @@ int moe_ep_grouped_swiglu(const moe_shape *shape, int rows, const void *a, const
  * specified, neither here nor there).  The numerics differ from moe_forward's in roundings only: x and H are quantised
  * as by moe_linear, and the experts' rows are kept in binary32 up to the one
  * rounding of out.
+ * out may be x's (h's) memory.
  * The launch needs every SM of the device for its blocks to wait for one
  * another: it starts when the kernels of other streams leave room for them,
  * and two such calls need a workspace each if they can overlap. */
@@ -490,7 +491,7 @@ size_t moe_linear_workspace_size(const moe_linear_shape *shape);
  *   w_scales fp32 [ceil(N/128), K/128]
  *   residual bf16 [T, N] or NULL
  *   out      [T, N] bf16 or fp32 (out_f32); may be the residual's memory when
- *            both are bf16 */
+ *            both are bf16; must not overlap a */
 int fp8_block_gemm(const moe_linear_shape *shape, const uint8_t *a, const float *a_scales,
                    const void *w, const float *w_scales, const uint16_t *residual, void *out,
                    void *ws, size_t ws_bytes, void *stream);
@@ -500,14 +501,14 @@ int fp8_block_gemm(const moe_linear_shape *shape, const uint8_t *a, const float 
  * operation rounded to binary32 (power-of-two scales, as by
  * fp8_block_quant_ue8m0, in MOE_FP8_UE8M0).  The scale and the factor are
  * within an ulp of fp8_block_quant's quotients, so an element at the border of
- * two codes may take the other one here. */
+ * two codes may take the other one here.  out may overlap x. */
 int moe_linear(const moe_linear_shape *shape, const uint16_t *x, const void *w,
                const float *w_scales, const uint16_t *residual, void *out, void *ws,
                size_t ws_bytes, void *stream);
 
 /* The same behind the block's pre-norm: x = bf16((h * rstd) * gamma), rstd as
  * in moe_forward_prenorm.
- *   h bf16 [T, K]; gamma bf16 [K]; eps >= 0 */
+ *   h bf16 [T, K]; gamma bf16 [K]; eps >= 0; out may overlap h */
 int moe_linear_prenorm(const moe_linear_shape *shape, const uint16_t *h, const uint16_t *gamma,
                        float eps, const void *w, const float *w_scales, void *out, void *ws,
                        size_t ws_bytes, void *stream);

@@ -1321,6 +1321,11 @@ int linear_product(const moe_linear_shape *s, const uint16_t *x, const void *a, 
     return MOE_OK;
 }
 
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
 // codes != NULL: the product of given codes; else x is quantised (after the
 // pre-norm, with gamma set) into the workspace first.
 int linear_impl(const char *name, const moe_linear_shape *s, const uint16_t *x, const uint16_t *gamma,
@@ -1344,13 +1349,16 @@ int linear_impl(const char *name, const moe_linear_shape *s, const uint16_t *x, 
     CHECK_PTR(out);
     if (residual && !aligned16(residual)) return fail(MOE_ERR_INVALID_ARG, "residual is not 16-byte aligned");
     if (gamma && !(eps >= 0.0f)) return fail(MOE_ERR_INVALID_ARG, "eps must be >= 0");
+    const size_t in = static_cast<size_t>(s->T) * s->K, out_bytes = static_cast<size_t>(s->T) * s->N * (s->out_f32 ? 4 : 2);
+    if (codes && overlap(codes, in, out, out_bytes)) return fail(MOE_ERR_INVALID_ARG, "out overlaps a");
     RETURN_IF(check_device());
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     int n = 0;
     const bool ue = s->precision == MOE_FP8_UE8M0;
     uint8_t *a = at<uint8_t>(ws, L.a);
     float *a_scales = at<float>(ws, L.a_scales);
-    const bool in_product = !codes && !gamma && linear_quantises(s);
+    // (in place, x is read whole before the product writes)
+    const bool in_product = !codes && !gamma && linear_quantises(s) && !overlap(x, 2 * in, out, out_bytes);
     if (gamma)
         LAUNCH(launch_linear_prenorm_quant(x, gamma, s->T, s->K, eps, ue, a, a_scales, st, &n), "pre-norm and quantise");
     else if (!codes && !in_product)

@@ -264,3 +264,46 @@ def test_shapes_that_objects_refuse():
     lin(x, out=flat)
     assert torch.equal(flat.reshape(4, 640), want)
     assert torch.equal(lin.forward_prenorm(x, gamma.reshape(1, 512)), lin.forward_prenorm(x, gamma))
+
+
+@pytest.mark.parametrize("T", [1, 5, 16, 17, 64, 300])
+def test_in_place(T):
+    """The output in the input's memory, and in what follows it: projections of equal
+    widths, the residual as well, behind the pre-norm; codes beside the output."""
+    K = 1536
+    lin, gamma = _linear(K=K, N=K), _x(1, K, 3).reshape(-1)
+    x = _x(T, K, 1)
+    want = lin(x), lin(x, residual=x), lin.forward_prenorm(x, gamma)
+    for w, call in zip(want, (lambda b: lin(b, out=b), lambda b: lin(b, out=b, residual=b),
+                              lambda b: lin.forward_prenorm(b, gamma, out=b))):
+        for _ in range(3):
+            buf = x.clone()
+            call(buf)
+            assert torch.equal(buf, w)
+    long = torch.zeros(T + 1, K, dtype=torch.bfloat16, device=DEV)
+    long[:T] = x
+    lin(long[:T], out=long[1:])
+    assert torch.equal(long[1:], want[0])
+    both = torch.empty(T * K * 3, dtype=torch.uint8, device=DEV)
+    s = torch.empty(T, K // 128, device=DEV)
+    moe.fp8_block_quant(x, 1, both[: T * K], s)
+    codes, out = both[: T * K].reshape(T, K), both[T * K :].view(torch.bfloat16).reshape(T, K)
+    clean = lin.quantized(codes.clone(), s)
+    assert torch.equal(lin.quantized(codes, s, out=out), clean)
+    with pytest.raises(moe.MoeError, match="overlaps"):
+        lin.quantized(codes, s, out=both[: 2 * T * K].view(torch.bfloat16).reshape(T, K))
+    assert lin.check_status() == 0
+
+
+@pytest.mark.parametrize("precision", ["fp8", "bf16"])
+@pytest.mark.parametrize("T", [1, 7, 16])
+def test_few_in_place(T, precision):
+    layer, gamma = _layer(precision=precision), _x(1, 1024, 3).reshape(-1)
+    x = _x(T, 1024, 1)
+    want = layer.forward_few(x), layer.forward_few_prenorm(x, gamma)
+    for _ in range(5):
+        a, b = x.clone(), x.clone()
+        layer.forward_few(a, out=a)
+        layer.forward_few_prenorm(b, gamma, out=b)
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+    assert layer.check_status(T) == 0
