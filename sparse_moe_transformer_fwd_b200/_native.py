@@ -485,6 +485,9 @@ class Workspaces:
         self._device = torch.device(device)
         self.clear()
 
+    def __reduce__(self):  # a copy of an object has workspaces of its own
+        return Workspaces, (self._device,)
+
     def clear(self) -> None:
         self._streams, self._captured, self._largest = {}, {}, 0  # by raw stream; those: lists
 

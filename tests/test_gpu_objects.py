@@ -1,6 +1,8 @@
 """Fp8Linear and MoELayer.forward_few as objects that a program shares: between
 streams, threads, graphs and batch sizes.  Overlapping calls give what each
 gives alone, bit for bit."""
+import copy
+import pickle
 import threading
 
 import pytest
@@ -307,3 +309,15 @@ def test_few_in_place(T, precision):
         layer.forward_few_prenorm(b, gamma, out=b)
         assert torch.equal(a, want[0]) and torch.equal(b, want[1])
     assert layer.check_status(T) == 0
+
+
+def test_copies_and_pickles():
+    """An object's copy has workspaces of its own."""
+    lin, layer = _linear(K=512, N=640), _layer(d=512)
+    x, y = _x(40, 512, 1), _x(4, 512, 2)
+    want = lin(x), layer.forward_few(y)
+    for again in (copy.deepcopy, lambda o: pickle.loads(pickle.dumps(o))):
+        a, b = again(lin), again(layer)
+        assert torch.equal(a(x), want[0]) and torch.equal(b.forward_few(y), want[1])
+        assert a.workspace(40).data_ptr() != lin.workspace(40).data_ptr()
+        assert a.check_status() == 0 and b.check_status(4) == 0
