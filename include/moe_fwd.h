@@ -501,7 +501,8 @@ int fp8_block_gemm(const moe_linear_shape *shape, const uint8_t *a, const float 
  * operation rounded to binary32 (power-of-two scales, as by
  * fp8_block_quant_ue8m0, in MOE_FP8_UE8M0).  The scale and the factor are
  * within an ulp of fp8_block_quant's quotients, so an element at the border of
- * two codes may take the other one here.  out may overlap x. */
+ * two codes may take the other one here.  A row with an infinity or NaN gives
+ * NaN.  out may overlap x. */
 int moe_linear(const moe_linear_shape *shape, const uint16_t *x, const void *w,
                const float *w_scales, const uint16_t *residual, void *out, void *ws,
                size_t ws_bytes, void *stream);

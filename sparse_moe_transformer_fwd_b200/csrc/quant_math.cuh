@@ -16,13 +16,19 @@ namespace moe {
 // of the quotient, so only an element at a border of two codes can differ.
 // The factor of a tile below 448 / FLT_MAX is held at FLT_MAX (no code is NaN
 // for 0 * inf); an all-zero tile gets scale 1 and factor 0; ue: power-of-two
-// scale (ue8m0_scale).
+// scale (ue8m0_scale).  An infinite amax gives factor 0, so the infinity's code
+// is NaN and the row's results are, with either scale (ue8m0_scale alone would
+// make it 448 * 2^120).
 __device__ __forceinline__ float tile_scale(float amax, bool ue, float *inv) {
     if (amax == 0.0f) {
         *inv = 0.0f;
         return 1.0f;
     }
-    if (ue) return ue8m0_scale(amax, inv);
+    if (ue) {
+        const float sc = ue8m0_scale(amax, inv);
+        if (isinf(amax)) *inv = 0.0f;
+        return sc;
+    }
     *inv = fminf(__fmul_rn(__frcp_rn(amax), 448.0f), 3.402823466e38f);
     return __fmul_rn(amax, static_cast<float>(1.0 / 448.0));
 }

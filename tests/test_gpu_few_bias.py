@@ -1,4 +1,4 @@
-"""moe_forward_few's selection where the bias holds infinities or NaN."""
+"""moe_forward_few where the bias or a token holds infinities or NaN."""
 import pytest
 import torch
 
@@ -41,3 +41,21 @@ def test_nan_in_the_bias_still_chooses_different_experts(E):
         assert torch.isfinite(out).all()
         assert torch.equal(layer.forward_few(x), out)
     assert layer._few_ws.status() == 0
+
+
+@pytest.mark.parametrize("precision", ["fp8", "fp8_ue8m0", "bf16"])
+@pytest.mark.parametrize("layout", ["tiled", "rowmajor"])
+def test_infinite_tokens_keep_to_their_rows(precision, layout):
+    g = torch.Generator(DEV).manual_seed(1)
+    n = lambda *s: (torch.randn(*s, generator=g, device=DEV) / s[-1] ** 0.5).bfloat16()
+    layer = moe.MoELayer(n(24, 512), torch.zeros(24, device=DEV), n(25, 256, 512), n(25, 512, 128), top_k=4,
+                         precision=precision, weight_layout=layout)
+    x, gamma = torch.randn(9, 512, generator=g, device=DEV).bfloat16(), torch.ones(512, dtype=torch.bfloat16, device=DEV)
+    y = x.clone()
+    y[2, 5], y[4, 9], y[8] = float("inf"), float("nan"), float("-inf")
+    keep = [0, 1, 3, 5, 6, 7]
+    for call in (layer.forward_few, lambda t: layer.forward_few_prenorm(t, gamma)):
+        want, got = call(x), call(y)
+        assert torch.equal(got[keep], want[keep])
+        assert not torch.isfinite(got[[2, 4, 8]]).any()
+    assert layer.check_status(9) == 0

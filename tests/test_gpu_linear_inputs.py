@@ -87,3 +87,39 @@ def test_weights_written_just_before_every_call(T, K, N, layout, kind):
                             layout=moe.MOE_LAYOUT_TILED if layout == "tiled" else moe.MOE_LAYOUT_ROWMAJOR)
         assert torch.equal(call(), want)
     assert lin.check_status(T) == 0
+
+
+@pytest.mark.parametrize("T,K", [(1, 8320), (5, 16384), (40, 12416), (2, 131072), (300, 8192), (300, 9088)])
+def test_long_rows_behind_the_prenorm(T, K):
+    """Rows longer than the statistics' piece in shared memory: the same codes as of
+    the pre-norm worked out apart, so the same output."""
+    g = torch.Generator(DEV).manual_seed(K)
+    h = torch.randn(T, K, generator=g, device=DEV).bfloat16()
+    gamma = (1 + 0.1 * torch.randn(K, generator=g, device=DEV)).bfloat16()
+    lin = moe.Fp8Linear((torch.randn(264, K, generator=g, device=DEV) / K ** 0.5).bfloat16(), weight_layout="rowmajor")
+    x, _ = oracle.rmsnorm(u16(h), u16(gamma), 1e-6)
+    x = torch.from_numpy(np.ascontiguousarray(x).reshape(T, K).view(np.int16)).view(torch.bfloat16).to(DEV)
+    assert torch.equal(lin.forward_prenorm(h, gamma), lin(x))
+    assert lin.check_status(T) == 0
+
+
+@pytest.mark.parametrize("precision", ["fp8", "fp8_ue8m0"])
+@pytest.mark.parametrize("T,N", [(9, 640), (20, 300), (300, 1000), (700, 999)])
+def test_infinities_and_nan_stay_in_their_rows(T, N, precision):
+    g = torch.Generator(DEV).manual_seed(T)
+    x = torch.randn(T, 1024, generator=g, device=DEV).bfloat16()
+    lin = moe.Fp8Linear((torch.randn(N, 1024, generator=g, device=DEV) / 32).bfloat16(), precision=precision, weight_layout="rowmajor")
+    want = lin(x)
+    y = x.clone()
+    y[1, 7], y[T // 2, 300], y[T - 1] = float("inf"), float("nan"), float("-inf")
+    got = lin(y)
+    bad = [1, T // 2, T - 1]
+    keep = [t for t in range(T) if t not in bad]
+    assert torch.equal(got[keep], want[keep])
+    assert torch.isnan(got[bad]).all()
+    res = torch.zeros(T, N, dtype=torch.bfloat16, device=DEV)
+    res[2], res[3, 5] = float("inf"), float("nan")
+    got = lin(x, residual=res)
+    assert torch.equal(got[[0, 1]], want[[0, 1]]) and torch.isinf(got[2]).all()
+    assert torch.isnan(got[3, 5]) and torch.isfinite(got[3, :5]).all() and torch.isfinite(got[3, 6:]).all()
+    assert lin.check_status(T) == 0
