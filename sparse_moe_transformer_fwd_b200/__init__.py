@@ -73,16 +73,16 @@ def _tokens(t, cols: int, name: str) -> int:
     than their shape; what an object is given says the shape itself.)"""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dim() == 0 or t.numel() != t.shape[0] * cols:
+    T = t.shape[0] if t.dim() else -1
+    if t.numel() != T * cols:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [T, {cols}]")
-    return t.shape[0]
+    return T
 
 
-def _columns(T: int, cols: int, **tensors) -> None:
-    """Refuses tensors (None passes) of other rows than [T, cols]; more rows may follow."""
-    for name, t in tensors.items():
-        if isinstance(t, torch.Tensor) and t.numel() != T * cols and (t.dim() < 2 or t.shape[-1] != cols):
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{T}, {cols}]")
+def _rows(t, T: int, cols: int, name: str) -> None:
+    """Refuses a tensor (None passes) of other rows than [T, cols]; more rows may follow."""
+    if t is not None and isinstance(t, torch.Tensor) and t.numel() != T * cols and (t.dim() < 2 or t.shape[-1] != cols):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{T}, {cols}]")
 
 
 class MoELayer:
@@ -121,7 +121,7 @@ class MoELayer:
             self.w13s = self.w2s = None
         else:
             raise ValueError(precision)
-        self._ws, self._few_ws, self._few_bytes = {}, Workspaces(self.w13.device), {}
+        self._ws, self._few_ws, self._few_shapes = {}, Workspaces(self.w13.device), {}
 
     def shape(self, T: int) -> MoeShape:
         return make_shape(T, self.d, self.E, self.top_k, self.de, self.n_shared,
@@ -158,10 +158,15 @@ class MoELayer:
     def few_workspace(self, T: int, stream=None) -> torch.Tensor:
         """The workspace that forward_few's calls of at most T tokens on `stream`
         take: streams have one each, captures theirs apart from eager calls'."""
-        nbytes = self._few_bytes.get(T)
-        if nbytes is None:
-            nbytes = self._few_bytes[T] = moe_few_workspace_size(self.shape(T))
-        return self._few_ws.get(nbytes, stream)
+        return self._few_ws.get(self._few_sized(T)[1], stream)
+
+    def _few_sized(self, T: int):
+        """The shape of T tokens and its workspace's bytes, worked out once."""
+        sized = self._few_shapes.get(T)
+        if sized is None:
+            s = self.shape(T)
+            sized = self._few_shapes[T] = s, moe_few_workspace_size(s)
+        return sized
 
     def forward_few(self, x: torch.Tensor, out: torch.Tensor | None = None,
                     topk_idx_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -170,13 +175,14 @@ class MoELayer:
         streams or from several threads may overlap; so may a graph's replay and
         eager calls, but not two graphs captured on one stream."""
         T = _tokens(x, self.d, "x")
-        _columns(T, self.d, out=out)
-        _columns(T, self.top_k, topk_idx_out=topk_idx_out)
+        _rows(out, T, self.d, "out")
+        _rows(topk_idx_out, T, self.top_k, "topk_idx_out")
         if out is None:
             out = new_output(T, self.d, torch.bfloat16, x.device, stream)
+        shape, nbytes = self._few_sized(T)
         with self._few_ws.lock:
-            moe_forward_few(self.shape(T), x, self.w_router, self.bias, self.w13, self.w13s, self.w2,
-                            self.w2s, out, self.few_workspace(T, stream), topk_idx_out=topk_idx_out, stream=stream)
+            moe_forward_few(shape, x, self.w_router, self.bias, self.w13, self.w13s, self.w2, self.w2s, out,
+                            self._few_ws.get(nbytes, stream), topk_idx_out=topk_idx_out, stream=stream)
         return out
 
     def forward_few_prenorm(self, h: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6,
@@ -184,15 +190,16 @@ class MoELayer:
                             topk_idx_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """forward_prenorm for at most MOE_FEW_MAX_TOKENS tokens."""
         T = _tokens(h, self.d, "h")
-        _columns(1, self.d, gamma=gamma)
-        _columns(T, self.d, out=out)
-        _columns(T, self.top_k, topk_idx_out=topk_idx_out)
+        _rows(gamma, 1, self.d, "gamma")
+        _rows(out, T, self.d, "out")
+        _rows(topk_idx_out, T, self.top_k, "topk_idx_out")
         if out is None:
             out = new_output(T, self.d, torch.bfloat16, h.device, stream)
+        shape, nbytes = self._few_sized(T)
         with self._few_ws.lock:
-            moe_forward_few_prenorm(self.shape(T), h, gamma, eps, self.w_router, self.bias, self.w13,
-                                    self.w13s, self.w2, self.w2s, out, self.few_workspace(T, stream),
-                                    topk_idx_out=topk_idx_out, stream=stream)
+            moe_forward_few_prenorm(shape, h, gamma, eps, self.w_router, self.bias, self.w13, self.w13s, self.w2,
+                                    self.w2s, out, self._few_ws.get(nbytes, stream), topk_idx_out=topk_idx_out,
+                                    stream=stream)
         return out
 
     def check_status(self, T: int) -> int:
@@ -292,14 +299,21 @@ class Fp8Linear:
             fp8_block_quant(w.contiguous(), 128, self.w, self.w_scales,
                             layout=MOE_LAYOUT_TILED if weight_layout == "tiled" else MOE_LAYOUT_ROWMAJOR,
                             ue8m0=precision == "fp8_ue8m0")
-        self._ws = Workspaces(w.device)
+        self._ws, self._shapes = Workspaces(w.device), {}
 
     def _sized(self, T: int):
-        s = make_linear_shape(T, self.K, self.N, self.precision, self.weight_layout, self.out_dtype)
-        return s, moe_linear_workspace_size(s)
+        """The shape of T tokens and its workspace's bytes, worked out once."""
+        key = T, self.out_dtype
+        sized = self._shapes.get(key)
+        if sized is None:
+            s = self.shape(T)
+            sized = self._shapes[key] = s, moe_linear_workspace_size(s)
+        return sized
 
     def shape(self, T: int) -> MoeLinearShape:
-        return self._sized(T)[0]
+        s = make_linear_shape(T, self.K, self.N, self.precision, self.weight_layout, self.out_dtype)
+        moe_linear_workspace_size(s)
+        return s
 
     def workspace(self, T: int, stream=None) -> torch.Tensor:
         """The workspace that calls of T tokens on `stream` take."""
@@ -309,7 +323,8 @@ class Fp8Linear:
                  residual: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """x W^T, plus the residual before the one rounding of a bf16 output."""
         T = _tokens(x, self.K, "x")
-        _columns(T, self.N, out=out, residual=residual)
+        _rows(out, T, self.N, "out")
+        _rows(residual, T, self.N, "residual")
         if out is None:
             out = new_output(T, self.N, self.out_dtype, self.w.device, stream)
         shape, nbytes = self._sized(T)
@@ -323,8 +338,9 @@ class Fp8Linear:
         """The product of codes that are quantised already (fp8_block_quant,
         block_rows 1): several projections of one x quantise it once."""
         T = _tokens(a, self.K, "a")
-        _columns(T, self.K // 128, a_scales=a_scales)
-        _columns(T, self.N, out=out, residual=residual)
+        _rows(a_scales, T, self.K // 128, "a_scales")
+        _rows(out, T, self.N, "out")
+        _rows(residual, T, self.N, "residual")
         if out is None:
             out = new_output(T, self.N, self.out_dtype, self.w.device, stream)
         shape, nbytes = self._sized(T)
@@ -337,8 +353,8 @@ class Fp8Linear:
                         out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """bf16(RMSNorm(h) * gamma) W^T (pre-norm fused)."""
         T = _tokens(h, self.K, "h")
-        _columns(1, self.K, gamma=gamma)
-        _columns(T, self.N, out=out)
+        _rows(gamma, 1, self.K, "gamma")
+        _rows(out, T, self.N, "out")
         if out is None:
             out = new_output(T, self.N, self.out_dtype, self.w.device, stream)
         shape, nbytes = self._sized(T)

@@ -470,6 +470,10 @@ def new_output(rows, cols, dtype, device, stream=None) -> torch.Tensor:
         return torch.empty(rows, cols, dtype=dtype, device=device)
 
 
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+_capturing = torch.cuda.is_current_stream_capturing
+
+
 class Workspaces:
     """The workspaces of one object's calls.  Calls that can overlap need one
     each, so every stream has its own, which grows to the largest call (what it
@@ -489,30 +493,31 @@ class Workspaces:
         return Workspaces, (self._device,)
 
     def clear(self) -> None:
-        self._streams, self._captured, self._largest = {}, {}, 0  # by raw stream; those: lists
+        self._streams, self._captured = {}, {}  # by raw stream: (bytes, workspace); lists of them
+        self._largest = 0
 
     def get(self, nbytes: int, stream=None) -> torch.Tensor:
-        index = self._device.index
-        if stream is None and torch._C._cuda_getDevice() == index and not torch.cuda.is_current_stream_capturing():
-            ws = self._streams.get(torch._C._cuda_getCurrentRawStream(index))
-            if ws is not None and ws.numel() >= nbytes:
+        if stream is None and _current_device() == self._device.index and not _capturing():
+            size, ws = self._streams.get(_raw_stream(self._device.index), (0, None))
+            if size >= nbytes:
                 return ws
         with self.lock, _on(stream, self._device):
-            raw = torch._C._cuda_getCurrentRawStream(index)
-            if not torch.cuda.is_current_stream_capturing():
-                ws = self._streams.get(raw)
-                if ws is None or ws.numel() < nbytes:
-                    ws = self._streams[raw] = _zeroed(nbytes, self._device)
+            raw = _raw_stream(self._device.index)
+            if not _capturing():
+                size, ws = self._streams.get(raw, (0, None))
+                if size < nbytes:
+                    ws = _zeroed(nbytes, self._device)
+                    self._streams[raw] = nbytes, ws
                     self._largest = max(self._largest, nbytes)
                 return ws
             held = self._captured.setdefault(raw, [])
-            for ws in held:
-                if ws.numel() >= nbytes:
+            for size, ws in held:
+                if size >= nbytes:
                     return ws
-            fit = [(ws.numel(), r) for r, ws in self._streams.items() if ws.numel() >= nbytes]
+            fit = [(size, r) for r, (size, _) in self._streams.items() if size >= nbytes]
             if fit:
                 held.append(self._streams.pop(min(fit)[1]))
-                return held[-1]
+                return held[-1][1]
             if nbytes > self._largest:
                 raise RuntimeError("allocate the workspace (or make one call of this size) before the capture")
             # taken over by other streams' captures: this call's own, out of the
@@ -528,7 +533,7 @@ class Workspaces:
                 return first
             torch.cuda.synchronize(self._device)  # whatever streams they are used on
         with torch.cuda.device(self._device):
-            for ws in every:
+            for _, ws in every:
                 rc = moe_check_status(ws)
                 first = first or rc
         return first
