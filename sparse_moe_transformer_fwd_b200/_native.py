@@ -84,8 +84,8 @@ _FAST = {}  # binding.c's functions
 
 
 def _fast(name):
-    """binding.c's function: it checks the arguments and makes the call in half
-    the host time that Python and ctypes take, or returns None where an argument
+    """binding.c's function: it checks the arguments and makes the call in two thirds
+    of the host time that Python and ctypes take, or returns None where an argument
     is not what the call needs; the path below then makes the call or says what
     is wrong."""
     if not _FAST:
@@ -164,7 +164,7 @@ def lib() -> ctypes.CDLL:
 def _c_binding(L) -> dict:
     """binding.c's functions.  Without the module (built for another Python, or
     not at all) every call takes the path through ctypes: the same checks and the
-    same kernels, in twice the host time."""
+    same kernels, in half as much host time again."""
     try:
         from . import _binding
     except ImportError:

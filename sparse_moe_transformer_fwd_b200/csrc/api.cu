@@ -1194,8 +1194,10 @@ bool linear_quantises(const moe_linear_shape *s) {
 //     and end.  (4096 tokens, 7168 x 4096, 512 tiles: in four rounds 132 us, with
 //     the last one cut in two 126.)
 //   both at least the weights, at 7 and 5.5 TB/s
-// The tiled GEMM needs enough tiles: 128 tokens, 7168 x 2112 (9 tiles) 23.4 us
-// against 10.9 in the stream kernel; 256 tokens, 16384 x 7168 52 against 77.
+// The tiled GEMM needs enough tiles: 32 tokens, 7168 x 2112 (9 tiles) 14.6 us
+// against 10.9 in the stream kernel; 256 tokens, 16384 x 7168 52 against 78.  Over
+// five K x N and eleven batches of 17 to 512 tokens the one taken is the faster
+// or at most 2.1 us slower (192 tokens, 7168 x 7168 30.1 against 28.0).
 // Power-of-two scales take the same promotion as the others: the block-scaled MMA
 // adds all of K in the tensor core, whose sum drops the low bits of small terms
 // (K = 7168, positive terms: up to 8e-6 of their sum, all one way, and 7e-5 at

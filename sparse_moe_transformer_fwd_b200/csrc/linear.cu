@@ -32,9 +32,8 @@
 //               rows; every CTA does it for the K blocks it reads, which costs
 //               less than a launch that writes the codes first
 // Measured (one B200, CUDA graph): 1 token, 7168 x 2112 7.7 us, of which start
-// and end take 4.5; 7 tokens, 7168 x 64007 76 us (6.0 TB/s); 64 tokens with a
-// residual, 16384 x 7168 29.3 us, of which the stream takes 19 and the parts' sums
-// of 64 tokens 5.
+// and end take 4.5; 7 tokens, 7168 x 64007 75 us (6.1 TB/s); 64 tokens, 16384 x
+// 7168 29.6 us (one token 25), 30.7 with a residual.
 // Every wait is bounded; on expiry the block records MOE_ERR_TIMEOUT, drains its
 // loads and MMAs, frees its TMEM and exits; the last CTA out zeroes the item
 // counter.  (A cluster's barrier has no limit of its own: every CTA reaches it,
@@ -1009,8 +1008,8 @@ cudaError_t launch_stream_t(const LinearStreamArgs &g, cudaStream_t st, int *lau
 // a whole one in 0.2 (0.3, 1); storing and adding parts takes 2 us, and 1 in clusters (not of two, which sit on one
 // pair of SMs: 64 tokens, 16384 x 7168 in 112 CTAs 36.7 us so and 32.8 spread
 // out with the second kernel).  Parts of all tiles together (equal shares of the
-// whole stream, two cut tiles a CTA) took 17.4 us for one token at 1536 x 24576
-// and 9.6 at 7168 x 2112, where this takes 10.5 and 6.8.
+// whole stream, two cut tiles a CTA) took 7 us longer for one token at 1536 x
+// 24576 and 3 at 7168 x 2112.
 LinearPlan linear_plan(int T, int tiles, int KB) {
     const int most = std::min(num_sms(), kLinearMaxCtas);
     LinearPlan p;
