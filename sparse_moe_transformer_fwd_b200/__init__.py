@@ -95,7 +95,11 @@ class MoELayer:
     at construction (the bf16 copies are then not needed); "bf16" repacks
     them.  weight_layout "tiled" (default: 128 x 128-byte tiles, one
     contiguous 16 KB read per TMA box) or "rowmajor" (the weights as given,
-    e4m3 codes row-major)."""
+    e4m3 codes row-major).
+
+    __call__ and forward_prenorm keep one workspace for each batch size: calls of
+    one size do not overlap (a layer object, or moe_forward with a workspace, for
+    each stream).  forward_few's calls may."""
 
     def __init__(self, w_router, bias, w13, w2, *, top_k: int, n_shared: int = 1,
                  routed_scale: float = 1.0, precision: str = "fp8", keep_bf16: bool = False,

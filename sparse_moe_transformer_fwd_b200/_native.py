@@ -470,7 +470,9 @@ def new_output(rows, cols, dtype, device, stream=None) -> torch.Tensor:
         return torch.empty(rows, cols, dtype=dtype, device=device)
 
 
-_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# (None in a torch without CUDA, which may still import this)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _capturing = torch.cuda.is_current_stream_capturing
 
 
